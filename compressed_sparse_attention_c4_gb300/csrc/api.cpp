@@ -16,6 +16,7 @@ namespace {
 constexpr int64_t kKvPageBytes = 64 * 448 + 64 * 128 + 64 * 32;   // 38912
 constexpr int64_t kIdxPageBytes = 64 * 128 + 64 * 8;              // 8704
 constexpr int64_t kIdxFp4PageBytes = 64 * 64 + 64 * 4;            // 4352
+constexpr int64_t kKvFp4PageBytes = 64 * 224 + 64 * 128 + 64 * 16;   // 23552
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -30,6 +31,32 @@ bool pool_ok(const dsv4sa_pool_desc* d, int32_t kind) {
          d->nope_off == ref.nope_off && d->rope_off == ref.rope_off && d->scale_off == ref.scale_off &&
          d->nope_row == ref.nope_row && d->rope_row == ref.rope_row && d->scale_row == ref.scale_row;
 }
+
+// Whether two byte ranges share any.
+bool overlap(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+// One to four pools of any kinds with the same pages.
+bool pools_ok(const dsv4sa_pool_desc* pools, int32_t n_pools) {
+  if (!pools || n_pools < 1 || n_pools > DSV4SA_MAX_POOLS) return false;
+  for (int32_t k = 0; k < n_pools; ++k) {
+    if (!pool_ok(pools + k, pools[k].kind) || pools[k].num_pages != pools[0].num_pages) return false;
+    if (pools[k].num_pages > INT32_MAX - 16384) return false;
+    for (int32_t j = 0; j < k; ++j)
+      if (overlap(pools[j].base, dsv4sa_pool_bytes(pools[j].kind, pools[j].num_pages), pools[k].base,
+                  dsv4sa_pool_bytes(pools[k].kind, pools[k].num_pages)))
+        return false;
+  }
+  return true;
+}
+
+bool cache_ok(const dsv4sa_cache_desc* c) {
+  return c && pools_ok(c->pools, c->n_pools) && c->rows >= 1 && c->pt_stride >= 1 && c->page_table &&
+         aligned(c->page_table, 4) && c->use && aligned(c->use, 16);
+}
+
 
 }  // namespace
 
@@ -63,6 +90,7 @@ DSV4SA_API const char* dsv4sa_status_string(int s) {
     case DSV4SA_ERR_CUDA: return "CUDA runtime error";
     case DSV4SA_ERR_INDEX_OOB: return "index or page id out of range (device)";
     case DSV4SA_ERR_DEVICE_TIMEOUT: return "device wait timed out";
+    case DSV4SA_ERR_NO_PAGES: return "no free page left (device)";
     default: return "unknown status";
   }
 }
@@ -72,6 +100,7 @@ DSV4SA_API size_t dsv4sa_pool_bytes(int32_t kind, int64_t num_pages) {
   if (kind == DSV4SA_POOL_KV) return static_cast<size_t>(num_pages) * kKvPageBytes;
   if (kind == DSV4SA_POOL_IDXK) return static_cast<size_t>(num_pages) * kIdxPageBytes;
   if (kind == DSV4SA_POOL_IDXK_FP4) return static_cast<size_t>(num_pages) * kIdxFp4PageBytes;
+  if (kind == DSV4SA_POOL_KV_FP4) return static_cast<size_t>(num_pages) * kKvFp4PageBytes;
   return 0;
 }
 
@@ -117,6 +146,18 @@ DSV4SA_API int dsv4sa_pool_desc_init(dsv4sa_pool_desc* d, int32_t kind, void* ba
     d->nope_row = 64;
     d->rope_row = 0;
     d->scale_row = 4;
+  } else if (kind == DSV4SA_POOL_KV_FP4) {
+    d->nope_dim = DSV4SA_NOPE_DIM;
+    d->rope_dim = DSV4SA_ROPE_DIM;
+    d->scale_group = 32;
+    d->n_scales = DSV4SA_NOPE_DIM / 32;
+    d->page_stride = kKvFp4PageBytes;
+    d->nope_off = 0;
+    d->rope_off = 64 * 224;
+    d->scale_off = 64 * 224 + 64 * 128;
+    d->nope_row = 224;
+    d->rope_row = 128;
+    d->scale_row = 16;
   } else {
     return DSV4SA_ERR_INVALID_ARG;
   }
@@ -231,6 +272,12 @@ DSV4SA_API int dsv4sa_attn_plan(int32_t mode, int32_t T, int32_t H, int32_t kc, 
   return dsv4sa::attn_plan(mode, T, H, kc, kw, nsplit, rows_per_split, launches);
 }
 
+// Whether an attention call reads FP4 pools: both of its pools are.
+static bool attn_fp4(const dsv4sa_attn_args* a) {
+  const dsv4sa_pool_desc* d = a->kc > 0 ? a->comp : (a->kw > 0 ? a->win : nullptr);
+  return d && d->kind == DSV4SA_POOL_KV_FP4;
+}
+
 static int attn_validate(int32_t mode, const dsv4sa_attn_args* a) {
   if (!a) return DSV4SA_ERR_INVALID_ARG;
   if (a->T < 0 || a->kc < 0 || a->kw < 0) return DSV4SA_ERR_INVALID_ARG;
@@ -239,16 +286,21 @@ static int attn_validate(int32_t mode, const dsv4sa_attn_args* a) {
   if (a->T == 0) return DSV4SA_OK;
   if (!a->q || !a->attn_sink || !a->q_seq || !a->out) return DSV4SA_ERR_INVALID_ARG;
   if (!aligned(a->q, 16) || !aligned(a->out, 16)) return DSV4SA_ERR_INVALID_ARG;
+  const bool fp4 = attn_fp4(a);
+  const int32_t kind = fp4 ? DSV4SA_POOL_KV_FP4 : DSV4SA_POOL_KV;
+  if (a->kc > 0 && a->kw > 0 && a->comp && a->win && a->comp->kind != a->win->kind &&
+      (a->comp->kind == DSV4SA_POOL_KV || fp4) && (a->win->kind == DSV4SA_POOL_KV || a->win->kind == DSV4SA_POOL_KV_FP4))
+    return DSV4SA_ERR_UNSUPPORTED;   // one FP8 and one FP4 pool
   if (a->kc > 0) {
-    if (!pool_ok(a->comp, DSV4SA_POOL_KV) || !a->comp_pt || !a->idx_c) return DSV4SA_ERR_INVALID_ARG;
+    if (!pool_ok(a->comp, kind) || !a->comp_pt || !a->idx_c) return DSV4SA_ERR_INVALID_ARG;
     if (a->idx_c_stride < a->kc || a->comp_pt_stride < 1) return DSV4SA_ERR_INVALID_ARG;
   }
   if (a->kw > 0) {
-    if (!pool_ok(a->win, DSV4SA_POOL_KV) || !a->win_pt || (!a->idx_w && !a->win_pos)) return DSV4SA_ERR_INVALID_ARG;
+    if (!pool_ok(a->win, kind) || !a->win_pt || (!a->idx_w && !a->win_pos)) return DSV4SA_ERR_INVALID_ARG;
     if ((a->idx_w && a->idx_w_stride < a->kw) || a->win_pt_stride < 1 || a->win_ring < 0) return DSV4SA_ERR_INVALID_ARG;
   }
   if (a->rope_cs && (!a->rope_pos || a->rope_rows < 1 || !aligned(a->rope_cs, 16))) return DSV4SA_ERR_INVALID_ARG;
-  const size_t need = dsv4sa_attn_workspace_size(mode, a->T, a->H, a->kc, a->kw);
+  const size_t need = fp4 ? 0 : dsv4sa_attn_workspace_size(mode, a->T, a->H, a->kc, a->kw);
   if (need > 0 && (!a->ws || a->ws_bytes < need || !aligned(a->ws, 16))) return DSV4SA_ERR_WORKSPACE;
   return DSV4SA_OK;
 }
@@ -289,7 +341,8 @@ DSV4SA_API int dsv4sa_cache_write(const dsv4sa_pool_desc* pool, const int32_t* p
                                   const int32_t* row_seq, const int32_t* row_entry, const void* rows, int32_t n,
                                   cudaStream_t stream) {
   if (n < 0 || pt_stride < 1) return DSV4SA_ERR_INVALID_ARG;
-  if (!pool_ok(pool, DSV4SA_POOL_KV) && !pool_ok(pool, DSV4SA_POOL_IDXK) && !pool_ok(pool, DSV4SA_POOL_IDXK_FP4))
+  if (!pool_ok(pool, DSV4SA_POOL_KV) && !pool_ok(pool, DSV4SA_POOL_IDXK) && !pool_ok(pool, DSV4SA_POOL_IDXK_FP4) &&
+      !pool_ok(pool, DSV4SA_POOL_KV_FP4))
     return DSV4SA_ERR_INVALID_ARG;
   if (n == 0) return DSV4SA_OK;
   if (!page_table || !row_seq || !row_entry || !rows || !aligned(rows, 16)) return DSV4SA_ERR_INVALID_ARG;
@@ -303,6 +356,86 @@ DSV4SA_API int dsv4sa_cache_write_rotated(const dsv4sa_pool_desc* pool, const in
   if (n == 0) return DSV4SA_OK;
   if (!page_table || !row_seq || !row_entry || !rows || !aligned(rows, 16)) return DSV4SA_ERR_INVALID_ARG;
   return dsv4sa::launch_cache_write(pool, page_table, pt_stride, row_seq, row_entry, rows, n, true, stream);
+}
+
+DSV4SA_API int dsv4sa_cache_read(const dsv4sa_pool_desc* pool, const int32_t* page_table, int32_t pt_stride,
+                                 const int32_t* row_seq, const int32_t* row_entry, void* rows, int32_t n,
+                                 cudaStream_t stream) {
+  if (n < 0 || pt_stride < 1) return DSV4SA_ERR_INVALID_ARG;
+  if (!pool_ok(pool, DSV4SA_POOL_KV) && !pool_ok(pool, DSV4SA_POOL_KV_FP4)) return DSV4SA_ERR_INVALID_ARG;
+  if (n == 0) return DSV4SA_OK;
+  if (!page_table || !row_seq || !row_entry || !rows || !aligned(rows, 16)) return DSV4SA_ERR_INVALID_ARG;
+  if (overlap(rows, static_cast<uint64_t>(n) * 1024, pool->base, dsv4sa_pool_bytes(pool->kind, pool->num_pages)))
+    return DSV4SA_ERR_INVALID_ARG;
+  return dsv4sa::launch_cache_read(pool, page_table, pt_stride, row_seq, row_entry, rows, n, stream);
+}
+
+DSV4SA_API int dsv4sa_pages_copy(const dsv4sa_pool_desc* pools, int32_t n_pools, const int32_t* src_page,
+                                 const int32_t* dst_page, int32_t n, cudaStream_t stream) {
+  if (n < 0 || !pools_ok(pools, n_pools)) return DSV4SA_ERR_INVALID_ARG;
+  if (n > (1 << 28)) return DSV4SA_ERR_UNSUPPORTED;
+  if (n == 0) return DSV4SA_OK;
+  if (!src_page || !dst_page) return DSV4SA_ERR_INVALID_ARG;
+  return dsv4sa::launch_pages_copy(pools, n_pools, src_page, dst_page, n, stream);
+}
+
+DSV4SA_API int dsv4sa_cache_release(const dsv4sa_cache_desc* cache, const int32_t* row, int32_t n,
+                                    cudaStream_t stream) {
+  if (n < 0 || !cache_ok(cache)) return DSV4SA_ERR_INVALID_ARG;
+  if (n == 0) return DSV4SA_OK;
+  if (!row) return DSV4SA_ERR_INVALID_ARG;
+  return dsv4sa::launch_cache_release(cache, row, n, stream);
+}
+
+DSV4SA_API int dsv4sa_cache_fork(const dsv4sa_cache_desc* cache, const int32_t* src_row, const int32_t* dst_row,
+                                 const int32_t* length, int32_t n, int32_t* new_page, cudaStream_t stream) {
+  if (n < 0 || !cache_ok(cache)) return DSV4SA_ERR_INVALID_ARG;
+  if (n > (1 << 28)) return DSV4SA_ERR_UNSUPPORTED;
+  if (n == 0) return DSV4SA_OK;
+  if (!src_row || !dst_row || !length || !new_page) return DSV4SA_ERR_INVALID_ARG;
+  return dsv4sa::launch_cache_fork(cache, src_row, dst_row, length, n, new_page, stream);
+}
+
+DSV4SA_API int dsv4sa_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* dst, int32_t* new_id,
+                                    int32_t* n_used, cudaStream_t stream) {
+  if (!cache_ok(src) || !cache_ok(dst) || !new_id || !n_used) return DSV4SA_ERR_INVALID_ARG;
+  if (src->n_pools != dst->n_pools || src->rows != dst->rows || src->pt_stride != dst->pt_stride)
+    return DSV4SA_ERR_INVALID_ARG;
+  const uint64_t entries = static_cast<uint64_t>(src->rows) * src->pt_stride * 4;
+  bool same = src->page_table == dst->page_table && src->use == dst->use;
+  for (int32_t k = 0; k < src->n_pools; ++k) {
+    if (src->pools[k].kind != dst->pools[k].kind) return DSV4SA_ERR_INVALID_ARG;
+    same = same && src->pools[k].base == dst->pools[k].base && src->pools[k].num_pages == dst->pools[k].num_pages;
+  }
+  if (!same) {   // in place altogether, or apart altogether
+    if (overlap(src->page_table, entries, dst->page_table, entries) ||
+        overlap(src->use, static_cast<uint64_t>(src->pools[0].num_pages) * 4, dst->use,
+                static_cast<uint64_t>(dst->pools[0].num_pages) * 4))
+      return DSV4SA_ERR_INVALID_ARG;
+    for (int32_t k = 0; k < src->n_pools; ++k)
+      for (int32_t j = 0; j < dst->n_pools; ++j)
+        if (overlap(src->pools[k].base, dsv4sa_pool_bytes(src->pools[k].kind, src->pools[k].num_pages),
+                    dst->pools[j].base, dsv4sa_pool_bytes(dst->pools[j].kind, dst->pools[j].num_pages)))
+          return DSV4SA_ERR_INVALID_ARG;
+  }
+  return dsv4sa::launch_cache_compact(src, dst, new_id, n_used, stream);
+}
+
+DSV4SA_API int dsv4sa_rmsnorm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                    const float* norm_w, float eps, int32_t n, int32_t dim, int32_t group,
+                                    void* residual_out, void* y, uint8_t* codes, float* scale, cudaStream_t stream) {
+  if (n < 0 || dim < 8 || dim % 8 != 0 || !(eps >= 0.f)) return DSV4SA_ERR_INVALID_ARG;
+  if (dim > DSV4SA_MAX_NORM_DIM || (group != 64 && group != 128)) return DSV4SA_ERR_UNSUPPORTED;
+  if (x_stride < dim || x_stride % 8 != 0) return DSV4SA_ERR_INVALID_ARG;
+  if (residual && (residual_stride < dim || residual_stride % 8 != 0)) return DSV4SA_ERR_INVALID_ARG;
+  if (!codes != !scale || (codes && dim % group != 0)) return DSV4SA_ERR_INVALID_ARG;
+  if (!residual_out && !y && !codes) return DSV4SA_ERR_INVALID_ARG;
+  if (n == 0) return DSV4SA_OK;
+  if (!x || !norm_w || !aligned(x, 16) || !aligned(residual, 16) || !aligned(norm_w, 16) || !aligned(residual_out, 16) ||
+      !aligned(y, 16) || !aligned(codes, 16) || !aligned(scale, 4))
+    return DSV4SA_ERR_INVALID_ARG;
+  return dsv4sa::launch_rmsnorm_quant(x, x_stride, residual, residual_stride, norm_w, eps, n, dim, group, residual_out,
+                                      y, codes, scale, stream);
 }
 
 DSV4SA_API int dsv4sa_compress_windows(const void* kv, const void* score, int64_t tok_stride, int64_t n_tok,
@@ -365,11 +498,13 @@ DSV4SA_API int dsv4sa_check_errors(cudaStream_t stream, uint32_t* bits_out) {
   const uint32_t bits = dsv4sa::read_error_word_indexer(stream, true) | dsv4sa::read_error_word_topk(stream, true) |
                         dsv4sa::read_error_word_attn(stream, true) | dsv4sa::read_error_word_attn_decode(stream, true) |
                         dsv4sa::read_error_word_writer(stream, true) |
-                        dsv4sa::read_error_word_compress(stream, true);
+                        dsv4sa::read_error_word_compress(stream, true) | dsv4sa::read_error_word_pages(stream, true) |
+                        dsv4sa::read_error_word_attn_fp4(stream, true);
   if (cudaGetLastError() != cudaSuccess) return DSV4SA_ERR_CUDA;
   if (bits_out) *bits_out = bits;
   if (bits & 2u) return DSV4SA_ERR_DEVICE_TIMEOUT;
   if (bits & 1u) return DSV4SA_ERR_INDEX_OOB;
+  if (bits & 4u) return DSV4SA_ERR_NO_PAGES;
   return DSV4SA_OK;
 }
 

@@ -825,11 +825,18 @@ static int fill_params(int32_t mode, const dsv4sa_attn_args* a, AttnParams& p, i
   return DSV4SA_OK;
 }
 
+// A call over FP4 pools (both are, the front end has checked).
+static bool fp4_pools(const dsv4sa_attn_args* a) {
+  const dsv4sa_pool_desc* d = a->kc > 0 ? a->comp : (a->kw > 0 ? a->win : nullptr);
+  return d && d->kind == DSV4SA_POOL_KV_FP4;
+}
+
 int launch_sparse_attn(int32_t mode, const dsv4sa_attn_args* a, cudaStream_t stream) {
   AttnParams p{};
   int hn = 0, groups = 0;
   const int rc = fill_params(mode, a, p, hn, groups);
   if (rc != DSV4SA_OK || a->T == 0) return rc;
+  if (fp4_pools(a)) return attn::launch_fp4(mode, p, stream);
   if (mode == DSV4SA_ATTN_DECODE && p.merge == kMergeCluster) return attn::launch_decode_cluster(p, hn, groups, stream);
   switch (hn) {
     case 16: return launch_hn<16>(p, groups, stream);
@@ -849,7 +856,8 @@ int launch_topk_sparse_attn(const dsv4sa_attn_args* a, const float* logits, int6
   int hn = 0, groups = 0;
   const int rc = fill_params(DSV4SA_ATTN_DECODE, a, p, hn, groups);
   if (rc != DSV4SA_OK || a->T == 0) return rc;
-  const bool fuse = p.merge == kMergeCluster && k <= a->kc && n_max <= attn::kFusedMaxRow &&
+  const bool fp4 = fp4_pools(a);
+  const bool fuse = !fp4 && p.merge == kMergeCluster && k <= a->kc && n_max <= attn::kFusedMaxRow &&
                     p.kc_split <= attn::kFusedMaxSplitRows && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
                     logits_stride % 4 == 0;
   if (fuse) {
@@ -864,7 +872,7 @@ int launch_topk_sparse_attn(const dsv4sa_attn_args* a, const float* logits, int6
   }
   const TopkPrefetch pf{a->comp, a->comp_pt, a->comp_pt_stride, a->q_seq};
   const int rt = launch_topk(logits, logits_stride, n_vis, a->T, n_max, k, const_cast<int32_t*>(a->idx_c),
-                             a->idx_c_stride, topk_ws, topk_ws_bytes, stream, a->kc > 0 ? &pf : nullptr);
+                             a->idx_c_stride, topk_ws, topk_ws_bytes, stream, a->kc > 0 && !fp4 ? &pf : nullptr);
   if (rt != DSV4SA_OK) return rt;
   return launch_sparse_attn(DSV4SA_ATTN_DECODE, a, stream);
 }

@@ -172,6 +172,8 @@ __device__ __forceinline__ void dequant16(const uint4 codes, float scale, uint4&
 int launch_decode_cluster(const AttnParams& p, int hn, int groups, cudaStream_t stream);
 // The largest cluster that kernel supports for hn heads per CTA (its merge slots fit in shared memory).
 int decode_max_cluster(int hn);
+// Either mode over FP4 pools (attn_fp4.cu); sets p.nsplit.
+int launch_fp4(int32_t mode, AttnParams& p, cudaStream_t stream);
 // The longest row the decode kernel selects from itself (fused top-k), and the
 // most compressed rows a CTA may take in that mode.
 constexpr int kFusedMaxRow = 16384;

@@ -20,9 +20,10 @@
 namespace dsv4sa {
 
 // ---------------------------------------------------------------- error word
-// Bit 0: an index or a page id was out of range.  Bit 1: a wait timed out.
+// Bit 0: an index or a page id was out of range.  Bit 1: a wait timed out.  Bit 2: no free page was left.
 constexpr uint32_t kErrIndex = 1u;
 constexpr uint32_t kErrTimeout = 2u;
+constexpr uint32_t kErrPages = 4u;    // no free page was left
 
 // One error word per translation unit (internal linkage); each .cu file
 // exposes a host reader for its own copy (see dsv4sa_internal.h).

@@ -60,6 +60,8 @@ uint32_t read_error_word_attn(cudaStream_t stream, bool clear);
 uint32_t read_error_word_attn_decode(cudaStream_t stream, bool clear);
 uint32_t read_error_word_writer(cudaStream_t stream, bool clear);
 uint32_t read_error_word_compress(cudaStream_t stream, bool clear);
+uint32_t read_error_word_attn_fp4(cudaStream_t stream, bool clear);
+uint32_t read_error_word_pages(cudaStream_t stream, bool clear);
 int launch_selftest_wait_timeout(int32_t* result, cudaStream_t stream);
 int launch_compress_windows(const void* kv, const void* score, int64_t tok_stride, int64_t n_tok,
                             const int32_t* first_tok,
@@ -73,5 +75,19 @@ int launch_compress_online(const void* kv, const void* score, int64_t tok_stride
 int launch_cache_write(const dsv4sa_pool_desc* pool, const int32_t* page_table, int32_t pt_stride,
                        const int32_t* row_seq, const int32_t* row_entry, const void* rows, int32_t n,
                        bool rotate, cudaStream_t stream);
+int launch_cache_read(const dsv4sa_pool_desc* pool, const int32_t* page_table, int32_t pt_stride,
+                      const int32_t* row_seq, const int32_t* row_entry, void* rows, int32_t n, cudaStream_t stream);
+
+int launch_pages_copy(const dsv4sa_pool_desc* pools, int32_t n_pools, const int32_t* src, const int32_t* dst, int32_t n,
+                      cudaStream_t stream);
+int launch_cache_release(const dsv4sa_cache_desc* c, const int32_t* rows, int32_t n, cudaStream_t stream);
+int launch_cache_fork(const dsv4sa_cache_desc* c, const int32_t* src, const int32_t* dst, const int32_t* len, int32_t n,
+                      int32_t* new_page, cudaStream_t stream);
+int launch_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* dst, int32_t* new_id, int32_t* n_used,
+                         cudaStream_t stream);
+
+int launch_rmsnorm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                         const float* norm_w, float eps, int32_t n, int32_t dim, int32_t group, void* residual_out,
+                         void* y, uint8_t* codes, float* scale, cudaStream_t stream);
 
 }  // namespace dsv4sa

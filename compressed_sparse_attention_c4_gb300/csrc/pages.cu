@@ -1,0 +1,530 @@
+// pages.cu -- the pages of a cache: copied, shared by forks, released, compacted.
+//
+// A cache is up to four pools that share page ids ("DeepSeek-V4 in SGLang" 概念5
+// DeepSeekV4TokenToKVPool: a paged pool; a sequence's KV rows and its indexer
+// keys lie in the same page of two pools), one page table and one use count per
+// page: how many table entries hold it, 0 for a free page.  All of it lives on
+// the device, so a beam step or a clean-up costs the host no round trip.
+//
+// Everything here moves bytes: the bound is HBM for whole pages and latency for
+// a few table rows.  Counts are 32-bit integers changed by atomic additions,
+// whose order does not change the result; page ids are handed out by scans in
+// id order, so a call gives the same ids every time.
+#include "common.cuh"
+#include "dsv4sa_internal.h"
+
+namespace dsv4sa {
+namespace {
+
+constexpr int kPage = DSV4SA_PAGE_SIZE;
+constexpr int kMaxPools = DSV4SA_MAX_POOLS;
+constexpr int kCopyThreads = 256;
+
+struct PoolBytes {
+  uint8_t* base;
+  int64_t stride;        // bytes of a page (a multiple of 256)
+  int32_t off[3];        // the page's blocks: byte offset, bytes per slot
+  int32_t row[3];
+};
+
+struct CacheParams {
+  PoolBytes pool[kMaxPools];
+  int32_t n_pools;
+  int32_t rows;
+  int32_t pt_stride;
+  int32_t num_pages;
+  int32_t* pt;
+  int32_t* use;
+};
+
+// Copy `units` 16-byte units, eight loads in flight per thread.
+__device__ __forceinline__ void copy_units(uint4* dst, const uint4* src, int units, int tid, int threads) {
+  int u = tid;
+  for (; u + 7 * threads < units; u += 8 * threads) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __ldcs(src + u + i * threads);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) __stcs(dst + u + i * threads, v[i]);
+  }
+  for (; u < units; u += threads) __stcs(dst + u, __ldcs(src + u));
+}
+
+// Exclusive scan over the 1024 threads of a CTA; returns the total.
+__device__ __forceinline__ int scan1024(int v, int* buf, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) buf[warp] = x;
+  __syncthreads();
+  const int w = buf[lane];
+  int wx = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, wx, o);
+    if (lane >= o) wx += y;
+  }
+  total = __shfl_sync(0xffffffffu, wx, 31);
+  const int before = __shfl_sync(0xffffffffu, wx - w, warp);
+  __syncthreads();
+  return before + x - v;
+}
+
+// ---------------------------------------------------------------- copy
+// Page dst[i] = page src[i] of every pool.  grid (n, pieces): a piece is a
+// contiguous share of each page.
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CacheParams p, const int32_t* src,
+                                                                  const int32_t* dst, int pieces) {
+  griddep_launch();
+  griddep_wait();
+  const int i = blockIdx.x / pieces, piece = blockIdx.x % pieces;
+  const int32_t a = __ldg(src + i), b = __ldg(dst + i);
+  if (a == -1 || b == -1) return;
+  if (a < 0 || b < 0 || a >= p.num_pages || b >= p.num_pages) {
+    if (threadIdx.x == 0 && piece == 0) raise_error(kErrIndex);
+    return;
+  }
+  if (a == b) return;
+  for (int k = 0; k < p.n_pools; ++k) {
+    const int units = static_cast<int>(p.pool[k].stride / 16);
+    const int u0 = units * piece / pieces, u1 = units * (piece + 1) / pieces;
+    copy_units(reinterpret_cast<uint4*>(p.pool[k].base + b * p.pool[k].stride) + u0,
+               reinterpret_cast<const uint4*>(p.pool[k].base + a * p.pool[k].stride) + u0, u1 - u0, threadIdx.x,
+               kCopyThreads);
+  }
+}
+
+// ---------------------------------------------------------------- release
+__global__ void __launch_bounds__(kCopyThreads) cache_release_kernel(const CacheParams p, const int32_t* rows, int n) {
+  griddep_launch();
+  griddep_wait();
+  const int64_t total = static_cast<int64_t>(n) * p.pt_stride;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; e < total;
+       e += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
+    const int64_t i = e / p.pt_stride, j = e - i * p.pt_stride;
+    const int32_t row = __ldg(rows + i);
+    if (row < 0 || row >= p.rows) {
+      if (j == 0 && row != -1) raise_error(kErrIndex);
+      continue;
+    }
+    int32_t* at = p.pt + static_cast<int64_t>(row) * p.pt_stride + j;
+    if (*at == -1) continue;
+    const int32_t page = atomicExch(at, -1);   // a row named twice is released once
+    if (page < 0 || page >= p.num_pages) {
+      if (page != -1) raise_error(kErrIndex);
+      continue;
+    }
+    if (atomicSub(p.use + page, 1) <= 0) {     // the page was free: keep its count
+      atomicAdd(p.use + page, 1);
+      raise_error(kErrIndex);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- fork
+struct ForkParams {
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* len;
+  int32_t* new_page;      // >= 0 the copied page, -1 none needed, kRefused, kUntouched
+  int32_t n;
+};
+
+constexpr int kRefused = -2;     // no page for it: its row stays empty
+constexpr int kUntouched = -3;   // its arguments are refused: its row stays as it is
+constexpr int kAllocThreads = 1024;
+constexpr int kAllocChunk = 8 * kAllocThreads;
+
+// Hands out pages: fork i whose length ends inside a page gets the lowest free
+// page not given to an earlier fork.  One CTA walks the use counts in id order,
+// 8192 at a time, and stops as soon as every fork is served.  A fork first
+// claims its row: the row must be empty (first entry negative), and of two forks
+// into one row the first one has it -- the claim is the fork's number, offset to
+// be the smaller the earlier, put into the row's first entry by an atomic
+// minimum.  A parent that is a row of this same call is thereby empty, too, and
+// refused.
+__global__ void __launch_bounds__(kAllocThreads) cache_fork_alloc_kernel(const CacheParams p, const ForkParams f) {
+  __shared__ int buf[32];
+  __shared__ int32_t free_ids[kAllocChunk];
+  griddep_launch();
+  griddep_wait();
+  const int tid = static_cast<int>(threadIdx.x);
+  int avail = 0, pos = 0, next = 0;            // ids listed, ids given out, next page to look at
+  for (int i0 = 0; i0 < f.n; i0 += kAllocThreads) {
+    const int i = i0 + tid;
+    int state = -1;                            // -1 nothing to copy, 1 a page wanted, or a refusal
+    int32_t* claim = nullptr;
+    if (i < f.n) {
+      const int32_t s = __ldg(f.src + i), d = __ldg(f.dst + i), len = __ldg(f.len + i);
+      bool ok = s >= 0 && s < p.rows && d >= 0 && d < p.rows && s != d && len >= 0 &&
+                len <= static_cast<int64_t>(p.pt_stride) * kPage;
+      if (ok && len > 0) {
+        const int32_t* srow = p.pt + static_cast<int64_t>(s) * p.pt_stride;
+        const int32_t last = __ldcg(srow + (len - 1) / kPage);
+        ok = __ldcg(srow) >= 0 && last >= 0 && last < p.num_pages;
+      }
+      if (ok) {
+        claim = p.pt + static_cast<int64_t>(d) * p.pt_stride;
+        if (__ldcg(claim) < 0) atomicMin(claim, INT32_MIN + i);
+        else ok = false;
+      }
+      state = !ok ? kUntouched : (len % kPage != 0 ? 1 : -1);
+    }
+    __syncthreads();                           // every claim of this batch is made
+    if (state != kUntouched && claim != nullptr && __ldcg(claim) != INT32_MIN + i) state = kUntouched;
+    if (state == kUntouched) raise_error(kErrIndex);
+    int wanted;
+    const int rank = scan1024(state == 1 ? 1 : 0, buf, wanted);
+    int given = 0;
+    int32_t mine = state == 1 ? kRefused : state;    // until a page is found for it
+    while (given < wanted) {                   // uniform: every bound here is the CTA's
+      if (pos == avail) {
+        if (next >= p.num_pages) {
+          if (tid == 0) raise_error(kErrPages);
+          break;
+        }
+        const int q0 = next + tid * 8;
+        int bits = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          int4 c = make_int4(1, 1, 1, 1);
+          const int q = q0 + 4 * h;
+          if (q + 3 < p.num_pages) {
+            c = *reinterpret_cast<const int4*>(p.use + q);
+          } else {
+            if (q < p.num_pages) c.x = p.use[q];
+            if (q + 1 < p.num_pages) c.y = p.use[q + 1];
+            if (q + 2 < p.num_pages) c.z = p.use[q + 2];
+          }
+          bits |= ((c.x == 0) | ((c.y == 0) << 1) | ((c.z == 0) << 2) | ((c.w == 0) << 3)) << (4 * h);
+        }
+        int at = scan1024(__popc(bits), buf, avail);
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          if (bits >> h & 1) free_ids[at++] = q0 + h;
+        pos = 0;
+        next += kAllocChunk;
+        __syncthreads();
+        continue;
+      }
+      const int take = min(wanted - given, avail - pos);
+      if (state == 1 && rank >= given && rank < given + take) mine = free_ids[pos + rank - given];
+      given += take;
+      pos += take;
+      __syncthreads();                         // the list is read before it is filled again
+    }
+    if (i < f.n) {
+      f.new_page[i] = mine;
+      if (mine >= 0) p.use[mine] = 1;          // never looked at again in this call: ids only go up
+    }
+    __syncthreads();
+  }
+}
+
+// Fork i by `pieces` CTAs: the row of dst is the parent's full pages (their
+// counts go up) and the new page, whose first len % 64 slots are copied.
+__global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(const CacheParams p, const ForkParams f, int pieces) {
+  griddep_launch();
+  griddep_wait();
+  const int i = blockIdx.x / pieces, piece = blockIdx.x % pieces, tid = static_cast<int>(threadIdx.x);
+  const int32_t d = __ldg(f.dst + i), s = __ldg(f.src + i), len = __ldg(f.len + i), page = f.new_page[i];
+  if (page == kUntouched) return;              // flagged by the first kernel
+  int32_t* drow = p.pt + static_cast<int64_t>(d) * p.pt_stride;
+  if (page == kRefused) {                      // only the claim was written
+    if (piece == 0 && tid == 0) drow[0] = -1;
+    return;
+  }
+  const int32_t* srow = p.pt + static_cast<int64_t>(s) * p.pt_stride;
+  const int full = len / kPage, slots = len % kPage;
+  if (page >= 0) {
+    const int64_t from = srow[full];
+    for (int k = 0; k < p.n_pools; ++k) {
+      const PoolBytes& pb = p.pool[k];
+      uint8_t* to = pb.base + page * pb.stride;
+      const uint8_t* fr = pb.base + from * pb.stride;
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        if (pb.row[b] == 0) continue;
+        const int bytes = slots * pb.row[b];   // row sizes are multiples of 4, block offsets of 16
+        const int units = bytes / 16, u0 = units * piece / pieces, u1 = units * (piece + 1) / pieces;
+        copy_units(reinterpret_cast<uint4*>(to + pb.off[b]) + u0, reinterpret_cast<const uint4*>(fr + pb.off[b]) + u0,
+                   u1 - u0, tid, kCopyThreads);
+        const int w = (bytes - units * 16) / 4;
+        if (piece == pieces - 1 && tid < w)
+          reinterpret_cast<uint32_t*>(to + pb.off[b] + units * 16)[tid] =
+              reinterpret_cast<const uint32_t*>(fr + pb.off[b] + units * 16)[tid];
+      }
+    }
+  }
+  for (int j = piece * kCopyThreads + tid; j < p.pt_stride; j += pieces * kCopyThreads) {
+    int32_t e = -1;
+    if (j < full) {
+      e = srow[j];
+      if (e < 0 || e >= p.num_pages) {
+        raise_error(kErrIndex);
+        e = -1;
+      } else {
+        atomicAdd(p.use + e, 1);
+      }
+    } else if (j == full && slots > 0) {
+      e = page;
+    }
+    drow[j] = e;
+  }
+}
+
+// ---------------------------------------------------------------- compact
+struct CompactParams {
+  CacheParams src;
+  CacheParams dst;
+  int32_t* new_id;        // [src.num_pages]
+  int32_t* n_used;
+  int32_t in_place;
+};
+
+// Eight use counts of the thread, from page q0 on: a bit for each page in use.
+__device__ __forceinline__ uint32_t used_bits(const CacheParams& p, int q0) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int q = q0 + 4 * h;
+    int4 c = make_int4(0, 0, 0, 0);
+    if (q + 3 < p.num_pages) {
+      c = *reinterpret_cast<const int4*>(p.use + q);
+    } else {
+      if (q < p.num_pages) c.x = p.use[q];
+      if (q + 1 < p.num_pages) c.y = p.use[q + 1];
+      if (q + 2 < p.num_pages) c.z = p.use[q + 2];
+    }
+    bits |= static_cast<uint32_t>((c.x > 0) | ((c.y > 0) << 1) | ((c.z > 0) << 2) | ((c.w > 0) << 3)) << (4 * h);
+  }
+  return bits;
+}
+
+// new_id of every page, by one CTA in id order.  To other pools: the rank among
+// the pages in use (-1 for a free page, or one that no longer fits).  In place:
+// pages below the number in use stay, the k-th one at or above it goes to the
+// k-th free page below it.  The free pages' list of that case is kept in
+// new_id[n_used ..] until its entries are replaced: the k-th page to move has an
+// id of at least n_used + k, so the chunks are walked from the highest ids down
+// and an entry is read before anything at or above its place is written.
+__global__ void __launch_bounds__(kAllocThreads) cache_plan_kernel(const CompactParams c) {
+  __shared__ int buf[32];
+  griddep_launch();
+  griddep_wait();
+  const int tid = static_cast<int>(threadIdx.x);
+  const int P = c.src.num_pages;
+  int total = 0;
+  if (c.in_place) {
+    int mine = 0;
+    for (int q0 = tid * 8; q0 < P; q0 += kAllocChunk) mine += __popc(used_bits(c.src, q0));
+    scan1024(mine, buf, total);
+  }
+  const int limit = c.in_place ? total : P;
+  int base = 0, holes = 0;
+  for (int c0 = 0; c0 < limit; c0 += kAllocChunk) {
+    const int q0 = c0 + tid * 8;
+    uint32_t bits = used_bits(c.src, q0);
+    if (c.in_place) {
+      const int in = max(0, min(8, limit - q0));
+      const uint32_t mask = (1u << in) - 1u;
+      int t;
+      int h = holes + scan1024(__popc(~bits & mask), buf, t);
+      holes += t;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (!(mask >> k & 1u)) continue;
+        if (bits >> k & 1u) c.new_id[q0 + k] = q0 + k;
+        else {
+          c.new_id[q0 + k] = -1;
+          c.new_id[total + h++] = q0 + k;      // holes <= pages at or above n_used: in range
+        }
+      }
+    } else {
+      int t;
+      int r = base + scan1024(__popc(bits), buf, t);
+      base += t;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (q0 + k >= P) continue;
+        int id = -1;
+        if (bits >> k & 1u) {
+          id = r < c.dst.num_pages ? r : -1;
+          ++r;
+        }
+        c.new_id[q0 + k] = id;
+      }
+    }
+  }
+  if (c.in_place) {
+    __syncthreads();
+    int left = holes;                          // pages at or above n_used not yet given their place
+    const int n_above = P - total;
+    for (int c0 = n_above > 0 ? (n_above - 1) / kAllocChunk * kAllocChunk : -1; c0 >= 0; c0 -= kAllocChunk) {
+      const int q0 = total + c0 + tid * 8;     // not a multiple of four: single loads
+      uint32_t bits = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) bits |= (q0 + k < P && c.src.use[q0 + k] > 0 ? 1u : 0u) << k;
+      int t;
+      const int before = scan1024(__popc(bits), buf, t);
+      int r = left - t + before;               // rank of the thread's first page to move
+      int32_t id[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) id[k] = bits >> k & 1u ? c.new_id[total + r++] : -1;
+      __syncthreads();                         // this chunk's list entries are read before they are replaced
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (q0 + k < P) c.new_id[q0 + k] = id[k];
+      left -= t;
+    }
+  } else {
+    total = base;
+    if (tid == 0 && total > c.dst.num_pages) raise_error(kErrPages);
+  }
+  if (tid == 0) *c.n_used = total;
+}
+
+// Moves the pages to their new ids and rewrites the table and the counts.
+__global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(const CompactParams c) {
+  griddep_launch();
+  griddep_wait();
+  const int tid = static_cast<int>(threadIdx.x);
+  const int64_t thread = static_cast<int64_t>(blockIdx.x) * kCopyThreads + tid;
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * kCopyThreads;
+  const int64_t entries = static_cast<int64_t>(c.src.rows) * c.src.pt_stride;
+  for (int64_t e = thread; e < entries; e += threads) {
+    const int32_t t = c.src.pt[e];
+    int32_t id = -1;
+    if (t >= 0 && t < c.src.num_pages) id = __ldg(c.new_id + t);
+    else if (t != -1) raise_error(kErrIndex);
+    c.dst.pt[e] = id;
+  }
+  if (!c.in_place) {
+    const int used = *c.n_used;
+    for (int64_t q = thread; q < c.dst.num_pages; q += threads)
+      if (q >= used) c.dst.use[q] = 0;
+  }
+  for (int q = blockIdx.x; q < c.src.num_pages; q += gridDim.x) {
+    const int32_t id = __ldg(c.new_id + q);
+    if (id < 0 || (c.in_place && id == q)) continue;
+    for (int k = 0; k < c.src.n_pools; ++k)
+      copy_units(reinterpret_cast<uint4*>(c.dst.pool[k].base + id * c.dst.pool[k].stride),
+                 reinterpret_cast<const uint4*>(c.src.pool[k].base + q * c.src.pool[k].stride),
+                 static_cast<int>(c.src.pool[k].stride / 16), tid, kCopyThreads);
+    if (tid == 0) {
+      c.dst.use[id] = c.src.use[q];
+      if (c.in_place) c.src.use[q] = 0;
+    }
+  }
+}
+
+void fill_pools(const dsv4sa_pool_desc* pools, int32_t n_pools, CacheParams& p) {
+  p.n_pools = n_pools;
+  p.num_pages = static_cast<int32_t>(pools[0].num_pages);
+  for (int k = 0; k < n_pools; ++k) {
+    const dsv4sa_pool_desc& d = pools[k];
+    PoolBytes& b = p.pool[k];
+    b.base = static_cast<uint8_t*>(d.base);
+    b.stride = d.page_stride;
+    b.off[0] = static_cast<int32_t>(d.nope_off), b.row[0] = d.nope_row;
+    b.off[1] = static_cast<int32_t>(d.rope_off), b.row[1] = d.rope_row;
+    b.off[2] = static_cast<int32_t>(d.scale_off), b.row[2] = d.scale_row;
+  }
+}
+
+void fill_cache(const dsv4sa_cache_desc* c, CacheParams& p) {
+  fill_pools(c->pools, c->n_pools, p);
+  p.rows = c->rows;
+  p.pt_stride = c->pt_stride;
+  p.pt = c->page_table;
+  p.use = c->use;
+}
+
+int sm_count(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSV4SA_ERR_CUDA;
+  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? DSV4SA_OK : DSV4SA_ERR_CUDA;
+}
+
+// CTAs that share one page's copy: enough that n pages fill the GPU, at most 8
+// (a share of a few kilobytes).
+int copy_pieces(int64_t n, int sms) {
+  int pieces = 1;
+  while (pieces < 8 && n * pieces < 4 * static_cast<int64_t>(sms)) pieces *= 2;
+  return pieces;
+}
+
+int done(cudaError_t e) { return e == cudaSuccess ? DSV4SA_OK : DSV4SA_ERR_CUDA; }
+
+}  // namespace
+
+int launch_pages_copy(const dsv4sa_pool_desc* pools, int32_t n_pools, const int32_t* src, const int32_t* dst, int32_t n,
+                      cudaStream_t stream) {
+  CacheParams p{};
+  fill_pools(pools, n_pools, p);
+  int sms = 0;
+  if (const int rc = sm_count(&sms); rc != DSV4SA_OK) return rc;
+  const int pieces = copy_pieces(n, sms);
+  return done(launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(static_cast<int64_t>(n) * pieces)),
+                         dim3(kCopyThreads), 0, stream, p, src, dst, pieces));
+}
+
+int launch_cache_release(const dsv4sa_cache_desc* c, const int32_t* rows, int32_t n, cudaStream_t stream) {
+  CacheParams p{};
+  fill_cache(c, p);
+  int sms = 0;
+  if (const int rc = sm_count(&sms); rc != DSV4SA_OK) return rc;
+  const int64_t want = (static_cast<int64_t>(n) * p.pt_stride + kCopyThreads - 1) / kCopyThreads;
+  const int64_t full = static_cast<int64_t>(sms) * 8;
+  return done(launch_pdl(cache_release_kernel, dim3(static_cast<unsigned>(want < full ? want : full)),
+                         dim3(kCopyThreads), 0, stream, p, rows, n));
+}
+
+int launch_cache_fork(const dsv4sa_cache_desc* c, const int32_t* src, const int32_t* dst, const int32_t* len, int32_t n,
+                      int32_t* new_page, cudaStream_t stream) {
+  CacheParams p{};
+  fill_cache(c, p);
+  const ForkParams f{src, dst, len, new_page, n};
+  int sms = 0;
+  if (const int rc = sm_count(&sms); rc != DSV4SA_OK) return rc;
+  if (launch_pdl(cache_fork_alloc_kernel, dim3(1), dim3(kAllocThreads), 0, stream, p, f) != cudaSuccess)
+    return DSV4SA_ERR_CUDA;
+  const int pieces = copy_pieces(n, sms);
+  return done(launch_pdl(cache_fork_kernel, dim3(static_cast<unsigned>(static_cast<int64_t>(n) * pieces)),
+                         dim3(kCopyThreads), 0, stream, p, f, pieces));
+}
+
+int launch_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* dst, int32_t* new_id, int32_t* n_used,
+                         cudaStream_t stream) {
+  CompactParams c{};
+  fill_cache(src, c.src);
+  fill_cache(dst, c.dst);
+  c.new_id = new_id;
+  c.n_used = n_used;
+  c.in_place = src->pools[0].base == dst->pools[0].base;
+  int sms = 0;
+  if (const int rc = sm_count(&sms); rc != DSV4SA_OK) return rc;
+  if (launch_pdl(cache_plan_kernel, dim3(1), dim3(kAllocThreads), 0, stream, c) != cudaSuccess) return DSV4SA_ERR_CUDA;
+  const int64_t full = static_cast<int64_t>(sms) * 8;
+  const int64_t want = c.src.num_pages;
+  return done(launch_pdl(cache_move_kernel, dim3(static_cast<unsigned>(want < full ? want : full)), dim3(kCopyThreads),
+                         0, stream, c));
+}
+
+uint32_t read_error_word_pages(cudaStream_t stream, bool clear) {
+  uint32_t v = 0;
+  cudaMemcpyFromSymbolAsync(&v, g_err_word, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+  cudaStreamSynchronize(stream);
+  if (clear && v) {
+    const uint32_t z = 0;
+    cudaMemcpyToSymbolAsync(g_err_word, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
+    cudaStreamSynchronize(stream);
+  }
+  return v;
+}
+
+}  // namespace dsv4sa

@@ -47,7 +47,7 @@ int run_body(dsv4sa_step* st, cudaStream_t stream) {
   // the top-k prefetches the attention's rows: its page table and q_seq come with the second copy
   if (cudaStreamWaitEvent(stream, st->join, 0) != cudaSuccess) return DSV4SA_ERR_CUDA;
   const dsv4sa_attn_args& a = st->attn;
-  rc = a.kc > 0 && a.comp
+  rc = a.kc > 0 && a.comp && a.comp->kind == DSV4SA_POOL_KV   // FP4 rows are not prefetched
            ? dsv4sa_topk_prefetch(d.logits, d.logits_stride, d.n_vis, d.T, d.n_max, d.k, d.idx, d.idx_stride,
                                   d.topk_ws, d.topk_ws_bytes, a.comp, a.comp_pt, a.comp_pt_stride, a.q_seq, stream)
            : dsv4sa_topk(d.logits, d.logits_stride, d.n_vis, d.T, d.n_max, d.k, d.idx, d.idx_stride, d.topk_ws,

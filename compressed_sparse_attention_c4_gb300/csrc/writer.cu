@@ -146,6 +146,19 @@ __device__ __forceinline__ uint32_t e2m1_code(float y) {
   return m | ((__float_as_uint(y) >> 28) & 8u);
 }
 
+// The value of an E2M1 code: magnitude m of codes 0-7 is m / 2 up to 4, then 3, 4, 6.
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+  const uint32_t m = code & 7u;
+  // exponent field 126 + (m >> 1) and the mantissa bit below it; codes 0 and 1 are 0 and 0.5
+  const uint32_t b = m >= 2u ? ((126u + (m >> 1)) << 23) | ((m & 1u) << 22) : m * 0x3F000000u;
+  return __uint_as_float(b | ((code & 8u) << 28));
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // fp32 nearest to 128^-0.5, the scale of the order-128 Hadamard rotation.
 constexpr float kRot128 = 0x1.6a09e6p-4f;
 
@@ -253,6 +266,195 @@ __global__ void __launch_bounds__(kThreads) fp4_key_write_kernel(const WriterPar
   }
 }
 
+// KV rows into a KV_FP4 pool: a warp per row, 16 values a lane; lanes 0-27 hold
+// the nope part (a 32-value block per lane pair, quantised as the FP4 keys are),
+// lanes 28-31 the rope values, stored as they are.  A lane's 16 codes leave as
+// one 8-byte store, the row's 14 exponent bytes as three 4-byte stores and one
+// 2-byte store (the last two bytes of the scale row are padding, never written).
+// A block that holds an infinity or a NaN gets the exponent byte 255 (E8M0 NaN)
+// and codes 0, so it reads back as NaN.  kRowsW rows per warp are in flight: the
+// row loads are independent of the entry -> page look-ups.
+constexpr int kRowsW = 2;
+
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+  uint32_t r;   // nearest, ties to even, saturating: the codes e2m1_code counts out
+  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterParams p) {
+  griddep_launch();
+  griddep_wait();   // the rows may come from the previous kernel of the stream
+  const int c = static_cast<int>(threadIdx.x & 31u);
+  const bool rope = c >= 28;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kRowsW;
+  for (int64_t r0 = ((static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5) * kRowsW; r0 < p.n;
+       r0 += stride) {   // warp-uniform: every lane takes part in the shuffles
+    int s[kRowsW], page[kRowsW];
+    bool ok[kRowsW];
+    uint4 v[kRowsW][2];
+#pragma unroll
+    for (int k = 0; k < kRowsW; ++k) {   // clamped rows: unconditional loads, all in flight
+      const int64_t rc = r0 + k < p.n ? r0 + k : p.n - 1;
+      s[k] = __ldg(p.row_entry + rc);
+      page[k] = __ldg(p.row_seq + rc);
+      const uint4* src = p.rows + rc * 64 + c * 2;
+      v[k][0] = __ldg(src);
+      v[k][1] = __ldg(src + 1);
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsW; ++k) {
+      ok[k] = s[k] >= 0 && (s[k] >> 6) < p.pt_stride && page[k] >= 0;
+      page[k] = __ldg(p.page_table + static_cast<int64_t>(ok[k] ? page[k] : 0) * p.pt_stride + (ok[k] ? s[k] >> 6 : 0));
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsW; ++k) {
+      const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+      uint32_t mag = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mag = max(mag, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+      mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));   // the block's lane pair
+      const bool finite = mag < 0x7F800000u;
+      const float t = __fmul_rn(fmaxf(__uint_as_float(finite ? mag : 0u), kFp4AmaxFloor), kFp4MaxInv);
+      const uint32_t tb = __float_as_uint(t);                 // normal: t >= 2^-126
+      const int e = static_cast<int>((tb >> 23) & 0xFFu) - 127 + ((tb & 0x7FFFFFu) != 0u ? 1 : 0);   // <= 126
+      const float inv = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.f;        // 2^-e
+      uint32_t lo = 0, hi = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x0 = finite ? __uint_as_float(w[j] << 16) : 0.f, x1 = finite ? __uint_as_float(w[j] & 0xFFFF0000u) : 0.f;
+        const uint32_t byte = e2m1x2(__fmul_rn(x0, inv), __fmul_rn(x1, inv));
+        if (j < 4) lo |= byte << (8 * j);
+        else hi |= byte << (8 * (j - 4));
+      }
+      // exponent bytes 4 m .. 4 m + 3 of the row, from lanes 8 m, 8 m + 2, 8 m + 4, 8 m + 6, in lane m
+      const uint32_t eb = finite ? static_cast<uint32_t>(e + 127) : 255u;
+      const int q0 = (c & 3) * 8;
+      const uint32_t e8 = __shfl_sync(0xffffffffu, eb, q0) | (__shfl_sync(0xffffffffu, eb, q0 + 2) << 8) |
+                          (__shfl_sync(0xffffffffu, eb, q0 + 4) << 16) | (__shfl_sync(0xffffffffu, eb, q0 + 6) << 24);
+      if (r0 + k >= p.n) continue;
+      if (!ok[k] || page[k] < 0 || page[k] >= p.num_pages) {
+        if (c == 0) raise_error(kErrIndex);
+        continue;
+      }
+      const int slot = s[k] & 63;
+      uint8_t* pg = p.base + static_cast<int64_t>(page[k]) * p.page_stride;
+      if (rope) {
+        uint4* dst = reinterpret_cast<uint4*>(pg + p.rope_off + static_cast<int64_t>(slot) * p.rope_row) + (c - 28) * 2;
+        dst[0] = v[k][0];
+        dst[1] = v[k][1];
+      } else {
+        *reinterpret_cast<uint2*>(pg + p.nope_off + static_cast<int64_t>(slot) * p.nope_row + c * 8) = make_uint2(lo, hi);
+        uint8_t* sc = pg + p.scale_off + static_cast<int64_t>(slot) * p.scale_row;
+        if (c < 3) reinterpret_cast<uint32_t*>(sc)[c] = e8;
+        if (c == 3) reinterpret_cast<uint16_t*>(sc)[6] = static_cast<uint16_t>(e8);
+      }
+    }
+  }
+}
+
+// Rows of a KV or KV_FP4 pool back as BF16: value e4m3(code) * scale rounded to
+// BF16, or e2m1(code) * 2^(b - 127), which BF16 holds exactly (2 significant
+// bits; past its range an infinity, as a product of the two rounds to).  A warp
+// per row and 16 values a lane as in the writer; kRowsR rows per warp in flight,
+// since each is three dependent loads (entry, page id, row).
+constexpr int kRowsR = 4;
+
+struct ReaderParams {
+  WriterParams w;          // rows unused
+  uint4* out;              // bf16 [n][512]
+};
+
+template <bool kFp4>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReaderParams q) {
+  const WriterParams& p = q.w;
+  griddep_launch();
+  griddep_wait();
+  const int c = static_cast<int>(threadIdx.x & 31u);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kRowsR;
+  for (int64_t r0 = ((static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5) * kRowsR; r0 < p.n; r0 += stride) {
+    int s[kRowsR], page[kRowsR];
+    bool ok[kRowsR];
+    uint4 lo[kRowsR], hi[kRowsR];     // nope: the lane's codes in lo; rope: its 32 bytes
+    float scl[kRowsR];
+#pragma unroll
+    for (int k = 0; k < kRowsR; ++k) {
+      const int64_t rc = r0 + k < p.n ? r0 + k : p.n - 1;
+      s[k] = __ldg(p.row_entry + rc);
+      page[k] = __ldg(p.row_seq + rc);
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsR; ++k) {
+      ok[k] = s[k] >= 0 && (s[k] >> 6) < p.pt_stride && page[k] >= 0;
+      page[k] = __ldg(p.page_table + static_cast<int64_t>(ok[k] ? page[k] : 0) * p.pt_stride + (ok[k] ? s[k] >> 6 : 0));
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsR; ++k) {
+      const bool bad = !ok[k] || page[k] < 0 || page[k] >= p.num_pages;
+      if (bad && s[k] != -1 && r0 + k < p.n && c == 0) raise_error(kErrIndex);   // -1: no row there, zeros
+      ok[k] = !bad;
+      const int slot = s[k] & 63;
+      const uint8_t* pg = p.base + static_cast<int64_t>(ok[k] ? page[k] : 0) * p.page_stride;
+      lo[k] = hi[k] = make_uint4(0u, 0u, 0u, 0u);
+      scl[k] = 0.f;
+      if (!ok[k]) continue;
+      if (c >= 28) {
+        const uint4* src = reinterpret_cast<const uint4*>(pg + p.rope_off + slot * p.rope_row) + (c - 28) * 2;
+        lo[k] = __ldcs(src);
+        hi[k] = __ldcs(src + 1);
+      } else if constexpr (kFp4) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(pg + p.nope_off + slot * p.nope_row) + c);
+        lo[k].x = v.x;
+        lo[k].y = v.y;
+        const uint32_t b = __ldcs(pg + p.scale_off + slot * p.scale_row + (c >> 1));
+        scl[k] = __uint_as_float(b == 0u ? 0x00400000u : (b == 255u ? 0x7FC00000u : b << 23));
+      } else {
+        lo[k] = __ldcs(reinterpret_cast<const uint4*>(pg + p.nope_off + slot * p.nope_row) + c);
+        scl[k] = __ldcs(reinterpret_cast<const float*>(pg + p.scale_off + slot * p.scale_row) + (c >> 2));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsR; ++k) {
+      if (r0 + k >= p.n) continue;
+      if (c < 28) {
+        uint32_t o[8];
+        if constexpr (kFp4) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t byte = ((j < 4 ? lo[k].x : lo[k].y) >> (8 * (j & 3))) & 0xFFu;
+            o[j] = pack2(e2m1_value(byte & 15u) * scl[k], e2m1_value(byte >> 4) * scl[k]);
+          }
+        } else {
+          const uint32_t w[4] = {lo[k].x, lo[k].y, lo[k].z, lo[k].w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                static_cast<__nv_fp8x2_storage_t>((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu), __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            o[j] = pack2(__fmul_rn(f.x, scl[k]), __fmul_rn(f.y, scl[k]));
+          }
+        }
+        lo[k] = make_uint4(o[0], o[1], o[2], o[3]);
+        hi[k] = make_uint4(o[4], o[5], o[6], o[7]);
+        if (!ok[k]) lo[k] = hi[k] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      uint4* dst = q.out + (r0 + k) * 64 + c * 2;
+      __stcs(dst, lo[k]);
+      __stcs(dst + 1, hi[k]);
+    }
+  }
+}
+
+// A resident grid of `rows_per_block`-row CTAs over n rows.
+template <class P>
+cudaError_t launch_rows(void (*kernel)(P), const P& p, int64_t n, int64_t rows_per_block, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cudaErrorUnknown;
+  const int64_t want = (n + rows_per_block - 1) / rows_per_block, cap = static_cast<int64_t>(sms) * 8;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(kThreads), 0, stream, p);
+}
+
 template <int kLanesPerRow, int kQuantBlocks>
 cudaError_t launch_writer(const WriterParams& p, cudaStream_t stream) {
   static int resident = 0;                       // CTAs per SM, queried once
@@ -273,15 +475,12 @@ cudaError_t launch_writer(const WriterParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_cache_write(const dsv4sa_pool_desc* pool, const int32_t* page_table, int32_t pt_stride,
-                       const int32_t* row_seq, const int32_t* row_entry, const void* rows, int32_t n,
-                       bool rotate, cudaStream_t stream) {
+static WriterParams pool_params(const dsv4sa_pool_desc* pool, const int32_t* page_table, int32_t pt_stride,
+                                const int32_t* row_seq, const int32_t* row_entry, int32_t n) {
   WriterParams p{};
-  const bool kv = pool->kind == DSV4SA_POOL_KV;
   p.page_table = page_table;
   p.row_seq = row_seq;
   p.row_entry = row_entry;
-  p.rows = static_cast<const uint4*>(rows);
   p.base = static_cast<uint8_t*>(pool->base);
   p.page_stride = pool->page_stride;
   p.num_pages = pool->num_pages;
@@ -293,7 +492,28 @@ int launch_cache_write(const dsv4sa_pool_desc* pool, const int32_t* page_table, 
   p.scale_row = pool->scale_row;
   p.pt_stride = pt_stride;
   p.n = n;
+  return p;
+}
+
+int launch_cache_read(const dsv4sa_pool_desc* pool, const int32_t* page_table, int32_t pt_stride,
+                      const int32_t* row_seq, const int32_t* row_entry, void* rows, int32_t n, cudaStream_t stream) {
+  const ReaderParams q{pool_params(pool, page_table, pt_stride, row_seq, row_entry, n), static_cast<uint4*>(rows)};
+  constexpr int64_t per = (kThreads / 32) * kRowsR;
+  const cudaError_t e = pool->kind == DSV4SA_POOL_KV_FP4 ? launch_rows(cache_read_kernel<true>, q, n, per, stream)
+                                                         : launch_rows(cache_read_kernel<false>, q, n, per, stream);
+  return e == cudaSuccess ? DSV4SA_OK : DSV4SA_ERR_CUDA;
+}
+
+int launch_cache_write(const dsv4sa_pool_desc* pool, const int32_t* page_table, int32_t pt_stride,
+                       const int32_t* row_seq, const int32_t* row_entry, const void* rows, int32_t n,
+                       bool rotate, cudaStream_t stream) {
+  WriterParams p = pool_params(pool, page_table, pt_stride, row_seq, row_entry, n);
+  p.rows = static_cast<const uint4*>(rows);
+  const bool kv = pool->kind == DSV4SA_POOL_KV;
   if (n == 0) return DSV4SA_OK;
+  if (pool->kind == DSV4SA_POOL_KV_FP4 && !rotate)
+    return launch_rows(kv_fp4_write_kernel, p, n, (kThreads / 32) * kRowsW, stream) == cudaSuccess ? DSV4SA_OK
+                                                                                                   : DSV4SA_ERR_CUDA;
   if (pool->kind == DSV4SA_POOL_IDXK_FP4) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DSV4SA_ERR_CUDA;

@@ -27,13 +27,16 @@ LIB_PATH = os.path.join(_HERE, "libdsv4sa.so")
 POOL_KV = 0
 POOL_IDXK = 1
 POOL_IDXK_FP4 = 2
+POOL_KV_FP4 = 3
+MAX_POOLS = 4
 ATTN_DECODE = 0
 ATTN_PREFILL = 1
 PAGE = 64
 HEAD_DIM = 512
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported size", 3: "workspace missing or too small",
-          4: "CUDA runtime error", 5: "index or page id out of range (device)", 6: "device wait timed out"}
+          4: "CUDA runtime error", 5: "index or page id out of range (device)", 6: "device wait timed out",
+          7: "no free page left (device)"}
 
 
 class DSV4SAError(RuntimeError):
@@ -65,6 +68,12 @@ class AttnArgs(ctypes.Structure):
                 ("win_pos", ctypes.c_void_p), ("win_ring", ctypes.c_int32), ("reserved1", ctypes.c_int32),
                 ("rope_cs", ctypes.c_void_p), ("rope_pos", ctypes.c_void_p), ("rope_rows", ctypes.c_int32),
                 ("reserved2", ctypes.c_int32)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("pools", ctypes.POINTER(PoolDesc)), ("n_pools", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("pt_stride", ctypes.c_int32), ("reserved", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("use", ctypes.c_void_p)]
 
 
 class StepDesc(ctypes.Structure):
@@ -101,6 +110,13 @@ _SIGS = {
     "dsv4sa_window_indices": ([_P, _I32, _I32, _I32, _P, _I32, _P], ctypes.c_int),
     "dsv4sa_cache_write": ([ctypes.POINTER(PoolDesc), _P, _I32, _P, _P, _P, _I32, _P], ctypes.c_int),
     "dsv4sa_cache_write_rotated": ([ctypes.POINTER(PoolDesc), _P, _I32, _P, _P, _P, _I32, _P], ctypes.c_int),
+    "dsv4sa_cache_read": ([ctypes.POINTER(PoolDesc), _P, _I32, _P, _P, _P, _I32, _P], ctypes.c_int),
+    "dsv4sa_pages_copy": ([ctypes.POINTER(PoolDesc), _I32, _P, _P, _I32, _P], ctypes.c_int),
+    "dsv4sa_cache_release": ([ctypes.POINTER(CacheDesc), _P, _I32, _P], ctypes.c_int),
+    "dsv4sa_cache_fork": ([ctypes.POINTER(CacheDesc), _P, _P, _P, _I32, _P, _P], ctypes.c_int),
+    "dsv4sa_cache_compact": ([ctypes.POINTER(CacheDesc), ctypes.POINTER(CacheDesc), _P, _P, _P], ctypes.c_int),
+    "dsv4sa_rmsnorm_quant": ([_P, _I64, _P, _I64, _P, ctypes.c_float, _I32, _I32, _I32, _P, _P, _P, _P, _P],
+                             ctypes.c_int),
     "dsv4sa_compress_indices": ([_P, _I32, _I32, _P, _I32, _P], ctypes.c_int),
     "dsv4sa_selftest_wait_timeout": ([_P, _P], ctypes.c_int),
     "dsv4sa_copy_async": ([_P, _P, _SZ, _P], ctypes.c_int),
@@ -244,6 +260,22 @@ def pack_key_pool_fp4(codes: np.ndarray, e8m0: np.ndarray, device="cuda"):
     return dev, dsv4sa_pool_desc_init(POOL_IDXK_FP4, dev, P)
 
 
+def pack_kv_pool_fp4(nope_codes: np.ndarray, nope_e8m0: np.ndarray, rope_bits: np.ndarray, device="cuda"):
+    """Logical FP4 KV pool arrays (E2M1 codes uint8 [P, 64, 448], one per byte; E8M0
+    bytes [P, 64, 14]; BF16 bits [P, 64, 64]) -> (device byte tensor, PoolDesc)."""
+    P = nope_codes.shape[0]
+    L = _layout(POOL_KV_FP4, P)
+    host = np.zeros((P, L.page_stride), dtype=np.uint8)
+    host[:, L.nope_off:L.nope_off + PAGE * L.nope_row] = pack_fp4_codes(nope_codes).reshape(P, -1)
+    host[:, L.rope_off:L.rope_off + PAGE * L.rope_row] = np.ascontiguousarray(rope_bits).view(np.uint8).reshape(P, -1)
+    sc = np.zeros((P, PAGE, L.scale_row), dtype=np.uint8)
+    sc[:, :, :L.n_scales] = nope_e8m0
+    host[:, L.scale_off:L.scale_off + PAGE * L.scale_row] = sc.reshape(P, -1)
+    dev = _alloc_pool(POOL_KV_FP4, P, device)
+    dev.copy_(torch.from_numpy(host.reshape(-1)))
+    return dev, dsv4sa_pool_desc_init(POOL_KV_FP4, dev, P)
+
+
 # ---------------------------------------------------------------- stage 1: indexer
 
 def dsv4sa_indexer_logits(kpool: PoolDesc, page_table, q_seq, n_vis, q_fp8, q_scale, w, n_max: int, logits,
@@ -325,8 +357,8 @@ def dsv4sa_window_indices(pos, window: int, ring: int, idx_w, stream=None):
 
 
 def dsv4sa_cache_write(pool: PoolDesc, page_table, row_seq, row_entry, rows, stream=None):
-    """Quantise BF16 rows [n, 512] (KV pool) or [n, 128] (indexer-key pool) into the pool."""
-    want = HEAD_DIM if pool.kind == POOL_KV else 128
+    """Quantise BF16 rows [n, 512] (KV and KV_FP4 pools) or [n, 128] (indexer-key pools) into the pool."""
+    want = HEAD_DIM if pool.kind in (POOL_KV, POOL_KV_FP4) else 128
     if rows.dim() != 2 or rows.shape[1] != want:
         raise ValueError(f"rows must be [n, {want}]")
     n = rows.shape[0]
@@ -345,6 +377,116 @@ def dsv4sa_cache_write_rotated(pool: PoolDesc, page_table, row_seq, row_entry, r
         ctypes.byref(pool), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
         _dev(row_seq, "row_seq", torch.int32), _dev(row_entry, "row_entry", torch.int32),
         _dev(rows, "rows", torch.bfloat16), rows.shape[0], _stream(stream)))
+
+
+def dsv4sa_cache_read(pool: PoolDesc, page_table, row_seq, row_entry, rows, stream=None):
+    """Rows of a KV or KV_FP4 pool into BF16 rows [n, 512]: the values the attention reads."""
+    n = row_entry.shape[0]
+    if rows.dim() != 2 or rows.shape[1] != HEAD_DIM or rows.shape[0] != n or row_seq.shape[0] != n:
+        raise ValueError("rows must be [n, 512] for n entries")
+    _check("dsv4sa_cache_read", lib().dsv4sa_cache_read(
+        ctypes.byref(pool), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
+        _dev(row_seq, "row_seq", torch.int32), _dev(row_entry, "row_entry", torch.int32),
+        _dev(rows, "rows", torch.bfloat16), n, _stream(stream)))
+
+
+# ---------------------------------------------------------------- pages of a cache
+
+def _pool_array(pools):
+    if not 1 <= len(pools) <= MAX_POOLS:
+        raise ValueError(f"a cache has 1 to {MAX_POOLS} pools")
+    return (PoolDesc * len(pools))(*pools)
+
+
+def page_cache(pools, page_table, use) -> CacheDesc:
+    """The descriptor of a cache: pools that share page ids, the page table int32
+    [rows, pt_stride] and the use counts int32 [num_pages] (table entries that
+    hold each page).  The tensors are kept alive by the descriptor."""
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [rows, pt_stride]")
+    if use.shape != (pools[0].num_pages,):
+        raise ValueError("use must have one count per page")
+    c = CacheDesc()
+    c._keep = (_pool_array(pools), page_table, use)
+    c.pools = ctypes.cast(c._keep[0], ctypes.POINTER(PoolDesc))
+    c.n_pools = len(pools)
+    c.rows, c.pt_stride = page_table.shape
+    c.page_table = _dev(page_table, "page_table", torch.int32)
+    c.use = _dev(use, "use", torch.int32)
+    return c
+
+
+def dsv4sa_pages_copy(pools, src_page, dst_page, stream=None):
+    """Copy pages src_page[i] -> dst_page[i] of every pool in the list (int32 [n]; -1: skip)."""
+    if src_page.shape != dst_page.shape:
+        raise ValueError("src_page and dst_page differ in length")
+    arr = _pool_array(pools)
+    _check("dsv4sa_pages_copy", lib().dsv4sa_pages_copy(
+        arr, len(pools), _dev(src_page, "src_page", torch.int32), _dev(dst_page, "dst_page", torch.int32),
+        src_page.numel(), _stream(stream)))
+
+
+def dsv4sa_cache_release(cache: CacheDesc, row, stream=None):
+    """Release rows (int32 [n]) of the page table: entries -1, their pages' counts down by one."""
+    _check("dsv4sa_cache_release", lib().dsv4sa_cache_release(
+        ctypes.byref(cache), _dev(row, "row", torch.int32), row.numel(), _stream(stream)))
+
+
+def dsv4sa_cache_fork(cache: CacheDesc, src_row, dst_row, length, new_page, stream=None):
+    """Fork the first length[i] entries of row src_row[i] into the empty row dst_row[i]:
+    full pages shared, a partial last page copied into new_page[i] (all int32 [n])."""
+    n = src_row.numel()
+    if dst_row.numel() != n or length.numel() != n or new_page.numel() != n:
+        raise ValueError("src_row, dst_row, length and new_page differ in length")
+    _check("dsv4sa_cache_fork", lib().dsv4sa_cache_fork(
+        ctypes.byref(cache), _dev(src_row, "src_row", torch.int32), _dev(dst_row, "dst_row", torch.int32),
+        _dev(length, "length", torch.int32), n, _dev(new_page, "new_page", torch.int32), _stream(stream)))
+
+
+def dsv4sa_cache_compact(src: CacheDesc, dst: CacheDesc, new_id, n_used, stream=None):
+    """Move the pages in use to the front of dst's pools (dst may be src: in place),
+    with dst's table and counts by the new ids.  new_id int32 [src pages], n_used int32 [1]."""
+    if new_id.numel() != src.pools[0].num_pages or n_used.numel() != 1:
+        raise ValueError("new_id must have one entry per page, n_used one")
+    _check("dsv4sa_cache_compact", lib().dsv4sa_cache_compact(
+        ctypes.byref(src), ctypes.byref(dst), _dev(new_id, "new_id", torch.int32), _dev(n_used, "n_used", torch.int32),
+        _stream(stream)))
+
+
+# ---------------------------------------------------------------- norm
+
+def _bf16_rows(t: torch.Tensor, name: str, n: int, dim: int):
+    """A BF16 CUDA tensor [n, dim] whose rows may be strided -> (pointer, row stride)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != (n, dim) or (dim > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{n}, {dim}] with consecutive values in a row")
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if n > 1 else dim)
+
+
+def dsv4sa_rmsnorm_quant(x, norm_w, codes=None, scale=None, group: int = 128, residual=None, residual_out=None, y=None,
+                         eps: float = 1e-6, stream=None):
+    """RMSNorm of BF16 rows x [n, dim] (+ residual) with fp32 weights [dim]: E4M3 codes
+    uint8 [n, dim] with fp32 scales [n, dim / group], the sum x + residual and
+    the norm's output as BF16 [n, dim], each where a tensor is given (see dsv4sa.h)."""
+    n, dim = x.shape
+    if norm_w.shape != (dim,):
+        raise ValueError("norm_w must be [dim]")
+    xp, xs = _bf16_rows(x, "x", n, dim)
+    rp, rs = _bf16_rows(residual, "residual", n, dim) if residual is not None else (None, 0)
+    for t, name, shape in ((residual_out, "residual_out", (n, dim)), (y, "y", (n, dim)), (codes, "codes", (n, dim))):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be [n, dim]")
+    if scale is not None and (group < 1 or scale.shape != (n, dim // group)):
+        raise ValueError("scale must be [n, dim / group]")
+    _check("dsv4sa_rmsnorm_quant", lib().dsv4sa_rmsnorm_quant(
+        xp, xs, rp, rs, _dev(norm_w, "norm_w", torch.float32), float(eps), n, dim, group,
+        _dev(residual_out, "residual_out", torch.bfloat16) if residual_out is not None else None,
+        _dev(y, "y", torch.bfloat16) if y is not None else None,
+        _dev(codes, "codes", torch.uint8) if codes is not None else None,
+        _dev(scale, "scale", torch.float32) if scale is not None else None, _stream(stream)))
 
 
 def dsv4sa_compress_windows(kv, score, first_tok, prev_tok, position, ratio: int, overlap: bool, ape, norm_w,

@@ -61,6 +61,8 @@ extern "C" {
 #define DSV4SA_MAX_IDX_HEADS 128
 #define DSV4SA_MAX_IDX_HEADS_FP4 64
 #define DSV4SA_MAX_TOPK    2048
+#define DSV4SA_MAX_POOLS   4    /* pools of one cache (dsv4sa_cache_desc)           */
+#define DSV4SA_MAX_NORM_DIM 16384
 
 typedef enum {
   DSV4SA_OK = 0,
@@ -69,13 +71,15 @@ typedef enum {
   DSV4SA_ERR_WORKSPACE = 3,      /* workspace missing or smaller than required    */
   DSV4SA_ERR_CUDA = 4,           /* a CUDA runtime call or launch failed          */
   DSV4SA_ERR_INDEX_OOB = 5,      /* device: an index or page id was out of range  */
-  DSV4SA_ERR_DEVICE_TIMEOUT = 6  /* device: a bounded wait ran out of time        */
+  DSV4SA_ERR_DEVICE_TIMEOUT = 6, /* device: a bounded wait ran out of time        */
+  DSV4SA_ERR_NO_PAGES = 7        /* device: no free page was left                 */
 } dsv4sa_status;
 
 typedef enum {
   DSV4SA_POOL_KV = 0,       /* attention KV rows: 448 e4m3 + 7 fp32 scales + 64 bf16   */
   DSV4SA_POOL_IDXK = 1,     /* indexer keys: 128 e4m3 + 2 fp32 scales                  */
-  DSV4SA_POOL_IDXK_FP4 = 2  /* indexer keys, FP4 variant: 128 e2m1 + 4 e8m0 scales     */
+  DSV4SA_POOL_IDXK_FP4 = 2, /* indexer keys, FP4 variant: 128 e2m1 + 4 e8m0 scales     */
+  DSV4SA_POOL_KV_FP4 = 3    /* attention KV rows, FP4: 448 e2m1 + 14 e8m0 + 64 bf16    */
 } dsv4sa_pool_kind;
 
 /*
@@ -92,10 +96,15 @@ typedef enum {
  *   IDXK_FP4 page (4352 B): key [64][64] bytes  at  0      (128 e2m1 codes, two per
  *                        byte, value 2j in the low nibble of byte j)
  *                        scale [64][4]   e8m0   at  4096   (one per 32 values)
+ *   KV_FP4 page (23552 B): nope  [64][224] bytes  at  0     (448 e2m1 codes, two per
+ *                        byte, value 2j in the low nibble of byte j)
+ *                        rope  [64][64]  bf16   at  14336   (128 B per slot)
+ *                        scale [64][16]  e8m0   at  22528   (14 used: one per 32 nope values)
  *
  * ([V4] §3.5 fp4_quant_kernel: FP4 E2M1 in blocks of 32 with a power-of-two
  * scale; [NVFP4] 32-group E8M0 scales for the indexer's q and k.)  Value of
- * element d of an IDXK_FP4 slot = e2m1(code[d]) * 2^(e8m0[d / 32] - 127).
+ * element d of an IDXK_FP4 or KV_FP4 slot = e2m1(code[d]) * 2^(e8m0[d / 32] - 127)
+ * (e8m0 255: NaN); BF16 holds it exactly, or as an infinity from 2^128 on.
  * The indexer (dsv4sa_indexer_logits) reads IDXK pools; IDXK_FP4 pools are
  * written by dsv4sa_cache_write and dsv4sa_cache_write_rotated and read by
  * dsv4sa_indexer_logits_fp4.
@@ -107,18 +116,19 @@ typedef enum {
 typedef struct {
   int32_t kind;          /* dsv4sa_pool_kind                                       */
   int32_t page_size;     /* 64                                                     */
-  int32_t nope_dim;      /* FP8 elements per slot: 448 (KV) | 128 (IDXK)           */
-  int32_t rope_dim;      /* BF16 elements per slot: 64 (KV) | 0 (IDXK)             */
-  int32_t scale_group;   /* 64 (32 for IDXK_FP4)                                   */
-  int32_t n_scales;      /* scales used per slot: 7 (KV) | 2 (IDXK) | 4 (IDXK_FP4) */
+  int32_t nope_dim;      /* FP8 / FP4 elements per slot: 448 (KV, KV_FP4) | 128    */
+  int32_t rope_dim;      /* BF16 elements per slot: 64 (KV, KV_FP4) | 0            */
+  int32_t scale_group;   /* 64 (32 for IDXK_FP4 and KV_FP4)                        */
+  int32_t n_scales;      /* scales used per slot: 7 (KV) | 2 (IDXK) | 4 (IDXK_FP4)
+                            | 14 (KV_FP4)                                          */
   int64_t num_pages;
   int64_t page_stride;   /* bytes between pages                                    */
-  int64_t nope_off;      /* byte offset of the FP8 block inside a page             */
-  int64_t rope_off;      /* byte offset of the BF16 block (KV only)                */
-  int64_t scale_off;     /* byte offset of the fp32 scale block                    */
-  int32_t nope_row;      /* bytes per slot in the code block  (448 | 128 | 64)     */
-  int32_t rope_row;      /* bytes per slot in the BF16 block  (128 | 0)            */
-  int32_t scale_row;     /* bytes per slot in the scale block (32 | 8 | 4)         */
+  int64_t nope_off;      /* byte offset of the code block inside a page            */
+  int64_t rope_off;      /* byte offset of the BF16 block (KV and KV_FP4 only)     */
+  int64_t scale_off;     /* byte offset of the scale block                         */
+  int32_t nope_row;      /* bytes per slot in the code block  (448 | 128 | 64 | 224) */
+  int32_t rope_row;      /* bytes per slot in the BF16 block  (128 | 0 | 0 | 128)  */
+  int32_t scale_row;     /* bytes per slot in the scale block (32 | 8 | 4 | 16)    */
   int32_t reserved;
   void*   base;          /* device pointer, caller-owned                           */
 } dsv4sa_pool_desc;
@@ -308,6 +318,11 @@ DSV4SA_API int dsv4sa_compress_indices(const int32_t* n_vis, int32_t T, int32_t 
  * QK^T and PV run on the tensor cores in BF16 with fp32 accumulation (the FP8
  * nope part is dequantised to BF16 on the gather); P is rounded to BF16 for
  * PV; the output is rounded to BF16 (round to nearest even).
+ *
+ * The pools are two of kind DSV4SA_POOL_KV, or two of kind DSV4SA_POOL_KV_FP4
+ * (a 4-bit cache; one of each is DSV4SA_ERR_UNSUPPORTED).  FP4 rows dequantise
+ * to BF16 exactly, partial results are exchanged in fp32, and no workspace is
+ * needed (ws may be null in either mode).
  */
 typedef struct {
   const void*  q;              /* device bf16 [T][H][512], 16-byte aligned                 */
@@ -370,12 +385,13 @@ typedef struct {
                                    over several CTAs and merged by log-sum-exp          */
 #define DSV4SA_ATTN_PREFILL 1   /* many queries: one CTA runs the whole online softmax   */
 
-/* Workspace bytes the given mode needs for these arguments (0 for prefill).
- * An upper bound over devices: a decode call may use less of it. */
+/* Workspace bytes the given mode needs for these arguments over KV pools (0 for
+ * prefill).  An upper bound over devices: a decode call may use less of it.
+ * Calls over KV_FP4 pools need none. */
 DSV4SA_API size_t dsv4sa_attn_workspace_size(int32_t mode, int32_t T, int32_t H, int32_t kc,
                                              int32_t kw);
 
-/* How a call with these arguments splits its work on the current device
+/* How a call with these arguments over KV pools splits its work on the current device
  * (host only; reads the device's SM count).  Outputs, each optional:
  *   nsplit          CTAs per (query, 64-head group) over which the rows are split
  *   rows_per_split  gathered rows per CTA
@@ -404,8 +420,8 @@ DSV4SA_API int dsv4sa_sparse_attn_prefill(const dsv4sa_attn_args* args, cudaStre
  * most 16384 entries, one kernel does both: the CTAs of a query's cluster
  * select its list from the logits together and gather their rows at once, so
  * no SM idles between a selection and the attention that waits for it.
- * Otherwise the two run as separate kernels (the top-k then prefetches the
- * selected rows into L2).
+ * Otherwise, and over KV_FP4 pools, the two run as separate kernels (over KV
+ * pools the top-k then prefetches the selected rows into L2).
  *   logits, logits_stride, n_vis, n_max   as dsv4sa_topk (logits 16-byte
  *            aligned with logits_stride % 4 == 0 for the one-kernel form)
  *   k        must equal attn->kc
@@ -436,6 +452,10 @@ DSV4SA_API int dsv4sa_topk_sparse_attn_decode(const dsv4sa_attn_args* attn, cons
  *               fast_round_scale): e = ceil(log2(max(amax, 6 * 2^-126) *
  *               fp32(1/6))), codes = E2M1 round-to-nearest-even of
  *               clamp(x / 2^e, -6, 6), the scale stored as the E8M0 byte e + 127.
+ *               DSV4SA_POOL_KV_FP4: rows are bf16 [n][512]; the 448 nope values
+ *               are quantised like FP4 keys (14 blocks), the 64 rope values
+ *               stored unchanged.  A block that holds an infinity or a NaN gets
+ *               the byte 255 and codes 0: it reads back as NaN.
  *   page_table  device int32 [rows][pt_stride]
  *   row_seq, row_entry  device int32 [n]
  *   rows        device bf16, 16-byte aligned
@@ -446,6 +466,115 @@ DSV4SA_API int dsv4sa_topk_sparse_attn_decode(const dsv4sa_attn_args* attn, cons
 DSV4SA_API int dsv4sa_cache_write(const dsv4sa_pool_desc* pool, const int32_t* page_table, int32_t pt_stride,
                                   const int32_t* row_seq, const int32_t* row_entry, const void* rows, int32_t n,
                                   cudaStream_t stream);
+
+/*
+ * Rows of a KV or KV_FP4 pool back as BF16 [n][512]: the value of each nope
+ * element rounded to BF16 (exact for KV_FP4), the rope values as stored -- what
+ * the attention reads.  Row r is entry row_entry[r] of the sequence whose
+ * page-table row is row_seq[r], as in dsv4sa_cache_write; an entry of -1 gives a
+ * row of zeros, any other entry or page id out of range also sets
+ * DSV4SA_ERR_INDEX_OOB on the device.  rows must not lie in the pool.
+ */
+DSV4SA_API int dsv4sa_cache_read(const dsv4sa_pool_desc* pool, const int32_t* page_table, int32_t pt_stride,
+                                 const int32_t* row_seq, const int32_t* row_entry, void* rows, int32_t n,
+                                 cudaStream_t stream);
+
+/*
+ * The pages of a cache ([SGL] 概念5 DeepSeekV4TokenToKVPool).  A cache is one to
+ * DSV4SA_MAX_POOLS pools that share page ids -- page p of each pool belongs
+ * together, e.g. a sequence's KV rows and its indexer keys -- one page table
+ * and a use count per page.  The calls below keep, for tables and counts that
+ * agree when they are called:
+ *   use[p] = table entries equal to p;  0: page p is free
+ * Entries of the table are page ids, or -1.  A caller that adds pages to a row
+ * itself sets their counts.
+ */
+typedef struct {
+  const dsv4sa_pool_desc* pools;  /* host array [n_pools], all with the same num_pages (< 2^31) */
+  int32_t  n_pools;
+  int32_t  rows;                  /* rows of the page table                                     */
+  int32_t  pt_stride;             /* entries of a row                                           */
+  int32_t  reserved;
+  int32_t* page_table;            /* device int32 [rows][pt_stride]                             */
+  int32_t* use;                   /* device int32 [num_pages], 16-byte aligned                  */
+} dsv4sa_cache_desc;
+
+/*
+ * Copy whole pages: page dst_page[i] of every pool becomes page src_page[i],
+ * for i < n; a pair with a -1 is skipped, an id out of range is skipped and sets
+ * DSV4SA_ERR_INDEX_OOB on the device.  The caller gives distinct dst pages, none
+ * of them a src of the same call.  Tables and counts are not touched.
+ *   src_page, dst_page   device int32 [n]
+ */
+DSV4SA_API int dsv4sa_pages_copy(const dsv4sa_pool_desc* pools, int32_t n_pools, const int32_t* src_page,
+                                 const int32_t* dst_page, int32_t n, cudaStream_t stream);
+
+/*
+ * Release rows of the table: every entry of row row[i], i < n, becomes -1 and
+ * its page's count goes down by one (a page whose count reaches 0 is free).
+ * A row of -1 is skipped; a row given twice is released once.  A row or page id
+ * out of range, or a page that was free already, sets DSV4SA_ERR_INDEX_OOB on
+ * the device.
+ */
+DSV4SA_API int dsv4sa_cache_release(const dsv4sa_cache_desc* cache, const int32_t* row, int32_t n,
+                                    cudaStream_t stream);
+
+/*
+ * Fork sequences (beams, samples of one prompt): fork i, i < n, makes row
+ * dst_row[i] a copy of the first length[i] entries (slots, not tokens) of row
+ * src_row[i].  Full pages are shared, their counts go up; a last page that is
+ * not full is copied -- its first length % 64 slots, in every pool -- into a
+ * free page, so the two sequences can go on apart.  The lowest free pages are
+ * taken, in the order of the forks.
+ *   new_page   device int32 [n]: the page fork i took, -1 when it needs none
+ * Refused forks, with their row left as it was: -3 and DSV4SA_ERR_INDEX_OOB on
+ * the device for a row, length or page id out of range, a dst row that was not
+ * released (its first entry is a page), one that an earlier fork of the call
+ * has taken, or a src that is empty, or a dst of this call, with length > 0; -2
+ * and DSV4SA_ERR_NO_PAGES on the device when no free page was left.
+ */
+DSV4SA_API int dsv4sa_cache_fork(const dsv4sa_cache_desc* cache, const int32_t* src_row, const int32_t* dst_row,
+                                 const int32_t* length, int32_t n, int32_t* new_page, cudaStream_t stream);
+
+/*
+ * Compact: the pages in use (use > 0) move to the front of dst's pools, in the
+ * order of their ids; dst's table and counts say what src's said, by the new
+ * ids.  dst may be src (the same pools, table and counts): then pages whose id
+ * is below the number of pages in use stay, and the others go, in order, to the
+ * free pages below it, so pages [n_used, num_pages) are free afterwards.  Else
+ * dst's memory must not overlap src's, src is left as it is, and dst has pools of
+ * the same kinds, as many rows and entries per row, and num_pages of its own; a
+ * page that does not fit gets -1 in table and new_id, and DSV4SA_ERR_NO_PAGES is
+ * set on the device.  dst pages past the used ones are not written.
+ *   new_id   device int32 [src num_pages]: the page's new id, -1 for a free page
+ *   n_used   device int32 [1]: pages in use
+ */
+DSV4SA_API int dsv4sa_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* dst, int32_t* new_id,
+                                    int32_t* n_used, cudaStream_t stream);
+
+/*
+ * RMSNorm with the residual's addition and an output in E4M3 with block scales
+ * ([V4] §2.5 RMSNorm, §3.4 act_quant_kernel).  Per row of `dim` BF16 values:
+ *   s = x + residual (fp32),  y = s / sqrt(mean(s^2) + eps) * norm_w  (fp32)
+ * and per `group` consecutive values of y: amax = max(max |y|, 1e-4), scale =
+ * amax * fp32(1/448), codes = E4M3 round-to-nearest-even of clamp(y / scale).
+ * With group 64 and dim 128 the outputs are dsv4sa_indexer_logits's q_fp8 and
+ * q_scale (n = T * Hi rows).  A row whose squares leave the fp32 range, or that
+ * holds a NaN, has no defined codes.
+ *   x, residual   bf16, rows x_stride / residual_stride values apart, 16-byte
+ *                 aligned, strides multiples of 8; residual may be null (s = x)
+ *   norm_w        device fp32 [dim], 16-byte aligned
+ *   residual_out  optional bf16 [n][dim]: s rounded to BF16; may be residual or x
+ *                 itself when that is [n][dim] without gaps
+ *   y             optional bf16 [n][dim]: y rounded to BF16
+ *   codes, scale  optional, together: uint8 [n][dim] and fp32 [n][dim / group]
+ *   dim           a multiple of 8 and, with codes, of group; <= DSV4SA_MAX_NORM_DIM
+ *   group         64 or 128
+ * At least one output is given; other outputs must not overlap the inputs.
+ */
+DSV4SA_API int dsv4sa_rmsnorm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                    const float* norm_w, float eps, int32_t n, int32_t dim, int32_t group,
+                                    void* residual_out, void* y, uint8_t* codes, float* scale, cudaStream_t stream);
 
 /*
  * The compressor's rotate path into an FP4 key pool ("DeepSeek-V4 全面解读"
@@ -537,8 +666,9 @@ DSV4SA_API int dsv4sa_selftest_wait_timeout(int32_t* result, cudaStream_t stream
 
 /* Synchronise `stream`, then read and clear the device error words of the
  * current device.  Returns DSV4SA_OK, DSV4SA_ERR_INDEX_OOB,
- * DSV4SA_ERR_DEVICE_TIMEOUT or DSV4SA_ERR_CUDA; `bits_out` (optional) receives
- * the raw bits (1 = index/page out of range, 2 = wait timeout). */
+ * DSV4SA_ERR_DEVICE_TIMEOUT, DSV4SA_ERR_NO_PAGES or DSV4SA_ERR_CUDA; `bits_out`
+ * (optional) receives the raw bits (1 = index/page out of range, 2 = wait
+ * timeout, 4 = no free page). */
 DSV4SA_API int dsv4sa_check_errors(cudaStream_t stream, uint32_t* bits_out);
 
 /*

@@ -753,3 +753,123 @@ def key_write_fp4_rotated(pool: dict, page_table_row, entries, key_bf16_bits) ->
     """The compressor's rotate path into an FP4 key pool (P1 §2.9 step 7): each
     key rotated (``hadamard_rotate_to_bf16``), then written as ``key_write_fp4``."""
     key_write_fp4(pool, page_table_row, entries, hadamard_rotate_to_bf16(np.asarray(key_bf16_bits, np.uint16)))
+
+
+# ---------------------------------------------------------------- FP4 KV cache
+# The KV rows in the format of the FP4 keys (P1 §3.5; P3: E2M1 values, one E8M0
+# scale per 32), the rope part BF16 as in the FP8 pool (P2 概念5).  Logical layout:
+#   nope_codes uint8 [P, 64, 448] -- one E2M1 code per value in the low 4 bits,
+#   nope_e8m0  uint8 [P, 64, 14], rope_bits uint16 [P, 64, 64].
+# A block that holds an infinity or a NaN is stored as codes 0 with the scale
+# byte 0xFF (the format's NaN): all its values read as NaN.
+
+def kv_write_fp4(pool: dict, page_table_row, entries, kv_bf16_bits) -> None:
+    """Write rows into an FP4 KV pool in place (fp4_quantize of the 448 nope values)."""
+    pages, slots = _locate(page_table_row, entries)
+    for r, (pg, sl) in enumerate(zip(pages, slots)):
+        bits = np.asarray(kv_bf16_bits[r], dtype=np.uint16)
+        blocks = bits[:NOPE].reshape(-1, FP4_BLOCK)
+        finite = np.all((blocks & 0x7F80) != 0x7F80, axis=1)
+        codes, e8m0 = fp4_quantize(np.where(finite[:, None], blocks, 0).astype(np.uint16).reshape(-1))
+        pool["nope_codes"][pg, sl] = codes
+        pool["nope_e8m0"][pg, sl] = np.where(finite, e8m0, 0xFF).astype(np.uint8)
+        pool["rope_bits"][pg, sl] = bits[NOPE:]
+
+
+def kv_rows_fp4(pool: dict, page_table_row, entries) -> np.ndarray:
+    """Dequantised FP4 KV rows [n, 512] in fp64."""
+    pages, slots = _locate(page_table_row, entries)
+    nope = fp4_dequantize(pool["nope_codes"][pages, slots], pool["nope_e8m0"][pages, slots])
+    return np.concatenate([nope, bf16_decode(pool["rope_bits"][pages, slots])], axis=1)
+
+
+def gather_rows_fp4(idx_c, comp_pool, comp_pt_row, idx_w, win_pool, win_pt_row) -> np.ndarray:
+    """gather_rows over FP4 pools."""
+    parts = [np.zeros((0, HEAD_DIM))]
+    for idx, pool, pt in ((idx_c, comp_pool, comp_pt_row), (idx_w, win_pool, win_pt_row)):
+        if idx is None:
+            continue
+        i = np.asarray(idx, np.int64)
+        i = i[i >= 0]
+        if i.size:
+            parts.append(kv_rows_fp4(pool, pt, i))
+    return np.concatenate(parts, axis=0)
+
+
+# ---------------------------------------------------------------- RMSNorm with a quantised output
+
+def rms_norm_quant(x_bf16_bits, residual_bf16_bits, weight, eps: float, group: int) -> dict:
+    """P1 §2.5 then §3.4 in fp64: s = x (+ residual), y = rms_norm(s), per block of
+    `group` values scale = max(amax, 1e-4) / 448 and z = y / scale, the value whose
+    nearest E4M3 code the output holds.  Returns s, y, scale, z."""
+    s = bf16_decode(x_bf16_bits)
+    if residual_bf16_bits is not None:
+        s = s + bf16_decode(residual_bf16_bits)
+    y = rms_norm(s, weight, eps)
+    blocks = y.reshape(*y.shape[:-1], -1, group)
+    scale = np.maximum(np.abs(blocks).max(axis=-1), AMAX_FLOOR) / FP8_MAX
+    return {"s": s, "y": y, "scale": scale, "z": (blocks / scale[..., None]).reshape(y.shape)}
+
+
+# ---------------------------------------------------------------- pages of a cache
+
+def use_counts(table, num_pages: int) -> np.ndarray:
+    """How many table entries hold each page (P2 概念5: a paged pool)."""
+    t = np.asarray(table).reshape(-1)
+    return np.bincount(t[t >= 0], minlength=num_pages).astype(np.int32)
+
+
+def cache_fork(table, use, pools, src, dst, length) -> np.ndarray:
+    """Fork rows in place, one after the other: dst[i] gets the full pages of
+    src[i]'s first length[i] entries, shared, and a copy of the slots of a last
+    page that is not full in the lowest free page.  pools: logical arrays
+    [P, 64, ...].  Returns the new pages (-1: none needed, -2: none left)."""
+    table_in, taken = table.copy(), []
+    new = np.full(len(src), -1, np.int32)
+    for i, (a, b, n) in enumerate(zip(src, dst, length)):
+        full, slots = divmod(int(n), PAGE)
+        if slots:
+            free = np.flatnonzero(use == 0)
+            if free.size == 0:
+                new[i] = -2
+                continue
+            new[i] = free[0]
+            use[free[0]] = 1
+            taken.append((table_in[a, full], free[0], slots))
+        table[b] = -1
+        for j in range(full):
+            table[b, j] = table_in[a, j]
+            use[table_in[a, j]] += 1
+        if slots:
+            table[b, full] = new[i]
+    for old, page, slots in taken:
+        for p in pools:
+            p[page, :slots] = p[old, :slots]
+    return new
+
+
+def cache_release(table, use, rows) -> None:
+    """Release rows in place."""
+    for r in rows:
+        if r < 0:
+            continue
+        for j, page in enumerate(table[r]):
+            if page >= 0:
+                use[page] -= 1
+                table[r, j] = -1
+
+
+def cache_compact_ids(use, in_place: bool) -> np.ndarray:
+    """New ids of the pages in use (-1 for free ones): their rank, or, in place,
+    their own id below the number in use, and the free ids below it, in order,
+    for the rest."""
+    used = np.flatnonzero(np.asarray(use) > 0)
+    new_id = np.full(len(use), -1, np.int32)
+    if not in_place:
+        new_id[used] = np.arange(used.size)
+        return new_id
+    stay = used[used < used.size]
+    new_id[stay] = stay
+    holes = [i for i in range(used.size) if use[i] == 0]
+    new_id[used[used >= used.size]] = holes
+    return new_id
