@@ -15,24 +15,28 @@
 //
 // Pipeline of a CTA.  The valid rows of the lists are packed -- J is a multiset,
 // their order is free -- into chunks of 128, so -1 entries cost no tensor work:
-//   gather warps (8): index -> page id -> row, 256 positions at a time, the valid
-//     ones appended to a ring; a chunk's rows (16-byte pieces, two threads a row)
-//     are loaded into registers while the tensor core works on the chunk before,
-//     then widened to BF16 and stored in the 128 x 512 tile, 128 dims at a time,
-//     each as soon as the previous chunk's PV has read those dims.
-//   MMA thread: S^T = KV . Q^T (M = 128 rows, N = HN, K = 512), 128 dims at a time
-//     as they arrive; then O^T += V^T . P^T (M = 128 dims x 4, N = HN, K = 128): the
-//     tile is read K-major for S and MN-major for PV.
-//   softmax warps (8): thread = row, half of the heads.  P in BF16 against a max
+//   gather warps (16): index -> page id -> row, 256 positions at a time, the valid
+//     ones appended to a ring; a chunk's rows (four threads a row) are loaded into
+//     registers while the chunk before is worked on, then widened to BF16 and
+//     stored in the 128 x 512 tile (128-byte swizzle) when its PV has read it.
+//   MMA warp: S^T = KV . Q^T (M = 128 rows, N = HN, K = 512), then O^T += V^T . P^T
+//     (M = 128 dims x 4, N = HN, K = 128): the tile is read K-major for S and
+//     MN-major for PV.
+//   softmax warps (8): thread = row, half of the heads.  P is BF16 against a max
 //     that is only moved (and O rescaled) when a score passes it by 2^8: a vote
-//     replaces the max's reduction in nearly every chunk but the first.  The
-//     sum of the probabilities stays with its row's thread until the
-//     end.  Then the output is scaled, rotated back and written from TMEM while
-//     the next item's S runs.
-// Widening is exact: a code's BF16 bits are looked up (two byte permutations for
-// four codes) and multiplied by the power of two in BF16.  P is the one operand
-// rounded (BF16, 2^-9 of a probability); S, O, maxima, sums and the partial
-// results that a cluster exchanges are fp32.
+//     replaces the max's reduction in nearly every chunk but the first.  The sum
+//     of the probabilities stays with its row's thread until the end.  At an
+//     item's end these warps write the output while the next item's first chunk
+//     is gathered and scored.
+// What bounds it: shared memory, and the hand-overs.  An MMA of M = 128, N = 64, K = 16
+// reads 6 KB and takes 48 cycles, the 128 bytes a clock of shared memory (measured),
+// so while MMAs run other accesses hardly proceed, and the phases of a chunk (3072
+// cycles of MMAs, 1024 of stores) follow one another however they are arranged:
+// handing the tile over by quarters (9900 cycles a chunk, each wait draining the
+// tensor pipe) and two tiles of 64 rows in turn with M = 64 (2 x 5400) were slower.
+// Widening is exact (see widen8).  P is the one operand rounded (BF16, 2^-8 of a
+// probability at most); S, O, maxima, sums and the partial results that a cluster
+// exchanges are fp32.
 #include "attn_common.cuh"
 
 namespace dsv4sa {
@@ -40,14 +44,22 @@ namespace {
 
 using namespace attn;
 
-constexpr int kComputeThreads = 256;     // warps 0-7
-constexpr int kGatherThreads = 256;      // warps 8-15
-constexpr int kThreads4 = kComputeThreads + kGatherThreads + 32;   // warp 16: MMA
-constexpr int kRing = 512;               // located rows waiting for a chunk
+constexpr int kComputeThreads = 256;     // warps 0-7: softmax, output
+constexpr int kGatherThreads = 512;      // warps 8-23
+constexpr int kMmaWarp = 24;
+constexpr int kThreads4 = kComputeThreads + kGatherThreads + 128;   // the last warpgroup: one MMA warp
+constexpr int kLocate = 256;             // list positions looked up at a time
+constexpr int kRing = 512;               // located rows waiting for a chunk (fewer than 128 + 256)
 constexpr int kRun = 32;                 // list positions a CTA of a cluster takes in a row
 constexpr int kFp4RopeOff = 14336;       // KV_FP4 page layout (see dsv4sa.h)
 constexpr int kFp4ScaleOff = 22528;
 constexpr float kSlack = 8.f;            // log2 units a score may pass the max in use by
+constexpr int kLastChunk = 256;          // meta: rows of the chunk (<= 128), and this for an item's last
+// Registers per thread (setmaxnreg): the launch gives 896 x 72 = 64512, the three
+// kinds of warpgroup then hold 256 x 96 + 512 x 64 + 128 x 56 = 64512.
+constexpr int kRegsCompute = 96, kRegsGather = 64, kRegsMma = 56;
+static_assert(kComputeThreads * kRegsCompute + kGatherThreads * kRegsGather + 128 * kRegsMma <= kThreads4 * 72,
+              "the register shares fit in the launch's");
 
 constexpr uint32_t kBarCompute4 = 1;     // named barriers
 constexpr uint32_t kBarGather4 = 2;
@@ -56,7 +68,7 @@ template <int HN>
 struct Smem4 {
   static constexpr int kKv = 0;
   static constexpr int kQ = kKvBytes;                    // 8 column blocks x HN rows x 128 B
-  static constexpr int kP = kQ + 8 * HN * 128;           // 128 rows x 128 B, or 2 blocks x HN rows x 128 B
+  static constexpr int kP = kQ + 8 * HN * 128;           // 128 rows x 128 B, or 2 blocks x HN rows x 128 B; output staging
   static constexpr int kTiles = kP + kRows * 128;        // end of the tiles (the merge may use all of them)
   static constexpr int kRing_ = kTiles;                  // uint64 [kRing]
   static constexpr int kRed = kRing_ + kRing * 8;        // float [HN][4]
@@ -64,44 +76,59 @@ struct Smem4 {
   static constexpr int kAlpha = kM + HN * 4;
   static constexpr int kFac = kAlpha + HN * 4;           // float [kMaxClusterSplits][HN]
   static constexpr int kMl = kFac + kMaxClusterSplits * HN * 4;   // float2 [kMaxClusterSplits][HN]
-  static constexpr int kCnt = kMl + kMaxClusterSplits * HN * 8;   // int [8]
-  static constexpr int kMeta = kCnt + 32;                // int [2]
+  static constexpr int kCnt = kMl + kMaxClusterSplits * HN * 8;   // int [16]
+  static constexpr int kMeta = kCnt + 64;                // int [4]
   static constexpr int kBar = kMeta + 16;                // barriers, see below
-  static constexpr int kTmem = kBar + 17 * 8 + 8;
+  static constexpr int kTmem = kBar + 13 * 8 + 8;
   static constexpr int kBytes = kTmem + 16;
 };
 
-// 32 E2M1 codes (16 bytes) times a power of two (BF16, in both halves) -> 32 BF16
-// values, out[w] = values 8 w .. 8 w + 7.
-__device__ __forceinline__ void widen32(const uint4 codes, uint32_t scale2, uint4* out) {
-  const uint32_t w4[4] = {codes.x, codes.y, codes.z, codes.w};
-  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&scale2);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = w4[i];
-    const uint32_t sel = w & 0x77777777u, sel2 = sel >> 16;
-    // BF16 of 0, 0.5, 1, 1.5, 2, 3, 4, 6: high bytes, then low bytes
-    const uint32_t h0 = __byte_perm(0x3F3F3F00u, 0x40404040u, sel), l0 = __byte_perm(0xC0800000u, 0xC0804000u, sel);
-    const uint32_t h1 = __byte_perm(0x3F3F3F00u, 0x40404040u, sel2), l1 = __byte_perm(0xC0800000u, 0xC0804000u, sel2);
-    uint32_t v[4] = {__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
-                     __byte_perm(l1, h1, 0x7362)};
-    v[0] |= ((w << 12) & 0x8000u) | ((w << 24) & 0x80000000u);
-    v[1] |= ((w << 4) & 0x8000u) | ((w << 16) & 0x80000000u);
-    v[2] |= ((w >> 4) & 0x8000u) | ((w << 8) & 0x80000000u);
-    v[3] |= ((w >> 12) & 0x8000u) | (w & 0x80000000u);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v[j]), s);
-      v[j] = *reinterpret_cast<const uint32_t*>(&x);
-    }
-    out[i] = make_uint4(v[0], v[1], v[2], v[3]);
-  }
+// The block scale 2^(b - 127) for widen8: `first` = 2^min(b - 1, 127) in BF16, in
+// both halves (the codes are placed 2^126 too small), `rest` = what is left of it.
+// Byte 255 is NaN.
+struct BlockScale {
+  uint32_t first;
+  uint32_t more;   // exponent still to be added: b - 128 when that is positive
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t b) {
+  const uint32_t e = min(b + 126u, 254u);                 // b = 0: 2^-1
+  const uint32_t h = b == 255u ? 0x7FC0u : e << 7;
+  return BlockScale{h | (h << 16), b > 128u && b != 255u ? b - 128u : 0u};
 }
 
-// 2^(b - 127) in BF16, in both halves; 255 is NaN.
-__device__ __forceinline__ uint32_t e8m0_bf16x2(uint32_t b) {
-  const uint32_t h = b == 0u ? 0x0040u : (b == 255u ? 0x7FC0u : b << 7);
-  return h | (h << 16);
+// Eight E2M1 codes -> eight BF16 values.  The two codes of a byte become one
+// register: a multiplication by 2^6 + 2^18 puts the three magnitude bits of either
+// where BF16 keeps the last two exponent bits and the first mantissa bit, one by
+// 2^12 + 2^24 their signs; as a BF16 number that is the value times 2^-126 (a
+// magnitude of 1, 0.5, is subnormal there as here), and the product with the
+// scale restores it exactly.  Half of the work is on the FMA pipe, so it does not
+// all queue for the ALU (a table by byte permutations took 2.1 times as long).
+__device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t first) {
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&first);
+  uint32_t v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t byte = __byte_perm(w, 0u, 0x4440 + j);
+    const uint32_t x = ((byte * 0x00040040u) & 0x01C001C0u) | ((byte * 0x01001000u) & 0x80008000u);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), s);
+    v[j] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+// Eight values times 2^more (a block of magnitudes above 12: rarely called).
+__device__ __forceinline__ uint4 scale_up(uint4 v, uint32_t more) {
+  // in two steps: 2^more may pass BF16's range although the product does not
+  const uint32_t a = min(more, 64u), c = more - a;
+  const uint32_t ha = (127u + a) << 7, hc = (127u + c) << 7;
+  const uint32_t fa = ha | (ha << 16), fc = hc | (hc << 16);
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&w[j]), *reinterpret_cast<const __nv_bfloat162*>(&fa));
+    x = __hmul2(x, *reinterpret_cast<const __nv_bfloat162*>(&fc));
+    w[j] = *reinterpret_cast<uint32_t*>(&x);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ bool any_of(bool v, uint32_t id, uint32_t n) {
@@ -122,6 +149,69 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t 
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// A contiguous range into L2 (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// tcgen05.mma and its commit by one elected lane of a converged warp: the
+// operands then stay in uniform registers (60 cycles an MMA against 68 to 80 from
+// a single-lane branch).
+// The low words of the descriptors (address and leading offset) vary, the high words
+// are the same for every operand here.
+__device__ __forceinline__ void mma_f16_elect(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+
+// mbar_wait without a function call: a kernel that moves registers between its
+// warpgroups cannot make one (the register allocation fails).
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_test_parity(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_test_parity(bar, parity)) return true;
+    if ((it & 63u) == 0u && global_timer_ns() - t0 > kWaitLimitNs) {
+      raise_error(kErrTimeout);
+      return false;
+    }
+  }
+}
+// The whole (converged) warp waits and stays converged: every branch is on a vote.
+// (Were one lane to wait for the others, the warp would go on in two parts, and each
+// elect.sync after it would have to bring them together: 280 cycles an MMA.)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_test_parity(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_test_parity(bar, parity))) return true;
+    if ((it & 63u) == 0u && __any_sync(0xffffffffu, global_timer_ns() - t0 > kWaitLimitNs)) {
+      raise_error(kErrTimeout);
+      return false;
+    }
+  }
+}
 
 // Positions of a list of n that CTA r of CS takes, and the k-th of them.
 __device__ __forceinline__ int share_of(int n, int r, int CS) {
@@ -133,8 +223,11 @@ __device__ __forceinline__ int share_at(int k, int r, int CS) { return ((k / kRu
 template <int HN>
 __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const AttnParams p, int groups) {
   using S = Smem4<HN>;
+  // 128-byte swizzled tiles need 1024-byte aligned bases.  An offset from the array (not
+  // a rounded address) lets the compiler see shared memory: 32-bit addresses, no
+  // generic loads.
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* kv = smem + S::kKv;
   uint8_t* qs = smem + S::kQ;
   uint8_t* ps = smem + S::kP;
@@ -146,16 +239,16 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   float2* mlr = reinterpret_cast<float2*>(smem + S::kMl);
   int* wcnt = reinterpret_cast<int*>(smem + S::kCnt);
   volatile int* meta = reinterpret_cast<volatile int*>(smem + S::kMeta);
-  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + S::kBar);   // [4]: 128 dims of the chunk are in the tile
-  uint64_t* bar_free = bar_full + 4;     // [4]: ... have been read by PV
-  uint64_t* bar_tok = bar_full + 8;      // [2]: a chunk's (or an item's end's) meta is written
-  uint64_t* bar_s = bar_full + 10;       // S is complete
-  uint64_t* bar_p = bar_full + 11;       // P is written
-  uint64_t* bar_o = bar_full + 12;       // every PV of the item is complete
-  uint64_t* bar_q = bar_full + 13;       // the item's Q is in place
-  uint64_t* bar_item = bar_full + 14;    // the end of the item has been seen
-  uint64_t* bar_recv = bar_full + 15;    // merge: the other splits' partials landed
-  uint64_t* bar_ml = bar_full + 16;      // merge: the other splits' (m, l) landed
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + S::kBar);   // the chunk is in the tile
+  uint64_t* bar_free = bar_full + 1;     // the tile has been read by PV
+  uint64_t* bar_tok = bar_full + 2;      // [4]: a chunk's (or an item's end's) meta is written
+  uint64_t* bar_s = bar_full + 6;        // S is complete
+  uint64_t* bar_p = bar_full + 7;        // P is written
+  uint64_t* bar_o = bar_full + 8;        // every PV of the item is complete
+  uint64_t* bar_q = bar_full + 9;        // the item's Q is in place
+  uint64_t* bar_item = bar_full + 10;    // the end of the item has been seen
+  uint64_t* bar_recv = bar_full + 11;    // merge: the other splits' partials landed
+  uint64_t* bar_ml = bar_full + 12;      // merge: the other splits' (m, l) landed
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::kTmem);
 
   constexpr int HW = HN / 2;             // heads of a softmax thread
@@ -171,14 +264,11 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   const int slot_bytes = slice * HN * 4;
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar_full + i, kGatherThreads / 32);
-      mbar_init(bar_free + i, 1);
-    }
-    mbar_init(bar_tok, 1);
-    mbar_init(bar_tok + 1, 1);
+    mbar_init(bar_full, kGatherThreads / 32);
+    mbar_init(bar_free, 1);
     mbar_init(bar_s, 1);
     mbar_init(bar_p, kComputeThreads / 32);
+    for (int i = 0; i < 4; ++i) mbar_init(bar_tok + i, 1);
     mbar_init(bar_o, 1);
     mbar_init(bar_q, kComputeThreads / 32);
     mbar_init(bar_item, 1);
@@ -187,7 +277,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     fence_mbar_init();
     if (CS > 1) mbar_arrive_expect_tx(bar_recv, static_cast<uint32_t>((CS - 1) * slot_bytes));
   }
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_holder, kTmemCols);
     tmem_relinquish();
   }
@@ -202,34 +292,34 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   const uint32_t tmem = *tmem_holder;
   bool ok = true;                        // no wait of this thread has run out
 
-  if (warp >= 8 && warp < 16) {
+  if (warp >= 8 && warp < kMmaWarp) {
     // =========================== gather warps ===========================
     // A wait that runs out is not repeated: the loop, whose length the lists
     // alone decide, goes on without waiting.
+    regs_dec<kRegsGather>();
     const int gt = tid - kComputeThreads;
-    const int row = gt >> 1, half = gt & 1;
+    const int row = gt >> 2, piece = gt & 3;
     bool waited = !p.early_window;
-    int chunk = 0, token = 0, n_item = 0;
-    for (int item = item0; item < n_items; item += item_step, ++n_item) {
+    int chunk = 0, token = 0;
+    int head = 0;                               // ring: first located row not yet loaded
+    const int cw = share_of(p.kw, crank, CS), total = cw + share_of(p.kc, crank, CS);   // this CTA's positions of an item
+    for (int item = item0, n_item = 0; item < n_items; item += item_step, ++n_item) {
       const int t = item / groups;
       const int seq = __ldg(p.q_seq + t);
-      const int32_t* cpt = p.comp_pt + static_cast<int64_t>(seq) * p.comp_pt_stride;
-      const int32_t* wpt = p.win_pt + static_cast<int64_t>(seq) * p.win_pt_stride;
-      const int32_t wpos = p.idx_w || p.kw == 0 ? 0 : __ldg(p.win_pos + t);
-      const int cw = share_of(p.kw, crank, CS), total = cw + share_of(p.kc, crank, CS);
-      int cursor = 0, head = 0, count = 0;      // positions located; ring state
+      const int wpos = p.idx_w || p.kw == 0 ? 0 : __ldg(p.win_pos + t);
+      int cursor = 0, count = 0;                // positions looked up, rows in the ring
       while (true) {
-        // ---- locate rows until a chunk is full or the lists are done
+        // ---- enough rows for a chunk, or the end of the lists
         while (count < kRows && cursor < total) {
           if (!waited && cursor == cw) {
             if (count > 0) break;               // the window's rows go first, before idx_c is there
             griddep_wait();
             waited = true;
           }
-          const int end = waited ? total : cw;
+          const int end = min(cursor + kLocate, waited ? total : cw);
           const int pos = cursor + gt;
           uint64_t rp = 0;
-          if (pos < end) {
+          if (gt < kLocate && pos < end) {
             const bool window = pos < cw;
             const int j = share_at(window ? pos : pos - cw, crank, CS);
             int32_t e;
@@ -242,15 +332,16 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
               e = pw < 0 ? -1 : static_cast<int32_t>(p.win_ring > 0 ? pw % p.win_ring : pw);
             }
             if (e >= 0) {
-              const int64_t lim = static_cast<int64_t>(window ? p.win_pt_stride : p.comp_pt_stride) * 64;
+              const int stride = window ? p.win_pt_stride : p.comp_pt_stride;
+              const int32_t* pt = (window ? p.win_pt : p.comp_pt) + static_cast<int64_t>(seq) * stride;
               const int64_t np = window ? p.win_num_pages : p.comp_num_pages;
-              const int32_t page = e < lim ? __ldg((window ? wpt : cpt) + (e >> 6)) : -1;
+              const int32_t page = (e >> 6) < stride ? __ldg(pt + (e >> 6)) : -1;
               if (page < 0 || page >= np) {
                 raise_error(kErrIndex);
               } else {
                 const uint8_t* base = window ? p.win_base : p.comp_base;
-                const int64_t stride = window ? p.win_page_stride : p.comp_page_stride;
-                rp = reinterpret_cast<uint64_t>(base + page * stride) | static_cast<uint64_t>(e & 63);
+                rp = reinterpret_cast<uint64_t>(base + page * (window ? p.win_page_stride : p.comp_page_stride)) |
+                     static_cast<uint64_t>(e & 63);
               }
             }
           }
@@ -260,134 +351,151 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
           named_barrier_sync(kBarGather4, kGatherThreads);
           int before = 0, all = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < kLocate / 32; ++i) {
             const int n = wcnt[i];
             before += i < w ? n : 0;
             all += n;
           }
-          if (rp != 0)
-            ring[(head + count + before + __popc(bits & ((1u << lane) - 1u))) & (kRing - 1)] = rp;
+          if (rp != 0) ring[(head + count + before + __popc(bits & ((1u << lane) - 1u))) & (kRing - 1)] = rp;
           named_barrier_sync(kBarGather4, kGatherThreads);
           count += all;
-          cursor = min(cursor + kGatherThreads, end);
+          cursor = end;
         }
         const int n = min(count, kRows);
         if (n == 0) break;
-        // ---- load: thread (row, half) takes the 16-byte code pieces 2 j + half (one
-        // scale block each), four rope pieces and the scale row; rows past n are zero
-        uint4 code[7], rope[4], scl;
+        // ---- load: the four threads of a row take its 16-byte code pieces 4 b + piece
+        // (a scale block each) of the first three quarters, 8 bytes of codes and 32 of
+        // rope values of the last; rows past n are zero
+        uint4 code[3], rope[2], scl;
+        uint2 code3;
         {
           const bool in = row < n;
           const uint64_t rp = in ? ring[(head + row) & (kRing - 1)] : 0;
           const uint8_t* page = reinterpret_cast<const uint8_t*>(rp & ~uint64_t(63));
           const int slot = static_cast<int>(rp & 63);
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          const uint4* cp = reinterpret_cast<const uint4*>(page + slot * 224) + half;
-          const uint4* rpp = reinterpret_cast<const uint4*>(page + kFp4RopeOff + slot * 128) + 4 * half;
+          const uint8_t* cp = page + slot * 224;
+          const uint4* rpp = reinterpret_cast<const uint4*>(page + kFp4RopeOff + slot * 128) + 2 * piece;
           scl = in ? __ldg(reinterpret_cast<const uint4*>(page + kFp4ScaleOff + slot * 16)) : zero;
 #pragma unroll
-          for (int j = 0; j < 7; ++j) code[j] = in ? __ldg(cp + 2 * j) : zero;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) rope[j] = in ? __ldg(rpp + j) : zero;
+          for (int b = 0; b < 3; ++b) code[b] = in ? __ldg(reinterpret_cast<const uint4*>(cp) + 4 * b + piece) : zero;
+          code3 = in ? __ldg(reinterpret_cast<const uint2*>(cp + 192) + piece) : make_uint2(0u, 0u);
+          rope[0] = in ? __ldg(rpp) : zero;
+          rope[1] = in ? __ldg(rpp + 1) : zero;
         }
         head += n;
         count -= n;
-        const uint32_t sb[4] = {scl.x, scl.y, scl.z, scl.w};
-        // ---- 128 dims at a time, as the previous chunk's PV has read them
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (chunk > 0) {
-            bool good = true;
-            if (ok && lane == 0) good = mbar_wait(bar_free + b, (chunk - 1) & 1);
-            ok = __shfl_sync(0xffffffffu, good ? 1 : 0, 0) != 0 && ok;
-          }
-          if (b == 0 && gt == 0) {        // the slot's last token has been read: its chunk's PV was issued
-            meta[token & 1] = n;
-            mbar_arrive(bar_tok + (token & 1));
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int j = 2 * b + i;       // column block
-            uint8_t* blk = kv + j * kKvBlock;
-            if (j < 7) {
-              uint4 v[4];                  // scale byte 2 j + half of the row
-              widen32(code[j], e8m0_bf16x2((sb[j >> 1] >> (16 * (j & 1) + 8 * half)) & 0xFFu), v);
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4*>(blk + sw128_offset(row, static_cast<uint32_t>(4 * half + x))) = v[x];
-            } else {
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4*>(blk + sw128_offset(row, static_cast<uint32_t>(4 * half + x))) = rope[x];
-            }
-          }
-          fence_proxy_async_smem();        // the tile is read by the tensor core
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_full + b);
+        // no row of the item is left to come: the softmax may replace Q once this chunk's S is complete
+        const bool last = count == 0 && cursor >= total;
+        // ---- into the tile, when the previous chunk's PV has read it
+        if (chunk > 0) {
+          if (gt == 0 && ok) ok = bar_wait(bar_free, (chunk - 1) & 1);
+          named_barrier_sync(kBarGather4, kGatherThreads);
         }
+        const uint32_t sw[4] = {scl.x, scl.y, scl.z, scl.w};
+#pragma unroll
+        for (int b = 0; b < 3; ++b) {
+          // 32 values: units 4 (piece & 1) + x of column block 2 b + (piece >> 1).  The
+          // upper two pieces take x in the order 2, 3, 0, 1, so that the eight lanes of
+          // two rows hit eight different bank groups.
+          const BlockScale bs = block_scale((sw[b] >> (8 * piece)) & 0xFFu);
+          uint8_t* blk = kv + (2 * b + (piece >> 1)) * kKvBlock;
+          const uint32_t c4[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = piece >= 2 ? c4[i ^ 2] : c4[i];
+            const uint32_t x = static_cast<uint32_t>(i) ^ (piece & 2);
+            uint4 v = widen8(w, bs.first);
+            if (bs.more) v = scale_up(v, bs.more);
+            *reinterpret_cast<uint4*>(blk + sw128_offset(row, static_cast<uint32_t>(4 * (piece & 1)) + x)) = v;
+          }
+        }
+        {
+          const BlockScale bs = block_scale((sw[3] >> (8 * (piece >> 1))) & 0xFFu);
+          const uint32_t u = static_cast<uint32_t>(2 * piece);
+          uint4 v0 = widen8(code3.x, bs.first), v1 = widen8(code3.y, bs.first);
+          if (bs.more) {
+            v0 = scale_up(v0, bs.more);
+            v1 = scale_up(v1, bs.more);
+          }
+          *reinterpret_cast<uint4*>(kv + 6 * kKvBlock + sw128_offset(row, u)) = v0;
+          *reinterpret_cast<uint4*>(kv + 6 * kKvBlock + sw128_offset(row, u + 1)) = v1;
+          *reinterpret_cast<uint4*>(kv + 7 * kKvBlock + sw128_offset(row, u)) = rope[0];
+          *reinterpret_cast<uint4*>(kv + 7 * kKvBlock + sw128_offset(row, u + 1)) = rope[1];
+        }
+        fence_proxy_async_smem();          // the tile is read by the tensor core
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_full);
+        if (gt == 0) {                    // the meta slot's last token, four ago, has been read
+          meta[token & 3] = n | (last ? kLastChunk : 0);
+          mbar_arrive(bar_tok + (token & 3));
+        }
+        __syncwarp();
         ++chunk;
         ++token;
       }
-      // ---- the item's end; of items without rows, the end before it has been seen
+      // ---- the item's end, once the end before it has been seen
       if (gt == 0) {
-        if (n_item > 0 && ok) ok = mbar_wait(bar_item, (n_item - 1) & 1);
-        meta[token & 1] = -1;
-        mbar_arrive(bar_tok + (token & 1));
+        if (n_item > 0 && ok) ok = bar_wait(bar_item, (n_item - 1) & 1);
+        meta[token & 3] = -1;
+        mbar_arrive(bar_tok + (token & 3));
       }
+      __syncwarp();
       ++token;
     }
-  } else if (warp == 16) {
-    // =========================== MMA thread ===========================
-    if (lane == 0) {
+  } else if (warp >= kMmaWarp) {
+    // =========================== MMA warp ===========================
+    regs_dec<kRegsMma>();
+    if (warp == kMmaWarp) {
       const uint32_t idesc_s = make_idesc(kFmtBF16, kFmtBF16, 0, 0, 128, HN);
       const uint32_t idesc_o = make_idesc(kFmtBF16, kFmtBF16, 1, HN == 64 ? 1 : 0, 128, HN);
-      const uint64_t kvk = smem_desc_sw128(smem_u32(kv), 16, 1024), qk = smem_desc_sw128(smem_u32(qs), 16, 1024);
-      const uint64_t kvm = smem_desc_sw128(smem_u32(kv), kKvBlock, 1024);
+      const uint32_t hi = static_cast<uint32_t>(smem_desc_sw128(0, 16, 1024) >> 32);   // stride, version, swizzle
+      const uint32_t kvk = static_cast<uint32_t>(smem_desc_sw128(smem_u32(kv), 16, 1024));
+      const uint32_t qk = static_cast<uint32_t>(smem_desc_sw128(smem_u32(qs), 16, 1024));
+      const uint32_t kvm = static_cast<uint32_t>(smem_desc_sw128(smem_u32(kv), kKvBlock, 1024));
       // P: [row][64 heads] (N contiguous) for 64 heads, else [head][64 rows] x 2
-      const uint64_t pd = smem_desc_sw128(smem_u32(ps), HN == 64 ? kRows * 128 : 16, 1024);
+      const uint32_t pd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(ps), HN == 64 ? kRows * 128 : 16, 1024));
       int chunk = 0, token = 0, n_item = 0;
       for (int item = item0; item < n_items && ok; item += item_step, ++n_item) {
-        ok = mbar_wait(bar_q, n_item & 1);
+        ok = warp_wait(bar_q, n_item & 1);
         bool first = true;
         while (ok) {
-          ok = mbar_wait(bar_tok + (token & 1), (token >> 1) & 1);
+          ok = warp_wait(bar_tok + (token & 3), (token >> 2) & 1);
           if (!ok) break;
-          const int n = meta[token & 1];
+          const int word = meta[token & 3];
           ++token;
-          if (n < 0) break;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            ok = ok && mbar_wait(bar_full + b, chunk & 1);
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 8 * b; kk < 8 * b + 8; ++kk) {
-              const uint32_t ao = ((kk >> 2) * kKvBlock + (kk & 3) * 32) >> 4;
-              const uint32_t bo = ((kk >> 2) * (HN * 128) + (kk & 3) * 32) >> 4;
-              mma_f16(tmem + kColS, kvk + ao, qk + bo, idesc_s, kk > 0 ? 1u : 0u);
-            }
-          }
-          mma_commit(bar_s);
-          ok = ok && mbar_wait(bar_p, chunk & 1);
+          if (word < 0) break;
+          ok = warp_wait(bar_full, chunk & 1);
           tc_fence_after();
+#pragma unroll 1
+          for (int b = 0; b < 8; ++b) {    // not unrolled: 32 pairs of descriptors would not fit in registers
 #pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_elect(tmem + kColS, kvk + ((b * kKvBlock + kk * 32) >> 4), qk + ((b * HN * 128 + kk * 32) >> 4), hi, idesc_s,
+                            b > 0 || kk > 0 ? 1u : 0u);
+          }
+          mma_commit_elect(bar_s);
+          ok = ok && warp_wait(bar_p, chunk & 1);
+          tc_fence_after();
+#pragma unroll 1
           for (int mb = 0; mb < 4; ++mb) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t ao = (2 * mb * kKvBlock + kk * 2048) >> 4;
               const uint32_t bo = (HN == 64 ? kk * 2048 : (kk >> 2) * (HN * 128) + (kk & 3) * 32) >> 4;
-              mma_f16(tmem + kColO + mb * HN, kvm + ao, pd + bo, idesc_o, (!first || kk > 0) ? 1u : 0u);
+              mma_f16_elect(tmem + kColO + mb * HN, kvm + ((2 * mb * kKvBlock + kk * 2048) >> 4), pd + bo, hi, idesc_o,
+                            (!first || kk > 0) ? 1u : 0u);
             }
-            mma_commit(bar_free + mb);
           }
+          mma_commit_elect(bar_free);
           first = false;
           ++chunk;
         }
-        mma_commit(bar_o);
+        mma_commit_elect(bar_o);
       }
     }
-    __syncwarp();
   } else {
     // =========================== softmax warps ===========================
+    regs_inc<kRegsCompute>();
     const uint32_t g = warp & 3u, hh = warp >> 2;
     const int r = static_cast<int>(g * 32 + lane);          // row of the chunk, and TMEM lane
     const int hb = static_cast<int>(hh) * HW;               // first head of this thread
@@ -396,13 +504,17 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     // Q of an item -> swizzled K-major tile; heads past H are zero
     auto load_q = [&](int item) {
       const int t = item / groups, h0 = (item - t * groups) * HN;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q) + static_cast<int64_t>(t) * p.H * 64;
+      const int hreal = min(HN, p.H - h0);
+      const uint4* src = reinterpret_cast<const uint4*>(p.q) + (static_cast<int64_t>(t) * p.H + h0) * 64;
 #pragma unroll 4
-      for (int u = tid; u < HN * 64; u += kComputeThreads) {
-        const int h = u >> 6, v = u & 63;
-        cp_async16(qs + (v >> 3) * (HN * 128) + sw128_offset(h, v & 7), src + static_cast<int64_t>(min(h0 + h, p.H - 1)) * 64 + v,
-                   h0 + h < p.H ? 16u : 0u);
+      for (int i = 0; i < HN / 4; ++i) {
+        const int u = i * kComputeThreads + tid, h = u >> 6, v = u & 63;
+        cp_async16(qs + (v >> 3) * (HN * 128) + sw128_offset(h, v & 7), src + min(h, hreal - 1) * 64 + v, h < hreal ? 16u : 0u);
       }
+    };
+    auto q_to_l2 = [&](int item) {
+      const int t = item / groups, h0 = (item - t * groups) * HN;
+      prefetch_l2(p.q + (static_cast<int64_t>(t) * p.H + h0) * 512, static_cast<uint32_t>(min(HN, p.H - h0)) * 1024u);
     };
     auto q_ready = [&]() {
       cp_async_wait();
@@ -414,6 +526,8 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       load_q(item0);
       q_ready();
     }
+    if (tid < HN) m_used[tid] = -1e30f;
+    named_barrier_sync(kBarCompute4, kComputeThreads);
     int chunk = 0, token = 0, n_item = 0;
     bool alive = true;                                      // the same in all compute threads
     for (int item = item0; item < n_items; item += item_step, ++n_item) {
@@ -422,24 +536,24 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       float lsum[HW];
 #pragma unroll
       for (int i = 0; i < HW; ++i) lsum[i] = 0.f;
-      if (tid < HN) m_used[tid] = -1e30f;
-      bool have_o = false;
+      bool have_o = false, q_sent = CS > 1 || item + item_step >= n_items;   // the next item's Q is on its way
+      if (!q_sent && tid == 0) q_to_l2(item + item_step);
       while (true) {
         // ---- one thread waits for the chunk's S (or the item's end), the others at the barrier
         bool bad = false;
-        if (tid == 0 && alive) {
-          bad = !mbar_wait(bar_tok + (token & 1), (token >> 1) & 1);
-          if (!bad && meta[token & 1] >= 0) bad = !mbar_wait(bar_s, chunk & 1);
+        if (tid == 0) {
+          bad = !bar_wait(bar_tok + (token & 3), (token >> 2) & 1);
+          if (!bad && meta[token & 3] >= 0) bad = !bar_wait(bar_s, chunk & 1);
         }
-        alive = !any_of(bad, kBarCompute4, kComputeThreads) && alive;
+        alive = !any_of(bad, kBarCompute4, kComputeThreads);
         if (!alive) break;
-        const int n = meta[token & 1];
+        const int word = meta[token & 3];
         ++token;
-        if (n < 0) break;
+        if (word < 0) break;
         tc_fence_after();
         float sv[HW];
         tmem_load_cols<HW>(ta + kColS + hb, sv);
-        const bool rvalid = r < n;
+        const bool rvalid = r < (word & (kLastChunk - 1));
         float over = -INFINITY;
 #pragma unroll
         for (int i = 0; i < HW; i += 4) {
@@ -518,12 +632,15 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p);
         ++chunk;
+        if ((word & kLastChunk) != 0 && !q_sent) {          // the item's last S is complete: Q may be replaced
+          load_q(item + item_step);
+          q_sent = true;
+        }
       }
       if (!alive) break;
       // ---- the item's end: its last S is complete, so Q may be replaced
-      if (CS == 1 && item + item_step < n_items) load_q(item + item_step);
-      // per-head sums over the rows
-      {
+      if (!q_sent) load_q(item + item_step);
+      {                                  // per-head sums over the rows
         const float l = TransposeReduce<HW>::run(lsum, lane, 16u, OpAdd());
         constexpr int kRep = 32 / HW;
         if ((lane & (kRep - 1)) == 0) red[(hb + lane / kRep) * 4 + g] = l;
@@ -535,22 +652,18 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       named_barrier_sync(kBarCompute4, kComputeThreads);
       float m_mine = -1e30f, l_mine = 0.f;
       if (tid < HN) {
-        const float4 q = *reinterpret_cast<const float4*>(red + tid * 4);
         m_mine = m_used[tid];
+        const float4 q = *reinterpret_cast<const float4*>(red + tid * 4);
         l_mine = (q.x + q.y) + (q.z + q.w);
-      }
-      if (CS > 1) {
-        if (tid < HN) {
+        if (CS > 1) {
 #pragma unroll 1
           for (int o = 0; o < CS; ++o) {
             if (o == crank) continue;
             st_cluster_v2f32(cluster_map(smem_u32(mlr + crank * HN + tid), static_cast<uint32_t>(o)), m_mine, l_mine);
             mbar_arrive_remote(cluster_map(smem_u32(bar_ml), static_cast<uint32_t>(o)));
           }
-          ok = mbar_wait(bar_ml, 0) && ok;
+          ok = bar_wait(bar_ml, 0) && ok;
         }
-      }
-      if (tid < HN) {
         const float sink2 = tid < hreal ? __ldg(p.sink + h0 + tid) * kLog2e : -INFINITY;
         auto ml_of = [&](int c) { return c == crank ? make_float2(m_mine, l_mine) : mlr[c * HN + tid]; };
         float M = sink2;
@@ -572,49 +685,56 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
           p.lse[static_cast<int64_t>(t) * p.H + h0 + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
       }
       bool bad = false;
-      if (tid == 0) bad = !mbar_wait(bar_o, n_item & 1);
+      if (tid == 0) bad = !bar_wait(bar_o, n_item & 1);
       alive = !any_of(bad, kBarCompute4, kComputeThreads);      // also publishes the factors
       tc_fence_after();
       if (!alive) break;
-      if (tid == 0) mbar_arrive(bar_item);                      // the MMA thread has read the end's token, too
-      if (CS == 1 && item + item_step < n_items) q_ready();
+      if (tid == 0) mbar_arrive(bar_item);                      // the MMA warp has read the end's token, too
       if (CS > 1) break;                 // merged below, by all warps of the cluster
-      // ---- output: thread = dim, lanes (d, d + 1) pair up to store two values of a head
+      if (item + item_step < n_items) q_ready();
+      // ---- output, eight heads at a time: thread = dim, staged as [head][512] BF16 in
+      // the two P buffers in turn, stored 16 bytes a thread
       const float4* rrow = rope_row(p, t);
 #pragma unroll 1
-      for (int b = 0; b < 2; ++b) {
-        const int blk = static_cast<int>(hh) * 2 + b;
-        const int d = blk * 128 + r;
-        uint16_t* orow = p.out + (static_cast<int64_t>(t) * p.H + h0) * 512 + (d & ~1);
-        const bool rot = rrow != nullptr && d >= 512 - 64;      // warp-uniform
-        const float2 cs = rot ? __ldg(reinterpret_cast<const float2*>(rrow) + ((d - (512 - 64)) >> 1)) : make_float2(1.f, 0.f);
-#pragma unroll 1
-        for (int j0 = 0; j0 < HN; j0 += 16) {
-          float v[16];
+      for (int j0 = 0; j0 < hreal; j0 += 8) {
+        __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(ps + ((j0 >> 3) & 1) * 8192);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int blk = static_cast<int>(hh) * 2 + b;
+          const int d = blk * 128 + static_cast<int>(g * 32 + lane);
+          float v[8];
           if (have_o) {
-            tmem_load_cols<16>(ta + kColO + blk * HN + j0, v);
+            tmem_load_cols<8>(ta + kColO + blk * HN + j0, v);
           } else {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) v[x] = 0.f;
+            for (int x = 0; x < 8; ++x) v[x] = 0.f;
+          }
+          const float4 fa = *reinterpret_cast<const float4*>(fac + j0), fb = *reinterpret_cast<const float4*>(fac + j0 + 4);
+          const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] *= f[x];
+          if (rrow != nullptr && d >= 512 - 64) {               // warp-uniform: dims (d, d ^ 1) are a pair, lanes (l, l ^ 1)
+            const float2 cs = __ldg(reinterpret_cast<const float2*>(rrow) + ((d - (512 - 64)) >> 1));
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const float other = __shfl_xor_sync(0xffffffffu, v[x], 1);
+              v[x] = (lane & 1) ? fmaf(v[x], cs.x, -(other * cs.y)) : fmaf(v[x], cs.x, other * cs.y);
+            }
           }
 #pragma unroll
-          for (int x = 0; x < 16; x += 2) {
-            float a = v[x] * fac[j0 + x], c = v[x + 1] * fac[j0 + x + 1];
-            // even lanes take head x, odd lanes head x + 1, of both dims
-            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : c, 1);
-            float lo = (lane & 1) ? got : a, hi = (lane & 1) ? c : got;
-            if (rot) {
-              const float2 z = rotate_back(lo, hi, cs.x, cs.y);
-              lo = z.x;
-              hi = z.y;
-            }
-            const int h = j0 + x + static_cast<int>(lane & 1);
-            if (h < hreal) *reinterpret_cast<uint32_t*>(orow + static_cast<int64_t>(h) * 512) = pack_bf16x2(lo, hi);
-          }
+          for (int x = 0; x < 8; ++x) stage[x * 512 + d] = __float2bfloat16_rn(v[x]);
         }
+        named_barrier_sync(kBarCompute4, kComputeThreads);      // and the buffer before last has been read out
+        const uint4* src = reinterpret_cast<const uint4*>(stage);
+        uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(t) * p.H + h0 + j0) * 512);
+        const int units = min(8, hreal - j0) * 64;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (i * kComputeThreads + tid < units) dst[i * kComputeThreads + tid] = src[i * kComputeThreads + tid];
       }
+      if (tid < HN) m_used[tid] = -1e30f;                       // read above by the same thread
       tc_fence_before();                 // O has been read; the next item's PV follows its bar_p
-      named_barrier_sync(kBarCompute4, kComputeThreads);        // m_used, red and fac are free again
+      named_barrier_sync(kBarCompute4, kComputeThreads);        // m_used, red, fac and the P buffers are free again
     }
     ok = ok && alive;
   }
@@ -670,7 +790,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
                              cluster_map(smem_u32(bar_recv), static_cast<uint32_t>(o)));
       }
     }
-    ok = mbar_wait(bar_recv, 0) && ok;   // the other splits' slots have landed here
+    ok = bar_wait(bar_recv, 0) && ok;   // the other splits' slots have landed here
     cluster_arrive();                    // ... so their copies out of the senders are complete
     if (compute) {
       const float4* rrow = rope_row(p, t);
@@ -723,7 +843,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
