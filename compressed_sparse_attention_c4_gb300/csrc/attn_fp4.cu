@@ -54,6 +54,7 @@ constexpr int kRun = 32;                 // list positions a CTA of a cluster ta
 constexpr int kFp4RopeOff = 14336;       // KV_FP4 page layout (see dsv4sa.h)
 constexpr int kFp4ScaleOff = 22528;
 constexpr float kSlack = 8.f;            // log2 units a score may pass the max in use by
+constexpr int kParts = 2;                // the tile is handed over in this many parts of its dims (1, 2 or 4)
 constexpr int kLastChunk = 256;          // meta: rows of the chunk (<= 128), and this for an item's last
 // Registers per thread (setmaxnreg): the launch gives 896 x 72 = 64512, the three
 // kinds of warpgroup then hold 256 x 96 + 512 x 64 + 128 x 56 = 64512.
@@ -79,7 +80,7 @@ struct Smem4 {
   static constexpr int kCnt = kMl + kMaxClusterSplits * HN * 8;   // int [16]
   static constexpr int kMeta = kCnt + 64;                // int [4]
   static constexpr int kBar = kMeta + 16;                // barriers, see below
-  static constexpr int kTmem = kBar + 13 * 8 + 8;
+  static constexpr int kTmem = kBar + (2 * kParts + 11) * 8 + 8;
   static constexpr int kBytes = kTmem + 16;
 };
 
@@ -239,16 +240,16 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   float2* mlr = reinterpret_cast<float2*>(smem + S::kMl);
   int* wcnt = reinterpret_cast<int*>(smem + S::kCnt);
   volatile int* meta = reinterpret_cast<volatile int*>(smem + S::kMeta);
-  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + S::kBar);   // the chunk is in the tile
-  uint64_t* bar_free = bar_full + 1;     // the tile has been read by PV
-  uint64_t* bar_tok = bar_full + 2;      // [4]: a chunk's (or an item's end's) meta is written
-  uint64_t* bar_s = bar_full + 6;        // S is complete
-  uint64_t* bar_p = bar_full + 7;        // P is written
-  uint64_t* bar_o = bar_full + 8;        // every PV of the item is complete
-  uint64_t* bar_q = bar_full + 9;        // the item's Q is in place
-  uint64_t* bar_item = bar_full + 10;    // the end of the item has been seen
-  uint64_t* bar_recv = bar_full + 11;    // merge: the other splits' partials landed
-  uint64_t* bar_ml = bar_full + 12;      // merge: the other splits' (m, l) landed
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + S::kBar);   // [kParts]: that part of the chunk's dims is in the tile
+  uint64_t* bar_free = bar_full + kParts;    // [kParts]: ... has been read by PV
+  uint64_t* bar_tok = bar_free + kParts;     // [4]: a chunk's (or an item's end's) meta is written
+  uint64_t* bar_s = bar_tok + 4;         // S is complete
+  uint64_t* bar_p = bar_s + 1;           // P is written
+  uint64_t* bar_o = bar_s + 2;           // every PV of the item is complete
+  uint64_t* bar_q = bar_s + 3;           // the item's Q is in place
+  uint64_t* bar_item = bar_s + 4;        // the end of the item has been seen
+  uint64_t* bar_recv = bar_s + 5;        // merge: the other splits' partials landed
+  uint64_t* bar_ml = bar_s + 6;          // merge: the other splits' (m, l) landed
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::kTmem);
 
   constexpr int HW = HN / 2;             // heads of a softmax thread
@@ -264,8 +265,10 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   const int slot_bytes = slice * HN * 4;
 
   if (tid == 0) {
-    mbar_init(bar_full, kGatherThreads / 32);
-    mbar_init(bar_free, 1);
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(bar_full + i, kGatherThreads / 32);
+      mbar_init(bar_free + i, 1);
+    }
     mbar_init(bar_s, 1);
     mbar_init(bar_p, kComputeThreads / 32);
     for (int i = 0; i < 4; ++i) mbar_init(bar_tok + i, 1);
@@ -308,6 +311,53 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       const int seq = __ldg(p.q_seq + t);
       const int wpos = p.idx_w || p.kw == 0 ? 0 : __ldg(p.win_pos + t);
       int cursor = 0, count = 0;                // positions looked up, rows in the ring
+      // look up the next positions, one a thread of half of them
+      auto locate = [&]() {
+        const int end = min(cursor + kLocate, waited ? total : cw);
+        const int pos = cursor + gt;
+        uint64_t rp = 0;
+        if (gt < kLocate && pos < end) {
+          const bool window = pos < cw;
+          const int j = share_at(window ? pos : pos - cw, crank, CS);
+          int32_t e;
+          if (!window) {
+            e = __ldg(p.idx_c + static_cast<int64_t>(t) * p.idx_c_stride + j);
+          } else if (p.idx_w) {
+            e = __ldg(p.idx_w + static_cast<int64_t>(t) * p.idx_w_stride + j);
+          } else {
+            const int64_t pw = static_cast<int64_t>(wpos) - p.kw + 1 + j;
+            e = pw < 0 ? -1 : static_cast<int32_t>(p.win_ring > 0 ? pw % p.win_ring : pw);
+          }
+          if (e >= 0) {
+            const int stride = window ? p.win_pt_stride : p.comp_pt_stride;
+            const int32_t* pt = (window ? p.win_pt : p.comp_pt) + static_cast<int64_t>(seq) * stride;
+            const int64_t np = window ? p.win_num_pages : p.comp_num_pages;
+            const int32_t page = (e >> 6) < stride ? __ldg(pt + (e >> 6)) : -1;
+            if (page < 0 || page >= np) {
+              raise_error(kErrIndex);
+            } else {
+              const uint8_t* base = window ? p.win_base : p.comp_base;
+              rp = reinterpret_cast<uint64_t>(base + page * (window ? p.win_page_stride : p.comp_page_stride)) |
+                   static_cast<uint64_t>(e & 63);
+            }
+          }
+        }
+        const uint32_t bits = __ballot_sync(0xffffffffu, rp != 0);
+        const int w = static_cast<int>(warp) - 8;
+        if (lane == 0) wcnt[w] = __popc(bits);
+        named_barrier_sync(kBarGather4, kGatherThreads);
+        int before = 0, all = 0;
+#pragma unroll
+        for (int i = 0; i < kLocate / 32; ++i) {
+          const int n = wcnt[i];
+          before += i < w ? n : 0;
+          all += n;
+        }
+        if (rp != 0) ring[(head + count + before + __popc(bits & ((1u << lane) - 1u))) & (kRing - 1)] = rp;
+        named_barrier_sync(kBarGather4, kGatherThreads);
+        count += all;
+        cursor = end;
+      };
       while (true) {
         // ---- enough rows for a chunk, or the end of the lists
         while (count < kRows && cursor < total) {
@@ -316,50 +366,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
             griddep_wait();
             waited = true;
           }
-          const int end = min(cursor + kLocate, waited ? total : cw);
-          const int pos = cursor + gt;
-          uint64_t rp = 0;
-          if (gt < kLocate && pos < end) {
-            const bool window = pos < cw;
-            const int j = share_at(window ? pos : pos - cw, crank, CS);
-            int32_t e;
-            if (!window) {
-              e = __ldg(p.idx_c + static_cast<int64_t>(t) * p.idx_c_stride + j);
-            } else if (p.idx_w) {
-              e = __ldg(p.idx_w + static_cast<int64_t>(t) * p.idx_w_stride + j);
-            } else {
-              const int64_t pw = static_cast<int64_t>(wpos) - p.kw + 1 + j;
-              e = pw < 0 ? -1 : static_cast<int32_t>(p.win_ring > 0 ? pw % p.win_ring : pw);
-            }
-            if (e >= 0) {
-              const int stride = window ? p.win_pt_stride : p.comp_pt_stride;
-              const int32_t* pt = (window ? p.win_pt : p.comp_pt) + static_cast<int64_t>(seq) * stride;
-              const int64_t np = window ? p.win_num_pages : p.comp_num_pages;
-              const int32_t page = (e >> 6) < stride ? __ldg(pt + (e >> 6)) : -1;
-              if (page < 0 || page >= np) {
-                raise_error(kErrIndex);
-              } else {
-                const uint8_t* base = window ? p.win_base : p.comp_base;
-                rp = reinterpret_cast<uint64_t>(base + page * (window ? p.win_page_stride : p.comp_page_stride)) |
-                     static_cast<uint64_t>(e & 63);
-              }
-            }
-          }
-          const uint32_t bits = __ballot_sync(0xffffffffu, rp != 0);
-          const int w = static_cast<int>(warp) - 8;
-          if (lane == 0) wcnt[w] = __popc(bits);
-          named_barrier_sync(kBarGather4, kGatherThreads);
-          int before = 0, all = 0;
-#pragma unroll
-          for (int i = 0; i < kLocate / 32; ++i) {
-            const int n = wcnt[i];
-            before += i < w ? n : 0;
-            all += n;
-          }
-          if (rp != 0) ring[(head + count + before + __popc(bits & ((1u << lane) - 1u))) & (kRing - 1)] = rp;
-          named_barrier_sync(kBarGather4, kGatherThreads);
-          count += all;
-          cursor = end;
+          locate();
         }
         const int n = min(count, kRows);
         if (n == 0) break;
@@ -387,48 +394,50 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         count -= n;
         // no row of the item is left to come: the softmax may replace Q once this chunk's S is complete
         const bool last = count == 0 && cursor >= total;
-        // ---- into the tile, when the previous chunk's PV has read it
-        if (chunk > 0) {
-          if (gt == 0 && ok) ok = bar_wait(bar_free, (chunk - 1) & 1);
-          named_barrier_sync(kBarGather4, kGatherThreads);
-        }
+        // ---- look ahead while the loads are in flight
+        if (count < kRows && cursor < total && (waited || cursor < cw)) locate();
+        // ---- into the tile, part by part, when the previous chunk's PV has read it
         const uint32_t sw[4] = {scl.x, scl.y, scl.z, scl.w};
 #pragma unroll
-        for (int b = 0; b < 3; ++b) {
-          // 32 values: units 4 (piece & 1) + x of column block 2 b + (piece >> 1).  The
-          // upper two pieces take x in the order 2, 3, 0, 1, so that the eight lanes of
-          // two rows hit eight different bank groups.
-          const BlockScale bs = block_scale((sw[b] >> (8 * piece)) & 0xFFu);
-          uint8_t* blk = kv + (2 * b + (piece >> 1)) * kKvBlock;
-          const uint32_t c4[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
+        for (int b = 0; b < 4; ++b) {
+          if (b % (4 / kParts) == 0 && chunk > 0 && ok) ok = warp_wait(bar_free + b / (4 / kParts), (chunk - 1) & 1);
+          if (b < 3) {
+            // 32 values: units 4 (piece & 1) + x of column block 2 b + (piece >> 1).  The
+            // upper two pieces take x in the order 2, 3, 0, 1, so that the eight lanes of
+            // two rows hit eight different bank groups.
+            const BlockScale bs = block_scale((sw[b] >> (8 * piece)) & 0xFFu);
+            uint8_t* blk = kv + (2 * b + (piece >> 1)) * kKvBlock;
+            const uint32_t c4[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w = piece >= 2 ? c4[i ^ 2] : c4[i];
-            const uint32_t x = static_cast<uint32_t>(i) ^ (piece & 2);
-            uint4 v = widen8(w, bs.first);
-            if (bs.more) v = scale_up(v, bs.more);
-            *reinterpret_cast<uint4*>(blk + sw128_offset(row, static_cast<uint32_t>(4 * (piece & 1)) + x)) = v;
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w = piece >= 2 ? c4[i ^ 2] : c4[i];
+              const uint32_t x = static_cast<uint32_t>(i) ^ (piece & 2);
+              uint4 v = widen8(w, bs.first);
+              if (bs.more) v = scale_up(v, bs.more);
+              *reinterpret_cast<uint4*>(blk + sw128_offset(row, static_cast<uint32_t>(4 * (piece & 1)) + x)) = v;
+            }
+          } else {
+            const BlockScale bs = block_scale((sw[3] >> (8 * (piece >> 1))) & 0xFFu);
+            const uint32_t u = static_cast<uint32_t>(2 * piece);
+            uint4 v0 = widen8(code3.x, bs.first), v1 = widen8(code3.y, bs.first);
+            if (bs.more) {
+              v0 = scale_up(v0, bs.more);
+              v1 = scale_up(v1, bs.more);
+            }
+            *reinterpret_cast<uint4*>(kv + 6 * kKvBlock + sw128_offset(row, u)) = v0;
+            *reinterpret_cast<uint4*>(kv + 6 * kKvBlock + sw128_offset(row, u + 1)) = v1;
+            *reinterpret_cast<uint4*>(kv + 7 * kKvBlock + sw128_offset(row, u)) = rope[0];
+            *reinterpret_cast<uint4*>(kv + 7 * kKvBlock + sw128_offset(row, u + 1)) = rope[1];
           }
-        }
-        {
-          const BlockScale bs = block_scale((sw[3] >> (8 * (piece >> 1))) & 0xFFu);
-          const uint32_t u = static_cast<uint32_t>(2 * piece);
-          uint4 v0 = widen8(code3.x, bs.first), v1 = widen8(code3.y, bs.first);
-          if (bs.more) {
-            v0 = scale_up(v0, bs.more);
-            v1 = scale_up(v1, bs.more);
+          if ((b + 1) % (4 / kParts) == 0) {
+            fence_proxy_async_smem();      // the tile is read by the tensor core
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_full + b / (4 / kParts));
           }
-          *reinterpret_cast<uint4*>(kv + 6 * kKvBlock + sw128_offset(row, u)) = v0;
-          *reinterpret_cast<uint4*>(kv + 6 * kKvBlock + sw128_offset(row, u + 1)) = v1;
-          *reinterpret_cast<uint4*>(kv + 7 * kKvBlock + sw128_offset(row, u)) = rope[0];
-          *reinterpret_cast<uint4*>(kv + 7 * kKvBlock + sw128_offset(row, u + 1)) = rope[1];
-        }
-        fence_proxy_async_smem();          // the tile is read by the tensor core
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_full);
-        if (gt == 0) {                    // the meta slot's last token, four ago, has been read
-          meta[token & 3] = n | (last ? kLastChunk : 0);
-          mbar_arrive(bar_tok + (token & 3));
+          if (b == 0 && gt == 0) {         // the meta slot's last token, four ago, has been read
+            meta[token & 3] = n | (last ? kLastChunk : 0);
+            mbar_arrive(bar_tok + (token & 3));
+          }
         }
         __syncwarp();
         ++chunk;
@@ -465,10 +474,12 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
           const int word = meta[token & 3];
           ++token;
           if (word < 0) break;
-          ok = warp_wait(bar_full, chunk & 1);
-          tc_fence_after();
 #pragma unroll 1
           for (int b = 0; b < 8; ++b) {    // not unrolled: 32 pairs of descriptors would not fit in registers
+            if (b % (8 / kParts) == 0) {
+              ok = ok && warp_wait(bar_full + b / (8 / kParts), chunk & 1);
+              tc_fence_after();
+            }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_f16_elect(tmem + kColS, kvk + ((b * kKvBlock + kk * 32) >> 4), qk + ((b * HN * 128 + kk * 32) >> 4), hi, idesc_s,
@@ -485,8 +496,8 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
               mma_f16_elect(tmem + kColO + mb * HN, kvm + ((2 * mb * kKvBlock + kk * 2048) >> 4), pd + bo, hi, idesc_o,
                             (!first || kk > 0) ? 1u : 0u);
             }
+            if ((mb + 1) % (4 / kParts) == 0) mma_commit_elect(bar_free + mb / (4 / kParts));
           }
-          mma_commit_elect(bar_free);
           first = false;
           ++chunk;
         }
@@ -536,20 +547,17 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       float lsum[HW];
 #pragma unroll
       for (int i = 0; i < HW; ++i) lsum[i] = 0.f;
+      // the head's sink now: at the end it would be a cold load
+      const float sink2 = tid < hreal ? __ldg(p.sink + h0 + tid) * kLog2e : -INFINITY;
       bool have_o = false, q_sent = CS > 1 || item + item_step >= n_items;   // the next item's Q is on its way
       if (!q_sent && tid == 0) q_to_l2(item + item_step);
       while (true) {
-        // ---- one thread waits for the chunk's S (or the item's end), the others at the barrier
-        bool bad = false;
-        if (tid == 0) {
-          bad = !bar_wait(bar_tok + (token & 3), (token >> 2) & 1);
-          if (!bad && meta[token & 3] >= 0) bad = !bar_wait(bar_s, chunk & 1);
-        }
-        alive = !any_of(bad, kBarCompute4, kComputeThreads);
-        if (!alive) break;
-        const int word = meta[token & 3];
+        // ---- each warp waits for the chunk's S (or the item's end).  A wait that runs out is
+        // told in the vote below, which every thread reaches, so all leave together.
+        bool bad = !warp_wait(bar_tok + (token & 3), (token >> 2) & 1);
+        const int word = bad ? 0 : meta[token & 3];
+        if (!bad && word >= 0) bad = !warp_wait(bar_s, chunk & 1);
         ++token;
-        if (word < 0) break;
         tc_fence_after();
         float sv[HW];
         tmem_load_cols<HW>(ta + kColS + hb, sv);
@@ -565,7 +573,9 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
             over = fmaxf(over, sv[i + x] - mm[x]);
           }
         }
-        if (any_of(over > kSlack, kBarCompute4, kComputeThreads)) {
+        if (any_of(bad || word < 0 || over > kSlack, kBarCompute4, kComputeThreads)) {
+          alive = !any_of(bad, kBarCompute4, kComputeThreads);
+          if (!alive || word < 0) break;
           // a score passes the max in use: take the chunk's max of those heads, rescale
           float tmp[HW];
 #pragma unroll
@@ -640,6 +650,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       if (!alive) break;
       // ---- the item's end: its last S is complete, so Q may be replaced
       if (!q_sent) load_q(item + item_step);
+      if (CS == 1 && item + item_step < n_items) q_ready();
       {                                  // per-head sums over the rows
         const float l = TransposeReduce<HW>::run(lsum, lane, 16u, OpAdd());
         constexpr int kRep = 32 / HW;
@@ -664,7 +675,6 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
           }
           ok = bar_wait(bar_ml, 0) && ok;
         }
-        const float sink2 = tid < hreal ? __ldg(p.sink + h0 + tid) * kLog2e : -INFINITY;
         auto ml_of = [&](int c) { return c == crank ? make_float2(m_mine, l_mine) : mlr[c * HN + tid]; };
         float M = sink2;
         for (int c = 0; c < CS; ++c) {
@@ -691,46 +701,52 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       if (!alive) break;
       if (tid == 0) mbar_arrive(bar_item);                      // the MMA warp has read the end's token, too
       if (CS > 1) break;                 // merged below, by all warps of the cluster
-      if (item + item_step < n_items) q_ready();
-      // ---- output, eight heads at a time: thread = dim, staged as [head][512] BF16 in
-      // the two P buffers in turn, stored 16 bytes a thread
+      // ---- output, eight heads at a time: thread = dim, staged in the two P buffers in
+      // turn as words of (head, head + 1), [4][512], read back eight dims a thread and
+      // stored 16 bytes a head
       const float4* rrow = rope_row(p, t);
 #pragma unroll 1
       for (int j0 = 0; j0 < hreal; j0 += 8) {
-        __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(ps + ((j0 >> 3) & 1) * 8192);
+        uint32_t* stage = reinterpret_cast<uint32_t*>(ps + ((j0 >> 3) & 1) * 8192);
+        float v[2][8];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const int blk = static_cast<int>(hh) * 2 + b;
-          const int d = blk * 128 + static_cast<int>(g * 32 + lane);
-          float v[8];
           if (have_o) {
-            tmem_load_cols<8>(ta + kColO + blk * HN + j0, v);
+            tmem_load_cols<8>(ta + kColO + (hh * 2 + b) * HN + j0, v[b]);
           } else {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = 0.f;
+            for (int x = 0; x < 8; ++x) v[b][x] = 0.f;
           }
-          const float4 fa = *reinterpret_cast<const float4*>(fac + j0), fb = *reinterpret_cast<const float4*>(fac + j0 + 4);
-          const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
+        }
+        const float4 fa = *reinterpret_cast<const float4*>(fac + j0), fb = *reinterpret_cast<const float4*>(fac + j0 + 4);
+        const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
 #pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] *= f[x];
+        for (int b = 0; b < 2; ++b) {
+          const int d = (static_cast<int>(hh) * 2 + b) * 128 + r;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[b][x] *= f[x];
           if (rrow != nullptr && d >= 512 - 64) {               // warp-uniform: dims (d, d ^ 1) are a pair, lanes (l, l ^ 1)
             const float2 cs = __ldg(reinterpret_cast<const float2*>(rrow) + ((d - (512 - 64)) >> 1));
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-              const float other = __shfl_xor_sync(0xffffffffu, v[x], 1);
-              v[x] = (lane & 1) ? fmaf(v[x], cs.x, -(other * cs.y)) : fmaf(v[x], cs.x, other * cs.y);
+              const float other = __shfl_xor_sync(0xffffffffu, v[b][x], 1);
+              v[b][x] = (lane & 1) ? fmaf(v[b][x], cs.x, -(other * cs.y)) : fmaf(v[b][x], cs.x, other * cs.y);
             }
           }
 #pragma unroll
-          for (int x = 0; x < 8; ++x) stage[x * 512 + d] = __float2bfloat16_rn(v[x]);
+          for (int x = 0; x < 4; ++x) stage[x * 512 + d] = pack_bf16x2(v[b][2 * x], v[b][2 * x + 1]);
         }
         named_barrier_sync(kBarCompute4, kComputeThreads);      // and the buffer before last has been read out
-        const uint4* src = reinterpret_cast<const uint4*>(stage);
-        uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(t) * p.H + h0 + j0) * 512);
-        const int units = min(8, hreal - j0) * 64;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (i * kComputeThreads + tid < units) dst[i * kComputeThreads + tid] = src[i * kComputeThreads + tid];
+        const int h = (tid >> 6) * 2;                           // heads j0 + h, j0 + h + 1; dims 8 (tid & 63) ..
+        const uint4 a = *reinterpret_cast<const uint4*>(stage + (tid >> 6) * 512 + (tid & 63) * 8);
+        const uint4 c = *reinterpret_cast<const uint4*>(stage + (tid >> 6) * 512 + (tid & 63) * 8 + 4);
+        uint16_t* dst = p.out + (static_cast<int64_t>(t) * p.H + h0 + j0 + h) * 512 + (tid & 63) * 8;
+        if (j0 + h < hreal)
+          *reinterpret_cast<uint4*>(dst) = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                                      __byte_perm(c.x, c.y, 0x5410), __byte_perm(c.z, c.w, 0x5410));
+        if (j0 + h + 1 < hreal)
+          *reinterpret_cast<uint4*>(dst + 512) = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                                            __byte_perm(c.x, c.y, 0x7632), __byte_perm(c.z, c.w, 0x7632));
       }
       if (tid < HN) m_used[tid] = -1e30f;                       // read above by the same thread
       tc_fence_before();                 // O has been read; the next item's PV follows its bar_p
