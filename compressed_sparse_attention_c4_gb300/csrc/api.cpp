@@ -428,9 +428,9 @@ DSV4SA_API int dsv4sa_rmsnorm_quant(const void* x, int64_t x_stride, const void*
   if (dim > DSV4SA_MAX_NORM_DIM || (group != 64 && group != 128)) return DSV4SA_ERR_UNSUPPORTED;
   if (x_stride < dim || x_stride % 8 != 0) return DSV4SA_ERR_INVALID_ARG;
   if (residual && (residual_stride < dim || residual_stride % 8 != 0)) return DSV4SA_ERR_INVALID_ARG;
+  if (n == 0) return DSV4SA_OK;
   if (!codes != !scale || (codes && dim % group != 0)) return DSV4SA_ERR_INVALID_ARG;
   if (!residual_out && !y && !codes) return DSV4SA_ERR_INVALID_ARG;
-  if (n == 0) return DSV4SA_OK;
   if (!x || !norm_w || !aligned(x, 16) || !aligned(residual, 16) || !aligned(norm_w, 16) || !aligned(residual_out, 16) ||
       !aligned(y, 16) || !aligned(codes, 16) || !aligned(scale, 4))
     return DSV4SA_ERR_INVALID_ARG;

@@ -47,7 +47,8 @@ using namespace attn;
 constexpr int kComputeThreads = 256;     // warps 0-7: softmax, output
 constexpr int kGatherThreads = 512;      // warps 8-23
 constexpr int kMmaWarp = 24;
-constexpr int kThreads4 = kComputeThreads + kGatherThreads + 128;   // the last warpgroup: one MMA warp
+constexpr int kThreads4 = kComputeThreads + kGatherThreads + 128;   // the last warpgroup: the MMA warp, then
+constexpr int kQThreads = 96;            // its other three warps fetch Q
 constexpr int kLocate = 256;             // list positions looked up at a time
 constexpr int kRing = 512;               // located rows waiting for a chunk (fewer than 128 + 256)
 constexpr int kRun = 32;                 // list positions a CTA of a cluster takes in a row
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     mbar_init(bar_p, kComputeThreads / 32);
     for (int i = 0; i < 4; ++i) mbar_init(bar_tok + i, 1);
     mbar_init(bar_o, 1);
-    mbar_init(bar_q, kComputeThreads / 32);
+    mbar_init(bar_q, kQThreads / 32);
     mbar_init(bar_item, 1);
     mbar_init(bar_recv, 1);
     mbar_init(bar_ml, CS > 1 ? (CS - 1) * HN : 1);
@@ -503,6 +504,57 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         }
         mma_commit_elect(bar_o);
       }
+    } else {
+      // ---- the warpgroup's other three warps fetch Q: the next item's, as soon as an
+      // item's last S is complete (it is brought into L2 when the item begins).
+      // Swizzled K-major tile; heads past the item's are zero.
+      const int qt = tid - (kMmaWarp + 1) * 32;
+      auto load_q = [&](int item) {
+        const int t = item / groups, h0 = (item - t * groups) * HN;
+        const int hreal = min(HN, p.H - h0);
+        const uint4* src = reinterpret_cast<const uint4*>(p.q) + (static_cast<int64_t>(t) * p.H + h0) * 64;
+#pragma unroll 4
+        for (int u = qt; u < HN * 64; u += kQThreads) {
+          const int h = u >> 6, v = u & 63;
+          cp_async16(qs + (v >> 3) * (HN * 128) + sw128_offset(h, v & 7), src + min(h, hreal - 1) * 64 + v, h < hreal ? 16u : 0u);
+        }
+      };
+      auto q_ready = [&]() {
+        cp_async_wait();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_q);
+      };
+      if (item0 < n_items) {
+        load_q(item0);
+        q_ready();
+      }
+      int chunk = 0, token = 0;
+      for (int item = item0; item < n_items && ok; item += item_step) {
+        const int next = item + item_step;
+        if (next < n_items && qt == 0) {
+          const int t = next / groups, h0 = (next - t * groups) * HN;
+          prefetch_l2(p.q + (static_cast<int64_t>(t) * p.H + h0) * 512, static_cast<uint32_t>(min(HN, p.H - h0)) * 1024u);
+        }
+        bool sent = next >= n_items;
+        while (ok) {
+          ok = warp_wait(bar_tok + (token & 3), (token >> 2) & 1);
+          if (!ok) break;
+          const int word = meta[token & 3];
+          ++token;
+          if (word >= 0) {
+            ok = warp_wait(bar_s, chunk & 1);
+            ++chunk;
+          }
+          if (ok && !sent && (word < 0 || (word & kLastChunk) != 0)) {
+            load_q(next);
+            q_ready();
+            sent = true;
+          }
+          if (word < 0) break;
+        }
+      }
+      cp_async_wait();
     }
   } else {
     // =========================== softmax warps ===========================
@@ -512,31 +564,6 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     const int hb = static_cast<int>(hh) * HW;               // first head of this thread
     const uint32_t ta = tmem + ((g * 32u) << 16);
     bool waited = !p.early_window;
-    // Q of an item -> swizzled K-major tile; heads past H are zero
-    auto load_q = [&](int item) {
-      const int t = item / groups, h0 = (item - t * groups) * HN;
-      const int hreal = min(HN, p.H - h0);
-      const uint4* src = reinterpret_cast<const uint4*>(p.q) + (static_cast<int64_t>(t) * p.H + h0) * 64;
-#pragma unroll 4
-      for (int i = 0; i < HN / 4; ++i) {
-        const int u = i * kComputeThreads + tid, h = u >> 6, v = u & 63;
-        cp_async16(qs + (v >> 3) * (HN * 128) + sw128_offset(h, v & 7), src + min(h, hreal - 1) * 64 + v, h < hreal ? 16u : 0u);
-      }
-    };
-    auto q_to_l2 = [&](int item) {
-      const int t = item / groups, h0 = (item - t * groups) * HN;
-      prefetch_l2(p.q + (static_cast<int64_t>(t) * p.H + h0) * 512, static_cast<uint32_t>(min(HN, p.H - h0)) * 1024u);
-    };
-    auto q_ready = [&]() {
-      cp_async_wait();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_q);
-    };
-    if (item0 < n_items) {
-      load_q(item0);
-      q_ready();
-    }
     if (tid < HN) m_used[tid] = -1e30f;
     named_barrier_sync(kBarCompute4, kComputeThreads);
     int chunk = 0, token = 0, n_item = 0;
@@ -548,9 +575,8 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
 #pragma unroll
       for (int i = 0; i < HW; ++i) lsum[i] = 0.f;
       // the head's sink now: at the end it would be a cold load
-      const float sink2 = tid < hreal ? __ldg(p.sink + h0 + tid) * kLog2e : -INFINITY;
-      bool have_o = false, q_sent = CS > 1 || item + item_step >= n_items;   // the next item's Q is on its way
-      if (!q_sent && tid == 0) q_to_l2(item + item_step);
+      const float sink = tid < hreal ? __ldg(p.sink + h0 + tid) : -INFINITY;
+      bool have_o = false;
       while (true) {
         // ---- each warp waits for the chunk's S (or the item's end).  A wait that runs out is
         // told in the vote below, which every thread reaches, so all leave together.
@@ -642,15 +668,12 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p);
         ++chunk;
-        if ((word & kLastChunk) != 0 && !q_sent) {          // the item's last S is complete: Q may be replaced
-          load_q(item + item_step);
-          q_sent = true;
+        if ((word & kLastChunk) != 0) {  // the item's end follows: no need to wait for its token
+          ++token;
+          break;
         }
       }
       if (!alive) break;
-      // ---- the item's end: its last S is complete, so Q may be replaced
-      if (!q_sent) load_q(item + item_step);
-      if (CS == 1 && item + item_step < n_items) q_ready();
       {                                  // per-head sums over the rows
         const float l = TransposeReduce<HW>::run(lsum, lane, 16u, OpAdd());
         constexpr int kRep = 32 / HW;
@@ -676,6 +699,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
           ok = bar_wait(bar_ml, 0) && ok;
         }
         auto ml_of = [&](int c) { return c == crank ? make_float2(m_mine, l_mine) : mlr[c * HN + tid]; };
+        const float sink2 = sink * kLog2e;
         float M = sink2;
         for (int c = 0; c < CS; ++c) {
           const float2 ml = ml_of(c);
@@ -701,52 +725,56 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       if (!alive) break;
       if (tid == 0) mbar_arrive(bar_item);                      // the MMA warp has read the end's token, too
       if (CS > 1) break;                 // merged below, by all warps of the cluster
-      // ---- output, eight heads at a time: thread = dim, staged in the two P buffers in
-      // turn as words of (head, head + 1), [4][512], read back eight dims a thread and
-      // stored 16 bytes a head
+      // ---- output, 16 heads at a time: thread = dim, staged in the P buffer as words of
+      // (head, head + 1), [8][512], read back eight dims a thread and stored 16 bytes a head
       const float4* rrow = rope_row(p, t);
+      uint32_t* stage = reinterpret_cast<uint32_t*>(ps);
 #pragma unroll 1
-      for (int j0 = 0; j0 < hreal; j0 += 8) {
-        uint32_t* stage = reinterpret_cast<uint32_t*>(ps + ((j0 >> 3) & 1) * 8192);
-        float v[2][8];
+      for (int j0 = 0; j0 < hreal; j0 += 16) {
+        float f[16];
+#pragma unroll
+        for (int x = 0; x < 16; x += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(fac + j0 + x);
+          f[x] = q.x, f[x + 1] = q.y, f[x + 2] = q.z, f[x + 3] = q.w;
+        }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
+          float v[16];
           if (have_o) {
-            tmem_load_cols<8>(ta + kColO + (hh * 2 + b) * HN + j0, v[b]);
+            tmem_load_cols<16>(ta + kColO + (hh * 2 + b) * HN + j0, v);
           } else {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[b][x] = 0.f;
+            for (int x = 0; x < 16; ++x) v[x] = 0.f;
           }
-        }
-        const float4 fa = *reinterpret_cast<const float4*>(fac + j0), fb = *reinterpret_cast<const float4*>(fac + j0 + 4);
-        const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
           const int d = (static_cast<int>(hh) * 2 + b) * 128 + r;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) v[b][x] *= f[x];
+          for (int x = 0; x < 16; ++x) v[x] *= f[x];
           if (rrow != nullptr && d >= 512 - 64) {               // warp-uniform: dims (d, d ^ 1) are a pair, lanes (l, l ^ 1)
             const float2 cs = __ldg(reinterpret_cast<const float2*>(rrow) + ((d - (512 - 64)) >> 1));
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const float other = __shfl_xor_sync(0xffffffffu, v[b][x], 1);
-              v[b][x] = (lane & 1) ? fmaf(v[b][x], cs.x, -(other * cs.y)) : fmaf(v[b][x], cs.x, other * cs.y);
+            for (int x = 0; x < 16; ++x) {
+              const float other = __shfl_xor_sync(0xffffffffu, v[x], 1);
+              v[x] = (lane & 1) ? fmaf(v[x], cs.x, -(other * cs.y)) : fmaf(v[x], cs.x, other * cs.y);
             }
           }
 #pragma unroll
-          for (int x = 0; x < 4; ++x) stage[x * 512 + d] = pack_bf16x2(v[b][2 * x], v[b][2 * x + 1]);
+          for (int x = 0; x < 8; ++x) stage[x * 512 + d] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
         }
-        named_barrier_sync(kBarCompute4, kComputeThreads);      // and the buffer before last has been read out
-        const int h = (tid >> 6) * 2;                           // heads j0 + h, j0 + h + 1; dims 8 (tid & 63) ..
-        const uint4 a = *reinterpret_cast<const uint4*>(stage + (tid >> 6) * 512 + (tid & 63) * 8);
-        const uint4 c = *reinterpret_cast<const uint4*>(stage + (tid >> 6) * 512 + (tid & 63) * 8 + 4);
-        uint16_t* dst = p.out + (static_cast<int64_t>(t) * p.H + h0 + j0 + h) * 512 + (tid & 63) * 8;
-        if (j0 + h < hreal)
-          *reinterpret_cast<uint4*>(dst) = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
-                                                      __byte_perm(c.x, c.y, 0x5410), __byte_perm(c.z, c.w, 0x5410));
-        if (j0 + h + 1 < hreal)
-          *reinterpret_cast<uint4*>(dst + 512) = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
-                                                            __byte_perm(c.x, c.y, 0x7632), __byte_perm(c.z, c.w, 0x7632));
+        named_barrier_sync(kBarCompute4, kComputeThreads);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int hp = (tid >> 6) + 4 * i, h = j0 + 2 * hp;   // heads h, h + 1; dims 8 (tid & 63) ..
+          const uint4 a = *reinterpret_cast<const uint4*>(stage + hp * 512 + (tid & 63) * 8);
+          const uint4 c = *reinterpret_cast<const uint4*>(stage + hp * 512 + (tid & 63) * 8 + 4);
+          uint16_t* dst = p.out + (static_cast<int64_t>(t) * p.H + h0 + h) * 512 + (tid & 63) * 8;
+          if (h < hreal)
+            *reinterpret_cast<uint4*>(dst) = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                                        __byte_perm(c.x, c.y, 0x5410), __byte_perm(c.z, c.w, 0x5410));
+          if (h + 1 < hreal)
+            *reinterpret_cast<uint4*>(dst + 512) = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                                              __byte_perm(c.x, c.y, 0x7632), __byte_perm(c.z, c.w, 0x7632));
+        }
+        named_barrier_sync(kBarCompute4, kComputeThreads);      // the buffer has been read out
       }
       if (tid < HN) m_used[tid] = -1e30f;                       // read above by the same thread
       tc_fence_before();                 // O has been read; the next item's PV follows its bar_p

@@ -11,8 +11,9 @@
 // being unit i kTpr + (its index) of the row, so loads and stores are coalesced
 // and a block's 8 or 16 units are neighbouring lanes of one warp: its absmax is
 // three or four shuffles.  The grid is resident and walks the rows; the weights
-// of a thread's columns are loaded once, and the next row's units are loaded
-// before the current row is reduced, so reads stay in flight.
+// of a thread's columns are loaded once.  To keep reads in flight a long row's
+// successor is loaded before the row is reduced, and short rows go several at a
+// time (a row of 128 is one 16-byte load a thread).
 #include <atomic>
 
 #include "common.cuh"
@@ -60,7 +61,7 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int kTpr, int kUnits>
+template <int kTpr, int kUnits, int kRowsAtOnce, bool kRes>
 __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256) rmsnorm_quant_kernel(const NormParams p) {
   constexpr int kThreads = kTpr > 256 ? kTpr : 256;
   constexpr int kRowsPerCta = kThreads / kTpr;
@@ -80,23 +81,20 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256) rmsnorm_quant_kernel(
     w[i][4] = b.x, w[i][5] = b.y, w[i][6] = b.z, w[i][7] = b.w;
   }
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 xv[kUnits], rv[kUnits];
-  auto load = [&](int64_t row) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRowsPerCta;
+  auto load = [&](int64_t row, uint4 (&xv)[kUnits], uint4 (&rv)[kUnits]) {
     const bool live = row < p.n;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int u = i * kTpr + c;
       const bool in = live && u < p.units;
       xv[i] = in ? __ldcs(p.x + row * p.x_stride + u) : zero;
-      rv[i] = in && p.r ? __ldcs(p.r + row * p.r_stride + u) : zero;
+      if constexpr (kRes) rv[i] = in ? __ldcs(p.r + row * p.r_stride + u) : zero;
     }
   };
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRowsPerCta;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + sub;
-  load(row);
   int buf = 0;
-  // the first row of the CTA decides: every thread takes part in shuffles and barriers
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRowsPerCta; first < p.n; first += step, row += step) {
+  // one row, from the units in xv and rv; `next` loads the row after it in between
+  auto process = [&](int64_t row, uint4 (&xv)[kUnits], uint4 (&rv)[kUnits], int64_t next) {
     const bool live = row < p.n;
     float s[kUnits][8];
     float sq = 0.f;
@@ -104,14 +102,14 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256) rmsnorm_quant_kernel(
     for (int i = 0; i < kUnits; ++i) {
       float r[8];
       unpack8(xv[i], s[i]);
-      unpack8(rv[i], r);
+      if constexpr (kRes) unpack8(rv[i], r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (p.r) s[i][j] += r[j];
+        if constexpr (kRes) s[i][j] += r[j];
         sq = fmaf(s[i][j], s[i][j], sq);
       }
     }
-    load(row + step);      // the next row's units, in flight while this one is reduced
+    if constexpr (kRowsAtOnce == 1) load(next, xv, rv);   // in flight while this row is reduced
 #pragma unroll
     for (int o = (kTpr < 32 ? kTpr : 32) / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
     if constexpr (kWarps > 1) {
@@ -160,11 +158,25 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256) rmsnorm_quant_kernel(
         }
       }
     }
+  };
+  // the first row of the CTA decides: every thread takes part in shuffles and barriers
+  int64_t first = static_cast<int64_t>(blockIdx.x) * kRowsPerCta;
+  uint4 xv[kRowsAtOnce][kUnits], rv[kRowsAtOnce][kUnits];
+  if constexpr (kRowsAtOnce == 1) {
+    load(first + sub, xv[0], rv[0]);
+    for (; first < p.n; first += step) process(first + sub, xv[0], rv[0], first + sub + step);
+  } else {
+    for (; first < p.n; first += kRowsAtOnce * step) {
+#pragma unroll
+      for (int k = 0; k < kRowsAtOnce; ++k) load(first + sub + k * step, xv[k], rv[k]);
+#pragma unroll
+      for (int k = 0; k < kRowsAtOnce; ++k) process(first + sub + k * step, xv[k], rv[k], 0);
+    }
   }
 }
 
-template <int kTpr, int kUnits>
-int launch_norm(const NormParams& p, cudaStream_t stream) {
+template <int kTpr, int kUnits, int kRowsAtOnce, bool kRes>
+int launch_norm_r(const NormParams& p, cudaStream_t stream) {
   constexpr int kThreads = kTpr > 256 ? kTpr : 256;
   constexpr int kRowsPerCta = kThreads / kTpr;
   static std::atomic<int> cached{0};   // CTAs per SM, a property of the kernel: queried once
@@ -172,17 +184,27 @@ int launch_norm(const NormParams& p, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess) return DSV4SA_ERR_CUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DSV4SA_ERR_CUDA;
   if (resident == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, rmsnorm_quant_kernel<kTpr, kUnits>, kThreads, 0) !=
-        cudaSuccess)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            &resident, rmsnorm_quant_kernel<kTpr, kUnits, kRowsAtOnce, kRes>, kThreads, 0) != cudaSuccess)
       return DSV4SA_ERR_CUDA;
+    if (resident < 1) resident = 1;
     cached.store(resident, std::memory_order_relaxed);
   }
+  // A CTA for each kRowsPerCta rows while there are few; a resident grid that keeps
+  // the weights in registers for long rows; for short ones (whose weights are a few
+  // cached lines) CTAs of a few batches each, which even out better
   const int64_t want = (static_cast<int64_t>(p.n) + kRowsPerCta - 1) / kRowsPerCta;
-  const int64_t full = static_cast<int64_t>(sms) * (resident > 0 ? resident : 1);
-  return launch_pdl(rmsnorm_quant_kernel<kTpr, kUnits>, dim3(static_cast<unsigned>(want < full ? want : full)),
-                    dim3(kThreads), 0, stream, p) == cudaSuccess
+  const int64_t full = static_cast<int64_t>(sms) * resident * (kRowsAtOnce > 1 ? 4 : 1);
+  return launch_pdl(rmsnorm_quant_kernel<kTpr, kUnits, kRowsAtOnce, kRes>,
+                    dim3(static_cast<unsigned>(want < full ? want : full)), dim3(kThreads), 0, stream, p) == cudaSuccess
              ? DSV4SA_OK
              : DSV4SA_ERR_CUDA;
+}
+
+template <int kTpr, int kUnits, int kRowsAtOnce>
+int launch_norm(const NormParams& p, cudaStream_t stream) {
+  return p.r ? launch_norm_r<kTpr, kUnits, kRowsAtOnce, true>(p, stream)
+             : launch_norm_r<kTpr, kUnits, kRowsAtOnce, false>(p, stream);
 }
 
 }  // namespace
@@ -206,14 +228,14 @@ int launch_rmsnorm_quant(const void* x, int64_t x_stride, const void* residual, 
   p.inv_dim = 1.0f / static_cast<float>(dim);
   p.eps = eps;
   // the fewest threads whose registers hold the row in at most four units each
-  if (dim <= 128) return launch_norm<16, 1>(p, stream);
-  if (dim <= 256) return launch_norm<32, 1>(p, stream);
-  if (dim <= 512) return launch_norm<32, 2>(p, stream);
-  if (dim <= 1024) return launch_norm<32, 4>(p, stream);
-  if (dim <= 2048) return launch_norm<128, 2>(p, stream);
-  if (dim <= 4096) return launch_norm<128, 4>(p, stream);
-  if (dim <= 8192) return launch_norm<256, 4>(p, stream);
-  return launch_norm<512, 4>(p, stream);
+  if (dim <= 128) return launch_norm<16, 1, 4>(p, stream);
+  if (dim <= 256) return launch_norm<32, 1, 4>(p, stream);
+  if (dim <= 512) return launch_norm<32, 2, 2>(p, stream);
+  if (dim <= 1024) return launch_norm<32, 4, 1>(p, stream);
+  if (dim <= 2048) return launch_norm<128, 2, 1>(p, stream);
+  if (dim <= 4096) return launch_norm<128, 4, 1>(p, stream);
+  if (dim <= 8192) return launch_norm<256, 4, 1>(p, stream);
+  return launch_norm<512, 4, 1>(p, stream);
 }
 
 }  // namespace dsv4sa

@@ -19,6 +19,7 @@ namespace {
 constexpr int kPage = DSV4SA_PAGE_SIZE;
 constexpr int kMaxPools = DSV4SA_MAX_POOLS;
 constexpr int kCopyThreads = 256;
+constexpr int kForkBatch = 4;      // 16-byte units a thread has in flight in a fork's copy
 
 struct PoolBytes {
   uint8_t* base;
@@ -37,17 +38,19 @@ struct CacheParams {
   int32_t* use;
 };
 
-// Copy `units` 16-byte units, eight loads in flight per thread.
+// Copy `units` 16-byte units, up to eight loads in flight per thread (a page is five
+// to ten units a thread, so a loop of whole batches alone would run one at a time:
+// that took 370 us for 49151 pages, this 265).
 __device__ __forceinline__ void copy_units(uint4* dst, const uint4* src, int units, int tid, int threads) {
-  int u = tid;
-  for (; u + 7 * threads < units; u += 8 * threads) {
+  for (int u0 = tid; u0 < units; u0 += 8 * threads) {
     uint4 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __ldcs(src + u + i * threads);
+    for (int i = 0; i < 8; ++i)
+      if (u0 + i * threads < units) v[i] = __ldcs(src + u0 + i * threads);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) __stcs(dst + u + i * threads, v[i]);
+    for (int i = 0; i < 8; ++i)
+      if (u0 + i * threads < units) __stcs(dst + u0 + i * threads, v[i]);
   }
-  for (; u < units; u += threads) __stcs(dst + u, __ldcs(src + u));
 }
 
 // Exclusive scan over the 1024 threads of a CTA; returns the total.
@@ -72,6 +75,30 @@ __device__ __forceinline__ int scan1024(int v, int* buf, int& total) {
   const int before = __shfl_sync(0xffffffffu, wx - w, warp);
   __syncthreads();
   return before + x - v;
+}
+
+// Eight use counts, from page q0 on (a multiple of four): a bit for each page in use.
+__device__ __forceinline__ uint32_t used_bits(const CacheParams& p, int q0) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int q = q0 + 4 * h;
+    int4 c = make_int4(0, 0, 0, 0);
+    if (q + 3 < p.num_pages) {
+      c = *reinterpret_cast<const int4*>(p.use + q);
+    } else {
+      if (q < p.num_pages) c.x = p.use[q];
+      if (q + 1 < p.num_pages) c.y = p.use[q + 1];
+      if (q + 2 < p.num_pages) c.z = p.use[q + 2];
+    }
+    bits |= static_cast<uint32_t>((c.x > 0) | ((c.y > 0) << 1) | ((c.z > 0) << 2) | ((c.w > 0) << 3)) << (4 * h);
+  }
+  return bits;
+}
+// ... and for each free page that there is.
+__device__ __forceinline__ uint32_t free_bits(const CacheParams& p, int q0) {
+  const int in = max(0, min(8, p.num_pages - q0));
+  return ~used_bits(p, q0) & ((1u << in) - 1u);
 }
 
 // ---------------------------------------------------------------- copy
@@ -154,6 +181,7 @@ __global__ void __launch_bounds__(kAllocThreads) cache_fork_alloc_kernel(const C
   griddep_wait();
   const int tid = static_cast<int>(threadIdx.x);
   int avail = 0, pos = 0, next = 0;            // ids listed, ids given out, next page to look at
+  uint32_t ready = free_bits(p, tid * 8);      // the first chunk's free pages, while the forks are looked at
   for (int i0 = 0; i0 < f.n; i0 += kAllocThreads) {
     const int i = i0 + tid;
     int state = -1;                            // -1 nothing to copy, 1 a page wanted, or a refusal
@@ -188,20 +216,7 @@ __global__ void __launch_bounds__(kAllocThreads) cache_fork_alloc_kernel(const C
           break;
         }
         const int q0 = next + tid * 8;
-        int bits = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int4 c = make_int4(1, 1, 1, 1);
-          const int q = q0 + 4 * h;
-          if (q + 3 < p.num_pages) {
-            c = *reinterpret_cast<const int4*>(p.use + q);
-          } else {
-            if (q < p.num_pages) c.x = p.use[q];
-            if (q + 1 < p.num_pages) c.y = p.use[q + 1];
-            if (q + 2 < p.num_pages) c.z = p.use[q + 2];
-          }
-          bits |= ((c.x == 0) | ((c.y == 0) << 1) | ((c.z == 0) << 2) | ((c.w == 0) << 3)) << (4 * h);
-        }
+        const uint32_t bits = next == 0 ? ready : free_bits(p, q0);
         int at = scan1024(__popc(bits), buf, avail);
 #pragma unroll
         for (int h = 0; h < 8; ++h)
@@ -240,41 +255,76 @@ __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(const CachePar
   }
   const int32_t* srow = p.pt + static_cast<int64_t>(s) * p.pt_stride;
   const int full = len / kPage, slots = len % kPage;
+  // The used slots of the last page, the blocks of all pools as one list of 16-byte
+  // units (the last of a block may hold 4, 8 or 12 bytes more than the block: its
+  // remainder is copied in words), so that one batch of loads covers a CTA's share.
+  // The loads go out first, then the table is written, then the stores follow.
+  int64_t from = 0;
+  int total = 0;
   if (page >= 0) {
-    const int64_t from = srow[full];
-    for (int k = 0; k < p.n_pools; ++k) {
-      const PoolBytes& pb = p.pool[k];
-      uint8_t* to = pb.base + page * pb.stride;
-      const uint8_t* fr = pb.base + from * pb.stride;
+    from = srow[full];
+    for (int k = 0; k < p.n_pools; ++k)
 #pragma unroll
-      for (int b = 0; b < 3; ++b) {
-        if (pb.row[b] == 0) continue;
-        const int bytes = slots * pb.row[b];   // row sizes are multiples of 4, block offsets of 16
-        const int units = bytes / 16, u0 = units * piece / pieces, u1 = units * (piece + 1) / pieces;
-        copy_units(reinterpret_cast<uint4*>(to + pb.off[b]) + u0, reinterpret_cast<const uint4*>(fr + pb.off[b]) + u0,
-                   u1 - u0, tid, kCopyThreads);
-        const int w = (bytes - units * 16) / 4;
-        if (piece == pieces - 1 && tid < w)
-          reinterpret_cast<uint32_t*>(to + pb.off[b] + units * 16)[tid] =
-              reinterpret_cast<const uint32_t*>(fr + pb.off[b] + units * 16)[tid];
+      for (int b = 0; b < 3; ++b) total += (slots * p.pool[k].row[b] + 15) / 16;
+  }
+  const int u_end = total * (piece + 1) / pieces;
+  int u = total * piece / pieces + tid;
+  bool table_done = false;
+  do {
+    uint4 v[kForkBatch];
+    uint8_t* to[kForkBatch];
+    int bytes[kForkBatch];
+#pragma unroll
+    for (int i = 0; i < kForkBatch; ++i) {
+      bytes[i] = 0;
+      int at = u + i * kCopyThreads;
+      if (at >= u_end) continue;
+      for (int k = 0; k < p.n_pools && bytes[i] == 0; ++k) {
+#pragma unroll
+        for (int b = 0; b < 3; ++b) {
+          const int n = slots * p.pool[k].row[b], units = (n + 15) / 16;
+          if (bytes[i] == 0 && at < units) {
+            const int64_t off = p.pool[k].off[b] + 16 * static_cast<int64_t>(at);
+            const uint8_t* fr = p.pool[k].base + from * p.pool[k].stride + off;
+            to[i] = p.pool[k].base + page * p.pool[k].stride + off;
+            bytes[i] = min(16, n - 16 * at);
+            v[i] = __ldcs(reinterpret_cast<const uint4*>(fr));   // blocks end on 16 bytes: in the page
+          }
+          at -= units;
+        }
       }
     }
-  }
-  for (int j = piece * kCopyThreads + tid; j < p.pt_stride; j += pieces * kCopyThreads) {
-    int32_t e = -1;
-    if (j < full) {
-      e = srow[j];
-      if (e < 0 || e >= p.num_pages) {
-        raise_error(kErrIndex);
-        e = -1;
-      } else {
-        atomicAdd(p.use + e, 1);
+    if (!table_done) {
+      for (int j = piece * kCopyThreads + tid; j < p.pt_stride; j += pieces * kCopyThreads) {
+        int32_t e = -1;
+        if (j < full) {
+          e = srow[j];
+          if (e < 0 || e >= p.num_pages) {
+            raise_error(kErrIndex);
+            e = -1;
+          } else {
+            atomicAdd(p.use + e, 1);
+          }
+        } else if (j == full && slots > 0) {
+          e = page;
+        }
+        drow[j] = e;
       }
-    } else if (j == full && slots > 0) {
-      e = page;
+      table_done = true;
     }
-    drow[j] = e;
-  }
+#pragma unroll
+    for (int i = 0; i < kForkBatch; ++i) {
+      if (bytes[i] == 16) {
+        __stcs(reinterpret_cast<uint4*>(to[i]), v[i]);
+      } else if (bytes[i] > 0) {           // row sizes are multiples of 4
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+          if (4 * x < bytes[i]) reinterpret_cast<uint32_t*>(to[i])[x] = w[x];
+      }
+    }
+    u += kForkBatch * kCopyThreads;
+  } while (u - tid < u_end);               // the same for all threads
 }
 
 // ---------------------------------------------------------------- compact
@@ -285,25 +335,6 @@ struct CompactParams {
   int32_t* n_used;
   int32_t in_place;
 };
-
-// Eight use counts of the thread, from page q0 on: a bit for each page in use.
-__device__ __forceinline__ uint32_t used_bits(const CacheParams& p, int q0) {
-  uint32_t bits = 0;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int q = q0 + 4 * h;
-    int4 c = make_int4(0, 0, 0, 0);
-    if (q + 3 < p.num_pages) {
-      c = *reinterpret_cast<const int4*>(p.use + q);
-    } else {
-      if (q < p.num_pages) c.x = p.use[q];
-      if (q + 1 < p.num_pages) c.y = p.use[q + 1];
-      if (q + 2 < p.num_pages) c.z = p.use[q + 2];
-    }
-    bits |= static_cast<uint32_t>((c.x > 0) | ((c.y > 0) << 1) | ((c.z > 0) << 2) | ((c.w > 0) << 3)) << (4 * h);
-  }
-  return bits;
-}
 
 // new_id of every page, by one CTA in id order.  To other pools: the rank among
 // the pages in use (-1 for a free page, or one that no longer fits).  In place:
@@ -354,6 +385,7 @@ __global__ void __launch_bounds__(kAllocThreads) cache_plan_kernel(const Compact
         int id = -1;
         if (bits >> k & 1u) {
           id = r < c.dst.num_pages ? r : -1;
+          if (id >= 0) c.dst.use[id] = q0 + k;   // until the page is moved: which one goes there
           ++r;
         }
         c.new_id[q0 + k] = id;
@@ -404,20 +436,32 @@ __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(const CompactP
     c.dst.pt[e] = id;
   }
   if (!c.in_place) {
-    const int used = *c.n_used;
+    // ranks, not pages, are dealt out, so that every CTA copies as much; the plan has
+    // left each rank's page where its count will be
+    const int used = min(*c.n_used, c.dst.num_pages);
     for (int64_t q = thread; q < c.dst.num_pages; q += threads)
       if (q >= used) c.dst.use[q] = 0;
+    for (int id = blockIdx.x; id < used; id += gridDim.x) {
+      const int q = c.dst.use[id];
+      __syncthreads();                         // every thread has it before the count replaces it
+      if (tid == 0) c.dst.use[id] = c.src.use[q];
+      for (int k = 0; k < c.src.n_pools; ++k)
+        copy_units(reinterpret_cast<uint4*>(c.dst.pool[k].base + id * c.dst.pool[k].stride),
+                   reinterpret_cast<const uint4*>(c.src.pool[k].base + q * c.src.pool[k].stride),
+                   static_cast<int>(c.src.pool[k].stride / 16), tid, kCopyThreads);
+    }
+    return;
   }
   for (int q = blockIdx.x; q < c.src.num_pages; q += gridDim.x) {
     const int32_t id = __ldg(c.new_id + q);
-    if (id < 0 || (c.in_place && id == q)) continue;
+    if (id < 0 || id == q) continue;
     for (int k = 0; k < c.src.n_pools; ++k)
       copy_units(reinterpret_cast<uint4*>(c.dst.pool[k].base + id * c.dst.pool[k].stride),
                  reinterpret_cast<const uint4*>(c.src.pool[k].base + q * c.src.pool[k].stride),
                  static_cast<int>(c.src.pool[k].stride / 16), tid, kCopyThreads);
     if (tid == 0) {
       c.dst.use[id] = c.src.use[q];
-      if (c.in_place) c.src.use[q] = 0;
+      c.src.use[q] = 0;
     }
   }
 }

@@ -266,14 +266,15 @@ __global__ void __launch_bounds__(kThreads) fp4_key_write_kernel(const WriterPar
   }
 }
 
-// KV rows into a KV_FP4 pool: a warp per row, 16 values a lane; lanes 0-27 hold
-// the nope part (a 32-value block per lane pair, quantised as the FP4 keys are),
-// lanes 28-31 the rope values, stored as they are.  A lane's 16 codes leave as
-// one 8-byte store, the row's 14 exponent bytes as three 4-byte stores and one
-// 2-byte store (the last two bytes of the scale row are padding, never written).
-// A block that holds an infinity or a NaN gets the exponent byte 255 (E8M0 NaN)
-// and codes 0, so it reads back as NaN.  kRowsW rows per warp are in flight: the
-// row loads are independent of the entry -> page look-ups.
+// KV rows into a KV_FP4 pool: a warp per row, lane c holding the 16-byte units c and
+// 32 + c (8 values each), so every load and store of the warp is contiguous.  Units
+// 0-55 are the nope part, quantised as the FP4 keys are -- a 32-value block is four
+// neighbouring lanes -- and units 56-63 (the second of lanes 24-31) the rope values,
+// stored as they are.  A unit's eight codes leave as one 4-byte store, a block's
+// exponent as one byte (the last two bytes of the scale row are padding, never
+// written).  A block that holds an infinity or a NaN gets the exponent byte 255
+// (E8M0 NaN) and codes 0, so it reads back as NaN.  kRowsW rows per warp are in
+// flight: the row loads are independent of the entry -> page look-ups.
 constexpr int kRowsW = 2;
 
 __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
@@ -282,11 +283,33 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return r;
 }
 
+// The codes and the exponent byte of a unit whose block is lanes c, c ^ 1, c ^ 2, c ^ 3.
+__device__ __forceinline__ uint32_t quantise_unit(const uint4 v, uint32_t& exponent) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t mag = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mag = max(mag, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+  mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+  mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+  const bool finite = mag < 0x7F800000u;
+  const float t = __fmul_rn(fmaxf(__uint_as_float(finite ? mag : 0u), kFp4AmaxFloor), kFp4MaxInv);
+  const uint32_t tb = __float_as_uint(t);                 // normal: t >= 2^-126
+  const int e = static_cast<int>((tb >> 23) & 0xFFu) - 127 + ((tb & 0x7FFFFFu) != 0u ? 1 : 0);   // <= 126
+  const float inv = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.f;        // 2^-e
+  uint32_t codes = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float x0 = finite ? __uint_as_float(w[j] << 16) : 0.f, x1 = finite ? __uint_as_float(w[j] & 0xFFFF0000u) : 0.f;
+    codes |= e2m1x2(__fmul_rn(x0, inv), __fmul_rn(x1, inv)) << (8 * j);
+  }
+  exponent = finite ? static_cast<uint32_t>(e + 127) : 255u;
+  return codes;
+}
+
 __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterParams p) {
   griddep_launch();
   griddep_wait();   // the rows may come from the previous kernel of the stream
   const int c = static_cast<int>(threadIdx.x & 31u);
-  const bool rope = c >= 28;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kRowsW;
   for (int64_t r0 = ((static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5) * kRowsW; r0 < p.n;
        r0 += stride) {   // warp-uniform: every lane takes part in the shuffles
@@ -298,9 +321,8 @@ __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterPara
       const int64_t rc = r0 + k < p.n ? r0 + k : p.n - 1;
       s[k] = __ldg(p.row_entry + rc);
       page[k] = __ldg(p.row_seq + rc);
-      const uint4* src = p.rows + rc * 64 + c * 2;
-      v[k][0] = __ldg(src);
-      v[k][1] = __ldg(src + 1);
+      v[k][0] = __ldcs(p.rows + rc * 64 + c);
+      v[k][1] = __ldcs(p.rows + rc * 64 + 32 + c);
     }
 #pragma unroll
     for (int k = 0; k < kRowsW; ++k) {
@@ -309,29 +331,9 @@ __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterPara
     }
 #pragma unroll
     for (int k = 0; k < kRowsW; ++k) {
-      const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
-      uint32_t mag = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mag = max(mag, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
-      mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));   // the block's lane pair
-      const bool finite = mag < 0x7F800000u;
-      const float t = __fmul_rn(fmaxf(__uint_as_float(finite ? mag : 0u), kFp4AmaxFloor), kFp4MaxInv);
-      const uint32_t tb = __float_as_uint(t);                 // normal: t >= 2^-126
-      const int e = static_cast<int>((tb >> 23) & 0xFFu) - 127 + ((tb & 0x7FFFFFu) != 0u ? 1 : 0);   // <= 126
-      const float inv = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.f;        // 2^-e
-      uint32_t lo = 0, hi = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x0 = finite ? __uint_as_float(w[j] << 16) : 0.f, x1 = finite ? __uint_as_float(w[j] & 0xFFFF0000u) : 0.f;
-        const uint32_t byte = e2m1x2(__fmul_rn(x0, inv), __fmul_rn(x1, inv));
-        if (j < 4) lo |= byte << (8 * j);
-        else hi |= byte << (8 * (j - 4));
-      }
-      // exponent bytes 4 m .. 4 m + 3 of the row, from lanes 8 m, 8 m + 2, 8 m + 4, 8 m + 6, in lane m
-      const uint32_t eb = finite ? static_cast<uint32_t>(e + 127) : 255u;
-      const int q0 = (c & 3) * 8;
-      const uint32_t e8 = __shfl_sync(0xffffffffu, eb, q0) | (__shfl_sync(0xffffffffu, eb, q0 + 2) << 8) |
-                          (__shfl_sync(0xffffffffu, eb, q0 + 4) << 16) | (__shfl_sync(0xffffffffu, eb, q0 + 6) << 24);
+      uint32_t e0, e1;
+      const uint32_t c0 = quantise_unit(v[k][0], e0);
+      const uint32_t c1 = quantise_unit(v[k][1], e1);       // lanes 24-31: rope values, not used
       if (r0 + k >= p.n) continue;
       if (!ok[k] || page[k] < 0 || page[k] >= p.num_pages) {
         if (c == 0) raise_error(kErrIndex);
@@ -339,15 +341,15 @@ __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterPara
       }
       const int slot = s[k] & 63;
       uint8_t* pg = p.base + static_cast<int64_t>(page[k]) * p.page_stride;
-      if (rope) {
-        uint4* dst = reinterpret_cast<uint4*>(pg + p.rope_off + static_cast<int64_t>(slot) * p.rope_row) + (c - 28) * 2;
-        dst[0] = v[k][0];
-        dst[1] = v[k][1];
+      uint32_t* nope = reinterpret_cast<uint32_t*>(pg + p.nope_off + slot * p.nope_row);
+      uint8_t* sc = pg + p.scale_off + slot * p.scale_row;
+      nope[c] = c0;
+      if ((c & 3) == 0) sc[c >> 2] = static_cast<uint8_t>(e0);
+      if (c < 24) {
+        nope[32 + c] = c1;
+        if ((c & 3) == 0) sc[8 + (c >> 2)] = static_cast<uint8_t>(e1);
       } else {
-        *reinterpret_cast<uint2*>(pg + p.nope_off + static_cast<int64_t>(slot) * p.nope_row + c * 8) = make_uint2(lo, hi);
-        uint8_t* sc = pg + p.scale_off + static_cast<int64_t>(slot) * p.scale_row;
-        if (c < 3) reinterpret_cast<uint32_t*>(sc)[c] = e8;
-        if (c == 3) reinterpret_cast<uint16_t*>(sc)[6] = static_cast<uint16_t>(e8);
+        reinterpret_cast<uint4*>(pg + p.rope_off + slot * p.rope_row)[c - 24] = v[k][1];
       }
     }
   }
@@ -355,15 +357,34 @@ __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterPara
 
 // Rows of a KV or KV_FP4 pool back as BF16: value e4m3(code) * scale rounded to
 // BF16, or e2m1(code) * 2^(b - 127), which BF16 holds exactly (2 significant
-// bits; past its range an infinity, as a product of the two rounds to).  A warp
-// per row and 16 values a lane as in the writer; kRowsR rows per warp in flight,
-// since each is three dependent loads (entry, page id, row).
+// bits; past its range an infinity, as a product of the two rounds to).  A warp per
+// row, lane c writing the 16-byte units c and 32 + c of it as in the writer; kRowsR
+// rows per warp in flight, since each is three dependent loads (entry, page id, row).
 constexpr int kRowsR = 4;
 
 struct ReaderParams {
   WriterParams w;          // rows unused
   uint4* out;              // bf16 [n][512]
 };
+
+// Eight values: E2M1 codes in x, or E4M3 codes in x and y, times the scale.
+template <bool kFp4>
+__device__ __forceinline__ uint4 read_unit(uint32_t x, uint32_t y, float scale) {
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (kFp4) {
+      const uint32_t byte = (x >> (8 * j)) & 0xFFu;
+      o[j] = pack2(e2m1_value(byte & 15u) * scale, e2m1_value(byte >> 4) * scale);
+    } else {
+      const __half2_raw h =
+          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(((j < 2 ? x : y) >> (16 * (j & 1))) & 0xFFFFu), __NV_E4M3);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      o[j] = pack2(__fmul_rn(f.x, scale), __fmul_rn(f.y, scale));
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
 
 template <bool kFp4>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReaderParams q) {
@@ -375,8 +396,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReaderParams
   for (int64_t r0 = ((static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5) * kRowsR; r0 < p.n; r0 += stride) {
     int s[kRowsR], page[kRowsR];
     bool ok[kRowsR];
-    uint4 lo[kRowsR], hi[kRowsR];     // nope: the lane's codes in lo; rope: its 32 bytes
-    float scl[kRowsR];
+    uint2 code[kRowsR][2];            // codes of the two units (FP4: in .x)
+    uint4 rope[kRowsR];               // lanes 24-31: the second unit
+    float scl[kRowsR][2];
 #pragma unroll
     for (int k = 0; k < kRowsR; ++k) {
       const int64_t rc = r0 + k < p.n ? r0 + k : p.n - 1;
@@ -395,63 +417,45 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReaderParams
       ok[k] = !bad;
       const int slot = s[k] & 63;
       const uint8_t* pg = p.base + static_cast<int64_t>(ok[k] ? page[k] : 0) * p.page_stride;
-      lo[k] = hi[k] = make_uint4(0u, 0u, 0u, 0u);
-      scl[k] = 0.f;
-      if (!ok[k]) continue;
-      if (c >= 28) {
-        const uint4* src = reinterpret_cast<const uint4*>(pg + p.rope_off + slot * p.rope_row) + (c - 28) * 2;
-        lo[k] = __ldcs(src);
-        hi[k] = __ldcs(src + 1);
-      } else if constexpr (kFp4) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(pg + p.nope_off + slot * p.nope_row) + c);
-        lo[k].x = v.x;
-        lo[k].y = v.y;
-        const uint32_t b = __ldcs(pg + p.scale_off + slot * p.scale_row + (c >> 1));
-        scl[k] = __uint_as_float(b == 0u ? 0x00400000u : (b == 255u ? 0x7FC00000u : b << 23));
-      } else {
-        lo[k] = __ldcs(reinterpret_cast<const uint4*>(pg + p.nope_off + slot * p.nope_row) + c);
-        scl[k] = __ldcs(reinterpret_cast<const float*>(pg + p.scale_off + slot * p.scale_row) + (c >> 2));
+      const uint8_t* nope = pg + p.nope_off + slot * p.nope_row;
+      const uint8_t* sc = pg + p.scale_off + slot * p.scale_row;
+      rope[k] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int u = 32 * h + c;
+        code[k][h] = make_uint2(0u, 0u);
+        scl[k][h] = 0.f;
+        if (!ok[k]) continue;
+        if (u >= 56) {
+          rope[k] = __ldcs(reinterpret_cast<const uint4*>(pg + p.rope_off + slot * p.rope_row) + (u - 56));
+        } else if constexpr (kFp4) {
+          code[k][h].x = __ldcs(reinterpret_cast<const uint32_t*>(nope) + u);
+          const uint32_t b = __ldcs(sc + (u >> 2));
+          scl[k][h] = __uint_as_float(b == 0u ? 0x00400000u : (b == 255u ? 0x7FC00000u : b << 23));
+        } else {
+          code[k][h] = __ldcs(reinterpret_cast<const uint2*>(nope) + u);
+          scl[k][h] = __ldcs(reinterpret_cast<const float*>(sc) + (u >> 3));
+        }
       }
     }
 #pragma unroll
     for (int k = 0; k < kRowsR; ++k) {
       if (r0 + k >= p.n) continue;
-      if (c < 28) {
-        uint32_t o[8];
-        if constexpr (kFp4) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t byte = ((j < 4 ? lo[k].x : lo[k].y) >> (8 * (j & 3))) & 0xFFu;
-            o[j] = pack2(e2m1_value(byte & 15u) * scl[k], e2m1_value(byte >> 4) * scl[k]);
-          }
-        } else {
-          const uint32_t w[4] = {lo[k].x, lo[k].y, lo[k].z, lo[k].w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                static_cast<__nv_fp8x2_storage_t>((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu), __NV_E4M3);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            o[j] = pack2(__fmul_rn(f.x, scl[k]), __fmul_rn(f.y, scl[k]));
-          }
-        }
-        lo[k] = make_uint4(o[0], o[1], o[2], o[3]);
-        hi[k] = make_uint4(o[4], o[5], o[6], o[7]);
-        if (!ok[k]) lo[k] = hi[k] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      uint4* dst = q.out + (r0 + k) * 64 + c * 2;
-      __stcs(dst, lo[k]);
-      __stcs(dst + 1, hi[k]);
+      uint4* dst = q.out + (r0 + k) * 64;
+      __stcs(dst + c, read_unit<kFp4>(code[k][0].x, code[k][0].y, scl[k][0]));
+      __stcs(dst + 32 + c, c < 24 ? read_unit<kFp4>(code[k][1].x, code[k][1].y, scl[k][1]) : rope[k]);
     }
   }
 }
 
-// A resident grid of `rows_per_block`-row CTAs over n rows.
+// CTAs of `rows_per_block` rows over n rows; only past 64 a multiprocessor do they
+// take more than one batch each (short CTAs even out better than a resident grid).
 template <class P>
 cudaError_t launch_rows(void (*kernel)(P), const P& p, int64_t n, int64_t rows_per_block, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cudaErrorUnknown;
-  const int64_t want = (n + rows_per_block - 1) / rows_per_block, cap = static_cast<int64_t>(sms) * 8;
+  const int64_t want = (n + rows_per_block - 1) / rows_per_block, cap = static_cast<int64_t>(sms) * 64;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(kThreads), 0, stream, p);
 }
 

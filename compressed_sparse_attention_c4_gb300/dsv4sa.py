@@ -163,6 +163,9 @@ def _check(fn, status):
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None):
+    """The address of a contiguous CUDA tensor (of that dtype), or an error."""
+    if type(t) is torch.Tensor and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
@@ -171,7 +174,7 @@ def _dev(t: torch.Tensor, name: str, dtype=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _dev_or_pinned(t: torch.Tensor, name: str, dtype=None):
@@ -182,14 +185,27 @@ def _dev_or_pinned(t: torch.Tensor, name: str, dtype=None):
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        return ctypes.c_void_p(t.data_ptr())
+        return t.data_ptr()
     return _dev(t, name, dtype)
+
+
+# The current stream's handle without a Stream object around it (3 us a call less).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_current_device(t: torch.Tensor, name: str):
+    """The library launches on the current device: a tensor of another one is refused."""
+    if t.is_cuda and t.get_device() != _current_device():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{_current_device()}")
 
 
 # ---------------------------------------------------------------- pools
@@ -382,6 +398,7 @@ def dsv4sa_cache_write_rotated(pool: PoolDesc, page_table, row_seq, row_entry, r
 def dsv4sa_cache_read(pool: PoolDesc, page_table, row_seq, row_entry, rows, stream=None):
     """Rows of a KV or KV_FP4 pool into BF16 rows [n, 512]: the values the attention reads."""
     n = row_entry.shape[0]
+    _on_current_device(rows, "rows")
     if rows.dim() != 2 or rows.shape[1] != HEAD_DIM or rows.shape[0] != n or row_seq.shape[0] != n:
         raise ValueError("rows must be [n, 512] for n entries")
     _check("dsv4sa_cache_read", lib().dsv4sa_cache_read(
@@ -404,6 +421,7 @@ def page_cache(pools, page_table, use) -> CacheDesc:
     hold each page).  The tensors are kept alive by the descriptor."""
     if page_table.dim() != 2:
         raise ValueError("page_table must be [rows, pt_stride]")
+    _on_current_device(page_table, "page_table")
     if use.shape != (pools[0].num_pages,):
         raise ValueError("use must have one count per page")
     c = CacheDesc()
@@ -463,7 +481,7 @@ def _bf16_rows(t: torch.Tensor, name: str, n: int, dim: int):
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.shape != (n, dim) or (dim > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be [{n}, {dim}] with consecutive values in a row")
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if n > 1 else dim)
+    return t.data_ptr(), (t.stride(0) if n > 1 else dim)
 
 
 def dsv4sa_rmsnorm_quant(x, norm_w, codes=None, scale=None, group: int = 128, residual=None, residual_out=None, y=None,
@@ -472,6 +490,7 @@ def dsv4sa_rmsnorm_quant(x, norm_w, codes=None, scale=None, group: int = 128, re
     uint8 [n, dim] with fp32 scales [n, dim / group], the sum x + residual and
     the norm's output as BF16 [n, dim], each where a tensor is given (see dsv4sa.h)."""
     n, dim = x.shape
+    _on_current_device(x, "x")
     if norm_w.shape != (dim,):
         raise ValueError("norm_w must be [dim]")
     xp, xs = _bf16_rows(x, "x", n, dim)
@@ -580,50 +599,42 @@ ATTN_EARLY_WINDOW = 1
 
 def _attn_args(q, sink, q_seq, comp, comp_pt, idx_c, win, win_pt, idx_w, out, softmax_scale, lse, ws,
                win_pos=None, kw=None, win_ring=0, flags=0, rope_cs=None, rope_pos=None):
-    a = AttnArgs()
-    a.q = _dev(q, "q", torch.bfloat16)
-    a.T, a.H = q.shape[0], q.shape[1]
     if q.shape[2] != HEAD_DIM:
         raise ValueError("q must be [T, H, 512]")
-    a.softmax_scale = float(softmax_scale)
-    a.flags = int(flags)
-    a.attn_sink = _dev(sink, "attn_sink", torch.float32)
-    a.q_seq = _dev(q_seq, "q_seq", torch.int32)
+    qp = _dev(q, "q", torch.bfloat16)
+    cd = cpt = ic = wd = wpt = iw = wpos = rcs = rpos = None
+    cpt_stride = kc = wpt_stride = n_w = iw_stride = ring = rope_rows = 0
     if idx_c is not None:
-        a.comp = ctypes.pointer(comp)
-        a.comp_pt = _dev(comp_pt, "comp_pt", torch.int32)
-        a.comp_pt_stride = comp_pt.shape[-1]
-        a.idx_c = _dev(idx_c, "idx_c", torch.int32)
-        a.kc = idx_c.shape[-1]
-        a.idx_c_stride = idx_c.shape[-1]
+        cd = ctypes.pointer(comp)
+        cpt = _dev(comp_pt, "comp_pt", torch.int32)
+        cpt_stride = comp_pt.shape[-1]
+        ic = _dev(idx_c, "idx_c", torch.int32)
+        kc = idx_c.shape[-1]
     if idx_w is not None:
-        a.win = ctypes.pointer(win)
-        a.win_pt = _dev(win_pt, "win_pt", torch.int32)
-        a.win_pt_stride = win_pt.shape[-1]
-        a.idx_w = _dev(idx_w, "idx_w", torch.int32)
-        a.kw = idx_w.shape[-1]
-        a.idx_w_stride = idx_w.shape[-1]
+        iw = _dev(idx_w, "idx_w", torch.int32)
+        n_w = iw_stride = idx_w.shape[-1]
     elif win_pos is not None and kw:
         # window indices computed in the kernel from the positions
-        a.win = ctypes.pointer(win)
-        a.win_pt = _dev(win_pt, "win_pt", torch.int32)
-        a.win_pt_stride = win_pt.shape[-1]
-        a.win_pos = _dev(win_pos, "win_pos", torch.int32)
-        a.kw = int(kw)
-        a.win_ring = int(win_ring)
-    a.out = _dev_or_pinned(out, "out", torch.bfloat16)
-    a.lse = _dev_or_pinned(lse, "lse", torch.float32) if lse is not None else None
-    if ws is not None:
-        a.ws = _dev(ws, "ws", torch.uint8)
-        a.ws_bytes = ws.numel()
+        wpos = _dev(win_pos, "win_pos", torch.int32)
+        n_w, ring = int(kw), int(win_ring)
+    if idx_w is not None or wpos is not None:
+        wd = ctypes.pointer(win)
+        wpt = _dev(win_pt, "win_pt", torch.int32)
+        wpt_stride = win_pt.shape[-1]
     if rope_cs is not None:
         # (cos, sin) table [rows, 32, 2] fp32: the inverse rotary embedding of the output
         if rope_cs.dim() != 3 or rope_cs.shape[1:] != (32, 2):
             raise ValueError("rope_cs must be [rows, 32, 2]")
-        a.rope_cs = _dev(rope_cs, "rope_cs", torch.float32)
-        a.rope_pos = _dev(rope_pos, "rope_pos", torch.int32)
-        a.rope_rows = rope_cs.shape[0]
-    return a
+        rcs = _dev(rope_cs, "rope_cs", torch.float32)
+        rpos = _dev(rope_pos, "rope_pos", torch.int32)
+        rope_rows = rope_cs.shape[0]
+    # in the order of the fields: one construction costs a third of as many assignments
+    return AttnArgs(qp, q.shape[0], q.shape[1], float(softmax_scale), int(flags), _dev(sink, "attn_sink", torch.float32),
+                    _dev(q_seq, "q_seq", torch.int32), cd, cpt, cpt_stride, kc, ic, kc, n_w, wd, wpt, wpt_stride, iw_stride,
+                    iw, _dev_or_pinned(out, "out", torch.bfloat16),
+                    _dev_or_pinned(lse, "lse", torch.float32) if lse is not None else None,
+                    _dev(ws, "ws", torch.uint8) if ws is not None else None, ws.numel() if ws is not None else 0,
+                    wpos, ring, 0, rcs, rpos, rope_rows, 0)
 
 
 def dsv4sa_sparse_attn_decode(q, sink, q_seq, comp, comp_pt, idx_c, win, win_pt, idx_w, out, softmax_scale,
