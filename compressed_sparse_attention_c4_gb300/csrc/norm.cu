@@ -6,14 +6,17 @@
 // fp32 for the norm; the residual stream's new value is s rounded to BF16.
 //
 // One pass: a row stays in registers between its sum of squares and its codes.
-// kTpr threads share a row (16 lanes for an indexer head of 128 values, up to
+// kTpr threads share a row (8 lanes for an indexer head of 128 values, up to
 // 512 threads for 16384), each holding kUnits 16-byte units, unit i of a thread
 // being unit i kTpr + (its index) of the row, so loads and stores are coalesced
 // and a block's 8 or 16 units are neighbouring lanes of one warp: its absmax is
 // three or four shuffles.  The grid is resident and walks the rows; the weights
-// of a thread's columns are loaded once.  To keep reads in flight a long row's
-// successor is loaded before the row is reduced, and short rows go several at a
-// time (a row of 128 is one 16-byte load a thread).
+// of a thread's columns are loaded once, and the next row's units before the
+// current row is reduced, so reads stay in flight.  Rows of up to 512 are bound by
+// their instructions as much as by HBM: two units a thread instead of one halve the
+// shuffles and addresses a value, packed fp32 the arithmetic, and 64 registers leave
+// 32 warps a multiprocessor (262144 rows of 128: 41 us before these, 18.6 with them,
+// 15.2 at the copy's rate; several rows a thread at once took 23 to 31).
 #include <atomic>
 
 #include "common.cuh"
@@ -42,27 +45,24 @@ struct NormParams {
   float eps;
 };
 
-__device__ __forceinline__ void unpack8(const uint4 v, float* f) {
+__device__ __forceinline__ void unpack8(const uint4 v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f) {
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[i].x, f[i].y);
     w[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int kTpr, int kUnits, int kRowsAtOnce, bool kRes>
-__global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256) rmsnorm_quant_kernel(const NormParams p) {
+template <int kTpr, int kUnits, bool kRes>
+__global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256, kTpr <= 32 && kUnits <= 2 ? 4 : (kTpr <= 256 ? 2 : 1)) rmsnorm_quant_kernel(const NormParams p) {
   constexpr int kThreads = kTpr > 256 ? kTpr : 256;
   constexpr int kRowsPerCta = kThreads / kTpr;
   constexpr int kWarps = kTpr > 32 ? kTpr / 32 : 1;         // warps that share a row
@@ -71,14 +71,14 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256) rmsnorm_quant_kernel(
   griddep_wait();
   const int tid = static_cast<int>(threadIdx.x);
   const int c = tid % kTpr, sub = tid / kTpr;               // place in the row, row of the CTA
-  float w[kUnits][8];
+  float2 w[kUnits][4];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const int u = i * kTpr + c;
     const float4 a = u < p.units ? __ldg(p.w + 2 * u) : make_float4(0.f, 0.f, 0.f, 0.f);
     const float4 b = u < p.units ? __ldg(p.w + 2 * u + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-    w[i][0] = a.x, w[i][1] = a.y, w[i][2] = a.z, w[i][3] = a.w;
-    w[i][4] = b.x, w[i][5] = b.y, w[i][6] = b.z, w[i][7] = b.w;
+    w[i][0] = make_float2(a.x, a.y), w[i][1] = make_float2(a.z, a.w);
+    w[i][2] = make_float2(b.x, b.y), w[i][3] = make_float2(b.z, b.w);
   }
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRowsPerCta;
@@ -96,20 +96,22 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256) rmsnorm_quant_kernel(
   // one row, from the units in xv and rv; `next` loads the row after it in between
   auto process = [&](int64_t row, uint4 (&xv)[kUnits], uint4 (&rv)[kUnits], int64_t next) {
     const bool live = row < p.n;
-    float s[kUnits][8];
-    float sq = 0.f;
+    float2 s[kUnits][4];
+    float2 sq2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      float r[8];
       unpack8(xv[i], s[i]);
-      if constexpr (kRes) unpack8(rv[i], r);
+      if constexpr (kRes) {
+        float2 r[4];
+        unpack8(rv[i], r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (kRes) s[i][j] += r[j];
-        sq = fmaf(s[i][j], s[i][j], sq);
+        for (int j = 0; j < 4; ++j) s[i][j] = make_float2(s[i][j].x + r[j].x, s[i][j].y + r[j].y);
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sq2 = fma2(s[i][j], s[i][j], sq2);
     }
-    if constexpr (kRowsAtOnce == 1) load(next, xv, rv);   // in flight while this row is reduced
+    float sq = sq2.x + sq2.y;
+    load(next, xv, rv);    // in flight while this row is reduced
 #pragma unroll
     for (int o = (kTpr < 32 ? kTpr : 32) / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
     if constexpr (kWarps > 1) {
@@ -120,62 +122,77 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256) rmsnorm_quant_kernel(
       for (int i = 0; i < kWarps; ++i) sq += part[buf][sub][i];
       buf ^= 1;            // the other copy: no thread writes it before every thread passed this barrier
     }
-    const float rstd = __frsqrt_rn(fmaf(sq, p.inv_dim, p.eps));
+    // 1 / sqrt by the hardware's estimate and one Newton step (relative 2^-23)
+    const float ms = fmaf(sq, p.inv_dim, p.eps);
+    const float r0 = rsqrtf(ms);
+    const float rstd = ms > 0.f && ms < INFINITY ? r0 * fmaf(-0.5f * ms * r0, r0, 1.5f) : r0;
+    const float2 rstd2 = make_float2(rstd, rstd);
+    const int64_t out0 = row * p.units + c;                  // this thread's first unit of the outputs
+    float top[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const bool in = live && i * kTpr + c < p.units;
+      if (in && p.sum) __stcs(p.sum + out0 + i * kTpr, pack8(s[i]));
+      top[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = mul2(s[i][j], w[i][j]);                    // t = s w; y = t rstd
+        top[i] = fmaxf(top[i], fmaxf(fabsf(s[i][j].x), fabsf(s[i][j].y)));
+      }
+      if (in && p.y) {
+        float2 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = mul2(s[i][j], rstd2);
+        __stcs(p.y + out0 + i * kTpr, pack8(y));
+      }
+    }
+    if (!p.codes) return;
+    // absmax of a block: its 8 units are neighbouring lanes, its 16 units twice as many,
+    // or with eight threads a row the same lanes' next units
+    if (kTpr == 8 && p.group_units == 16) {
+#pragma unroll
+      for (int i = 0; i + 1 < kUnits; i += 2) top[i] = top[i + 1] = fmaxf(top[i], top[i + 1]);
+    }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int u = i * kTpr + c;
       const bool in = live && u < p.units;
-      if (in && p.sum) __stcs(p.sum + row * p.units + u, pack8(s[i]));
-      float amax = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[i][j] = s[i][j] * rstd * w[i][j];
-        amax = fmaxf(amax, fabsf(s[i][j]));
-      }
-      if (in && p.y) __stcs(p.y + row * p.units + u, pack8(s[i]));
-      if (p.codes) {
+      {
+        float amax = top[i];                                 // of t
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-        if (p.group_units == 16) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
-        const float scale = __fmul_rn(fmaxf(amax, kAmaxFloor), kFp8MaxInv);
-        // y itself carries fp32 roundings, so a multiply by the rounded
-        // reciprocal instead of a division moves a code only where y is already
-        // within them of a tie; the conversion saturates at +-448
-        const float inv = __frcp_rn(scale);
+        if (kTpr > 8 && p.group_units == 16) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+        const float scale = __fmul_rn(fmaxf(amax * rstd, kAmaxFloor), kFp8MaxInv);
+        // y / scale = t (448 / amax(t)), in which the row's factor cancels (unless the
+        // block is below the floor): three roundings from the sum to the code, where
+        // norm, weight, scale and quotient in turn take five.  The quotient is the
+        // hardware's estimate with its residual added; the conversion saturates.
+        const float r = __fdividef(1.f, amax), k0 = 448.f * r;
+        const float inv = amax * rstd > kAmaxFloor ? fmaf(fmaf(-amax, k0, 448.f), r, k0) : rstd * (448.f / kAmaxFloor);
+        const float2 inv2 = make_float2(inv, inv);
         uint32_t q[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(s[i][4 * h] * inv, s[i][4 * h + 1] * inv),
-                                                       __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(s[i][4 * h + 2] * inv, s[i][4 * h + 3] * inv),
-                                                       __NV_SATFINITE, __NV_E4M3);
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(s[i][2 * h], inv2), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(s[i][2 * h + 1], inv2), __NV_SATFINITE, __NV_E4M3);
           q[h] = lo | (hi << 16);
         }
         if (in) {
-          __stcs(p.codes + row * p.units + u, make_uint2(q[0], q[1]));
-          if ((u & (p.group_units - 1)) == 0) p.scale[row * (p.units / p.group_units) + u / p.group_units] = scale;
+          __stcs(p.codes + out0 + i * kTpr, make_uint2(q[0], q[1]));
+          if ((u & (p.group_units - 1)) == 0) p.scale[(row * p.units + u) >> (p.group_units == 16 ? 4 : 3)] = scale;
         }
       }
     }
   };
   // the first row of the CTA decides: every thread takes part in shuffles and barriers
   int64_t first = static_cast<int64_t>(blockIdx.x) * kRowsPerCta;
-  uint4 xv[kRowsAtOnce][kUnits], rv[kRowsAtOnce][kUnits];
-  if constexpr (kRowsAtOnce == 1) {
-    load(first + sub, xv[0], rv[0]);
-    for (; first < p.n; first += step) process(first + sub, xv[0], rv[0], first + sub + step);
-  } else {
-    for (; first < p.n; first += kRowsAtOnce * step) {
-#pragma unroll
-      for (int k = 0; k < kRowsAtOnce; ++k) load(first + sub + k * step, xv[k], rv[k]);
-#pragma unroll
-      for (int k = 0; k < kRowsAtOnce; ++k) process(first + sub + k * step, xv[k], rv[k], 0);
-    }
-  }
+  uint4 xv[kUnits], rv[kUnits];
+  load(first + sub, xv, rv);
+  for (; first < p.n; first += step) process(first + sub, xv, rv, first + sub + step);
 }
 
-template <int kTpr, int kUnits, int kRowsAtOnce, bool kRes>
+template <int kTpr, int kUnits, bool kRes>
 int launch_norm_r(const NormParams& p, cudaStream_t stream) {
   constexpr int kThreads = kTpr > 256 ? kTpr : 256;
   constexpr int kRowsPerCta = kThreads / kTpr;
@@ -185,26 +202,23 @@ int launch_norm_r(const NormParams& p, cudaStream_t stream) {
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DSV4SA_ERR_CUDA;
   if (resident == 0) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-            &resident, rmsnorm_quant_kernel<kTpr, kUnits, kRowsAtOnce, kRes>, kThreads, 0) != cudaSuccess)
+            &resident, rmsnorm_quant_kernel<kTpr, kUnits, kRes>, kThreads, 0) != cudaSuccess)
       return DSV4SA_ERR_CUDA;
     if (resident < 1) resident = 1;
     cached.store(resident, std::memory_order_relaxed);
   }
-  // A CTA for each kRowsPerCta rows while there are few; a resident grid that keeps
-  // the weights in registers for long rows; for short ones (whose weights are a few
-  // cached lines) CTAs of a few batches each, which even out better
   const int64_t want = (static_cast<int64_t>(p.n) + kRowsPerCta - 1) / kRowsPerCta;
-  const int64_t full = static_cast<int64_t>(sms) * resident * (kRowsAtOnce > 1 ? 4 : 1);
-  return launch_pdl(rmsnorm_quant_kernel<kTpr, kUnits, kRowsAtOnce, kRes>,
+  const int64_t full = static_cast<int64_t>(sms) * resident;
+  return launch_pdl(rmsnorm_quant_kernel<kTpr, kUnits, kRes>,
                     dim3(static_cast<unsigned>(want < full ? want : full)), dim3(kThreads), 0, stream, p) == cudaSuccess
              ? DSV4SA_OK
              : DSV4SA_ERR_CUDA;
 }
 
-template <int kTpr, int kUnits, int kRowsAtOnce>
+template <int kTpr, int kUnits>
 int launch_norm(const NormParams& p, cudaStream_t stream) {
-  return p.r ? launch_norm_r<kTpr, kUnits, kRowsAtOnce, true>(p, stream)
-             : launch_norm_r<kTpr, kUnits, kRowsAtOnce, false>(p, stream);
+  return p.r ? launch_norm_r<kTpr, kUnits, true>(p, stream)
+             : launch_norm_r<kTpr, kUnits, false>(p, stream);
 }
 
 }  // namespace
@@ -228,14 +242,14 @@ int launch_rmsnorm_quant(const void* x, int64_t x_stride, const void* residual, 
   p.inv_dim = 1.0f / static_cast<float>(dim);
   p.eps = eps;
   // the fewest threads whose registers hold the row in at most four units each
-  if (dim <= 128) return launch_norm<16, 1, 4>(p, stream);
-  if (dim <= 256) return launch_norm<32, 1, 4>(p, stream);
-  if (dim <= 512) return launch_norm<32, 2, 2>(p, stream);
-  if (dim <= 1024) return launch_norm<32, 4, 1>(p, stream);
-  if (dim <= 2048) return launch_norm<128, 2, 1>(p, stream);
-  if (dim <= 4096) return launch_norm<128, 4, 1>(p, stream);
-  if (dim <= 8192) return launch_norm<256, 4, 1>(p, stream);
-  return launch_norm<512, 4, 1>(p, stream);
+  if (dim <= 128) return launch_norm<8, 2>(p, stream);
+  if (dim <= 256) return launch_norm<16, 2>(p, stream);
+  if (dim <= 512) return launch_norm<32, 2>(p, stream);
+  if (dim <= 1024) return launch_norm<32, 4>(p, stream);
+  if (dim <= 2048) return launch_norm<128, 2>(p, stream);
+  if (dim <= 4096) return launch_norm<128, 4>(p, stream);
+  if (dim <= 8192) return launch_norm<256, 4>(p, stream);
+  return launch_norm<512, 4>(p, stream);
 }
 
 }  // namespace dsv4sa

@@ -53,6 +53,29 @@ __device__ __forceinline__ void copy_units(uint4* dst, const uint4* src, int uni
   }
 }
 
+// Page `to` of every pool of d = page `from` of s's, by a CTA: one list of 16-byte
+// units over the pools, eight in flight a thread.
+__device__ __forceinline__ void copy_page(const CacheParams& d, int64_t to, const CacheParams& s, int64_t from, int tid) {
+  int total = 0;
+  for (int k = 0; k < s.n_pools; ++k) total += static_cast<int>(s.pool[k].stride / 16);
+  for (int u0 = tid; u0 < total; u0 += 8 * kCopyThreads) {
+    uint4 v[8];
+    uint4* dst[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      int at = u0 + i * kCopyThreads;
+      if (at >= total) continue;
+      int k = 0;
+      for (; at >= static_cast<int>(s.pool[k].stride / 16); ++k) at -= static_cast<int>(s.pool[k].stride / 16);
+      dst[i] = reinterpret_cast<uint4*>(d.pool[k].base + to * d.pool[k].stride) + at;
+      v[i] = __ldcs(reinterpret_cast<const uint4*>(s.pool[k].base + from * s.pool[k].stride) + at);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (u0 + i * kCopyThreads < total) __stcs(dst[i], v[i]);
+  }
+}
+
 // Exclusive scan over the 1024 threads of a CTA; returns the total.
 __device__ __forceinline__ int scan1024(int v, int* buf, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -336,86 +359,109 @@ struct CompactParams {
   int32_t in_place;
 };
 
-// new_id of every page, by one CTA in id order.  To other pools: the rank among
-// the pages in use (-1 for a free page, or one that no longer fits).  In place:
-// pages below the number in use stay, the k-th one at or above it goes to the
-// k-th free page below it.  The free pages' list of that case is kept in
-// new_id[n_used ..] until its entries are replaced: the k-th page to move has an
-// id of at least n_used + k, so the chunks are walked from the highest ids down
-// and an entry is read before anything at or above its place is written.
+// new_id of every page when they go to other pools: the rank among the pages in use
+// (-1 for a free page, or one that does not fit).  A cluster of eight CTAs, each with a
+// contiguous share of the counts: it counts its pages in use, learns the counts before
+// it through distributed shared memory, and ranks its pages.
+constexpr int kPlanCtas = 8;
+
 __global__ void __launch_bounds__(kAllocThreads) cache_plan_kernel(const CompactParams c) {
+  __shared__ int buf[32];
+  __shared__ int counts[kPlanCtas];
+  griddep_launch();
+  griddep_wait();
+  const int tid = static_cast<int>(threadIdx.x), r = static_cast<int>(cluster_ctarank());
+  const int P = c.src.num_pages;
+  const int share = ((P + kPlanCtas - 1) / kPlanCtas + 7) & ~7;
+  const int p0 = min(P, r * share), p1 = min(P, p0 + share);   // p0 a multiple of 8, or P
+  auto bits_at = [&](int q0) {                                 // of the thread's eight pages inside the share
+    return q0 < p1 ? used_bits(c.src, q0) & ((1u << min(8, p1 - q0)) - 1u) : 0u;
+  };
+  const uint32_t first = bits_at(p0 + tid * 8);                // most shares are one chunk: read once
+  int mine = __popc(first), total;
+  for (int q0 = p0 + kAllocChunk + tid * 8; q0 < p1; q0 += kAllocChunk) mine += __popc(bits_at(q0));
+  scan1024(mine, buf, total);
+  cluster_sync();                              // every CTA runs before its shared memory is written
+  if (tid < kPlanCtas) st_cluster_u32(cluster_map(smem_u32(counts + r), static_cast<uint32_t>(tid)), static_cast<uint32_t>(total));
+  cluster_sync();
+  int base = 0, all = 0;
+#pragma unroll
+  for (int k = 0; k < kPlanCtas; ++k) {
+    base += k < r ? counts[k] : 0;
+    all += counts[k];
+  }
+  for (int c0 = p0; c0 < p1; c0 += kAllocChunk) {
+    const int q0 = c0 + tid * 8;
+    const uint32_t bits = c0 == p0 ? first : bits_at(q0);
+    int t;
+    int rank = base + scan1024(__popc(bits), buf, t);
+    base += t;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (q0 + k >= p1) continue;
+      int id = -1;
+      if (bits >> k & 1u) {
+        id = rank < c.dst.num_pages ? rank : -1;
+        if (id >= 0) c.dst.use[id] = q0 + k;   // until the page is moved: which one goes there
+        ++rank;
+      }
+      c.new_id[q0 + k] = id;
+    }
+  }
+  if (r == 0 && tid == 0) {
+    *c.n_used = all;
+    if (all > c.dst.num_pages) raise_error(kErrPages);
+  }
+}
+
+// ... and in place, by one CTA: pages below the number in use stay, the k-th one at or
+// above it goes to the k-th free page below it.  The free pages' list is kept in
+// new_id[n_used ..] until its entries are replaced: the k-th page to move has an id of
+// at least n_used + k, so the chunks are walked from the highest ids down and an
+// entry is read before anything at or above its place is written.
+__global__ void __launch_bounds__(kAllocThreads) cache_plan_in_place_kernel(const CompactParams c) {
   __shared__ int buf[32];
   griddep_launch();
   griddep_wait();
   const int tid = static_cast<int>(threadIdx.x);
   const int P = c.src.num_pages;
-  int total = 0;
-  if (c.in_place) {
-    int mine = 0;
-    for (int q0 = tid * 8; q0 < P; q0 += kAllocChunk) mine += __popc(used_bits(c.src, q0));
-    scan1024(mine, buf, total);
-  }
-  const int limit = c.in_place ? total : P;
-  int base = 0, holes = 0;
-  for (int c0 = 0; c0 < limit; c0 += kAllocChunk) {
+  int total = 0, mine = 0;
+  for (int q0 = tid * 8; q0 < P; q0 += kAllocChunk) mine += __popc(used_bits(c.src, q0));
+  scan1024(mine, buf, total);
+  int holes = 0;
+  for (int c0 = 0; c0 < total; c0 += kAllocChunk) {
     const int q0 = c0 + tid * 8;
-    uint32_t bits = used_bits(c.src, q0);
-    if (c.in_place) {
-      const int in = max(0, min(8, limit - q0));
-      const uint32_t mask = (1u << in) - 1u;
-      int t;
-      int h = holes + scan1024(__popc(~bits & mask), buf, t);
-      holes += t;
+    const uint32_t bits = used_bits(c.src, q0), mask = (1u << max(0, min(8, total - q0))) - 1u;
+    int t;
+    int h = holes + scan1024(__popc(~bits & mask), buf, t);
+    holes += t;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (!(mask >> k & 1u)) continue;
-        if (bits >> k & 1u) c.new_id[q0 + k] = q0 + k;
-        else {
-          c.new_id[q0 + k] = -1;
-          c.new_id[total + h++] = q0 + k;      // holes <= pages at or above n_used: in range
-        }
-      }
-    } else {
-      int t;
-      int r = base + scan1024(__popc(bits), buf, t);
-      base += t;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (q0 + k >= P) continue;
-        int id = -1;
-        if (bits >> k & 1u) {
-          id = r < c.dst.num_pages ? r : -1;
-          if (id >= 0) c.dst.use[id] = q0 + k;   // until the page is moved: which one goes there
-          ++r;
-        }
-        c.new_id[q0 + k] = id;
-      }
+    for (int k = 0; k < 8; ++k) {
+      if (!(mask >> k & 1u)) continue;
+      const bool used = bits >> k & 1u;
+      c.new_id[q0 + k] = used ? q0 + k : -1;
+      if (!used) c.new_id[total + h++] = q0 + k;   // as many pages in use lie above: in range
     }
   }
-  if (c.in_place) {
-    __syncthreads();
-    int left = holes;                          // pages at or above n_used not yet given their place
-    const int n_above = P - total;
-    for (int c0 = n_above > 0 ? (n_above - 1) / kAllocChunk * kAllocChunk : -1; c0 >= 0; c0 -= kAllocChunk) {
-      const int q0 = total + c0 + tid * 8;     // not a multiple of four: single loads
-      uint32_t bits = 0;
+  __syncthreads();
+  int left = holes;                            // pages at or above n_used not yet given their place
+  const int n_above = P - total;
+  for (int c0 = n_above > 0 ? (n_above - 1) / kAllocChunk * kAllocChunk : -1; c0 >= 0; c0 -= kAllocChunk) {
+    const int q0 = total + c0 + tid * 8;       // not a multiple of four: single loads
+    uint32_t bits = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) bits |= (q0 + k < P && c.src.use[q0 + k] > 0 ? 1u : 0u) << k;
-      int t;
-      const int before = scan1024(__popc(bits), buf, t);
-      int r = left - t + before;               // rank of the thread's first page to move
-      int32_t id[8];
+    for (int k = 0; k < 8; ++k) bits |= (q0 + k < P && c.src.use[q0 + k] > 0 ? 1u : 0u) << k;
+    int t;
+    const int before = scan1024(__popc(bits), buf, t);
+    int r = left - t + before;                 // rank of the thread's first page to move
+    int32_t id[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) id[k] = bits >> k & 1u ? c.new_id[total + r++] : -1;
-      __syncthreads();                         // this chunk's list entries are read before they are replaced
+    for (int k = 0; k < 8; ++k) id[k] = bits >> k & 1u ? c.new_id[total + r++] : -1;
+    __syncthreads();                           // this chunk's list entries are read before they are replaced
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (q0 + k < P) c.new_id[q0 + k] = id[k];
-      left -= t;
-    }
-  } else {
-    total = base;
-    if (tid == 0 && total > c.dst.num_pages) raise_error(kErrPages);
+    for (int k = 0; k < 8; ++k)
+      if (q0 + k < P) c.new_id[q0 + k] = id[k];
+    left -= t;
   }
   if (tid == 0) *c.n_used = total;
 }
@@ -441,24 +487,22 @@ __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(const CompactP
     const int used = min(*c.n_used, c.dst.num_pages);
     for (int64_t q = thread; q < c.dst.num_pages; q += threads)
       if (q >= used) c.dst.use[q] = 0;
-    for (int id = blockIdx.x; id < used; id += gridDim.x) {
-      const int q = c.dst.use[id];
-      __syncthreads();                         // every thread has it before the count replaces it
+    int id = blockIdx.x;
+    int q = id < used ? c.dst.use[id] : 0;
+    for (; id < used; id += gridDim.x) {
+      const int ahead = id + static_cast<int>(gridDim.x);
+      const int q_next = ahead < used ? c.dst.use[ahead] : 0;
+      __syncthreads();                         // every thread has q, read before, when the count replaces it
       if (tid == 0) c.dst.use[id] = c.src.use[q];
-      for (int k = 0; k < c.src.n_pools; ++k)
-        copy_units(reinterpret_cast<uint4*>(c.dst.pool[k].base + id * c.dst.pool[k].stride),
-                   reinterpret_cast<const uint4*>(c.src.pool[k].base + q * c.src.pool[k].stride),
-                   static_cast<int>(c.src.pool[k].stride / 16), tid, kCopyThreads);
+      copy_page(c.dst, id, c.src, q, tid);
+      q = q_next;
     }
     return;
   }
   for (int q = blockIdx.x; q < c.src.num_pages; q += gridDim.x) {
     const int32_t id = __ldg(c.new_id + q);
     if (id < 0 || id == q) continue;
-    for (int k = 0; k < c.src.n_pools; ++k)
-      copy_units(reinterpret_cast<uint4*>(c.dst.pool[k].base + id * c.dst.pool[k].stride),
-                 reinterpret_cast<const uint4*>(c.src.pool[k].base + q * c.src.pool[k].stride),
-                 static_cast<int>(c.src.pool[k].stride / 16), tid, kCopyThreads);
+    copy_page(c.dst, id, c.src, q, tid);
     if (tid == 0) {
       c.dst.use[id] = c.src.use[q];
       c.src.use[q] = 0;
@@ -552,7 +596,10 @@ int launch_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* 
   c.in_place = src->pools[0].base == dst->pools[0].base;
   int sms = 0;
   if (const int rc = sm_count(&sms); rc != DSV4SA_OK) return rc;
-  if (launch_pdl(cache_plan_kernel, dim3(1), dim3(kAllocThreads), 0, stream, c) != cudaSuccess) return DSV4SA_ERR_CUDA;
+  if ((c.in_place ? launch_pdl(cache_plan_in_place_kernel, dim3(1), dim3(kAllocThreads), 0, stream, c)
+                  : launch_cluster_pdl(cache_plan_kernel, dim3(kPlanCtas), dim3(kAllocThreads), 0, kPlanCtas, stream, c)) !=
+      cudaSuccess)
+    return DSV4SA_ERR_CUDA;
   const int64_t full = static_cast<int64_t>(sms) * 8;
   const int64_t want = c.src.num_pages;
   return done(launch_pdl(cache_move_kernel, dim3(static_cast<unsigned>(want < full ? want : full)), dim3(kCopyThreads),

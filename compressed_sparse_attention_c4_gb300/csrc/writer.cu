@@ -25,6 +25,7 @@
 // block's 64 codes leave as one contiguous 64-byte piece.
 #include "common.cuh"
 #include "dsv4sa_internal.h"
+#include "fp4.cuh"
 
 namespace dsv4sa {
 namespace {
@@ -144,14 +145,6 @@ __device__ __forceinline__ uint32_t e2m1_code(float y) {
   const float a = fabsf(y);
   const uint32_t m = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
   return m | ((__float_as_uint(y) >> 28) & 8u);
-}
-
-// The value of an E2M1 code: magnitude m of codes 0-7 is m / 2 up to 4, then 3, 4, 6.
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-  const uint32_t m = code & 7u;
-  // exponent field 126 + (m >> 1) and the mantissa bit below it; codes 0 and 1 are 0 and 0.5
-  const uint32_t b = m >= 2u ? ((126u + (m >> 1)) << 23) | ((m & 1u) << 22) : m * 0x3F000000u;
-  return __uint_as_float(b | ((code & 8u) << 28));
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -284,26 +277,33 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
 }
 
 // The codes and the exponent byte of a unit whose block is lanes c, c ^ 1, c ^ 2, c ^ 3.
+// The block's absmax is a maximum of BF16 pairs (NaN wins).
 __device__ __forceinline__ uint32_t quantise_unit(const uint4 v, uint32_t& exponent) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t mag = 0;
+  uint32_t a[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mag = max(mag, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
-  mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
-  mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+  for (int j = 0; j < 4; ++j) a[j] = w[j] & 0x7FFF7FFFu;
+  auto max2 = [](uint32_t x, uint32_t y) {
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  };
+  uint32_t m2 = max2(max2(a[0], a[1]), max2(a[2], a[3]));
+  m2 = max2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+  m2 = max2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
+  const uint32_t mag = max(m2 << 16, m2 & 0x7FFF0000u);   // as fp32 bits
   const bool finite = mag < 0x7F800000u;
   const float t = __fmul_rn(fmaxf(__uint_as_float(finite ? mag : 0u), kFp4AmaxFloor), kFp4MaxInv);
   const uint32_t tb = __float_as_uint(t);                 // normal: t >= 2^-126
   const int e = static_cast<int>((tb >> 23) & 0xFFu) - 127 + ((tb & 0x7FFFFFu) != 0u ? 1 : 0);   // <= 126
-  const float inv = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.f;        // 2^-e
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);                       // 2^-e
   uint32_t codes = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float x0 = finite ? __uint_as_float(w[j] << 16) : 0.f, x1 = finite ? __uint_as_float(w[j] & 0xFFFF0000u) : 0.f;
-    codes |= e2m1x2(__fmul_rn(x0, inv), __fmul_rn(x1, inv)) << (8 * j);
+    const float2 y = mul2(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), make_float2(inv, inv));
+    codes |= e2m1x2(y.x, y.y) << (8 * j);
   }
   exponent = finite ? static_cast<uint32_t>(e + 127) : 255u;
-  return codes;
+  return finite ? codes : 0u;
 }
 
 __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterParams p) {
@@ -367,21 +367,22 @@ struct ReaderParams {
   uint4* out;              // bf16 [n][512]
 };
 
-// Eight values: E2M1 codes in x, or E4M3 codes in x and y, times the scale.
-template <bool kFp4>
-__device__ __forceinline__ uint4 read_unit(uint32_t x, uint32_t y, float scale) {
+// Eight values: E2M1 codes in x times the scale of byte b, or E4M3 codes in x and y
+// times a scale.
+__device__ __forceinline__ uint4 read_fp4(uint32_t x, uint32_t b) {
+  const BlockScale bs = block_scale(b);
+  uint4 v = widen8(x, bs.first);
+  if (bs.more) v = scale_up(v, bs.more);
+  return v;
+}
+__device__ __forceinline__ uint4 read_fp8(uint32_t x, uint32_t y, float scale) {
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if constexpr (kFp4) {
-      const uint32_t byte = (x >> (8 * j)) & 0xFFu;
-      o[j] = pack2(e2m1_value(byte & 15u) * scale, e2m1_value(byte >> 4) * scale);
-    } else {
-      const __half2_raw h =
-          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(((j < 2 ? x : y) >> (16 * (j & 1))) & 0xFFFFu), __NV_E4M3);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      o[j] = pack2(__fmul_rn(f.x, scale), __fmul_rn(f.y, scale));
-    }
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(((j < 2 ? x : y) >> (16 * (j & 1))) & 0xFFFFu), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    o[j] = pack2(__fmul_rn(f.x, scale), __fmul_rn(f.y, scale));
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReaderParams
     bool ok[kRowsR];
     uint2 code[kRowsR][2];            // codes of the two units (FP4: in .x)
     uint4 rope[kRowsR];               // lanes 24-31: the second unit
-    float scl[kRowsR][2];
+    uint32_t scl[kRowsR][2];          // the scale byte, or the fp32 scale's bits
 #pragma unroll
     for (int k = 0; k < kRowsR; ++k) {
       const int64_t rc = r0 + k < p.n ? r0 + k : p.n - 1;
@@ -424,17 +425,16 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReaderParams
       for (int h = 0; h < 2; ++h) {
         const int u = 32 * h + c;
         code[k][h] = make_uint2(0u, 0u);
-        scl[k][h] = 0.f;
+        scl[k][h] = 0u;
         if (!ok[k]) continue;
         if (u >= 56) {
           rope[k] = __ldcs(reinterpret_cast<const uint4*>(pg + p.rope_off + slot * p.rope_row) + (u - 56));
         } else if constexpr (kFp4) {
           code[k][h].x = __ldcs(reinterpret_cast<const uint32_t*>(nope) + u);
-          const uint32_t b = __ldcs(sc + (u >> 2));
-          scl[k][h] = __uint_as_float(b == 0u ? 0x00400000u : (b == 255u ? 0x7FC00000u : b << 23));
+          scl[k][h] = __ldcs(sc + (u >> 2));
         } else {
           code[k][h] = __ldcs(reinterpret_cast<const uint2*>(nope) + u);
-          scl[k][h] = __ldcs(reinterpret_cast<const float*>(sc) + (u >> 3));
+          scl[k][h] = __ldcs(reinterpret_cast<const uint32_t*>(sc) + (u >> 3));
         }
       }
     }
@@ -442,8 +442,13 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReaderParams
     for (int k = 0; k < kRowsR; ++k) {
       if (r0 + k >= p.n) continue;
       uint4* dst = q.out + (r0 + k) * 64;
-      __stcs(dst + c, read_unit<kFp4>(code[k][0].x, code[k][0].y, scl[k][0]));
-      __stcs(dst + 32 + c, c < 24 ? read_unit<kFp4>(code[k][1].x, code[k][1].y, scl[k][1]) : rope[k]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 v;
+        if constexpr (kFp4) v = read_fp4(code[k][h].x, scl[k][h]);
+        else v = read_fp8(code[k][h].x, code[k][h].y, __uint_as_float(scl[k][h]));
+        __stcs(dst + 32 * h + c, h == 1 && c >= 24 ? rope[k] : v);
+      }
     }
   }
 }
