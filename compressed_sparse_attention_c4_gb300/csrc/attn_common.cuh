@@ -80,14 +80,17 @@ constexpr int kMaxClusterSplits = 8;
 // Inverse rotary embedding of the output: the rotation table row of query t
 // (16 float4 = 32 (cos, sin) pairs), or null when there is no rotation or the
 // position is out of range (flagged).
-__device__ __forceinline__ const float4* rope_row(const AttnParams& p, int t) {
+__device__ __forceinline__ const float4* rope_row_of(const AttnParams& p, int t, bool reporter) {
   if (p.rope_cs == nullptr) return nullptr;
   const int r = __ldg(p.rope_pos + t);
   if (r < 0 || r >= p.rope_rows) {
-    if (threadIdx.x == 0) raise_error(kErrIndex);
+    if (reporter) raise_error(kErrIndex);
     return nullptr;
   }
   return p.rope_cs + static_cast<int64_t>(r) * 16;
+}
+__device__ __forceinline__ const float4* rope_row(const AttnParams& p, int t) {
+  return rope_row_of(p, t, threadIdx.x == 0);
 }
 
 // (x + i y) times the conjugate of (c + i s)

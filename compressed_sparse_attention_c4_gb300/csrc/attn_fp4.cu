@@ -168,6 +168,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// Store two floats into another CTA's shared memory, counted as 8 bytes on a barrier
+// there.  (A plain store with a releasing remote arrival each took 0.7 us apiece, one
+// after the other: 4.7 us for the (m, l) of a cluster of four, 6.4 of eight.)
+__device__ __forceinline__ void st_async_v2f32(uint32_t addr, float a, float b, uint32_t mbar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr), "f"(a),
+               "f"(b), "r"(mbar)
+               : "memory");
+}
+
 // Positions of a list of n that CTA r of CS takes, and the k-th of them.
 __device__ __forceinline__ int share_of(int n, int r, int CS) {
   const int whole = n / (kRun * CS), rest = n - whole * kRun * CS - r * kRun;
@@ -230,9 +239,12 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     mbar_init(bar_q, kQThreads / 32);
     mbar_init(bar_item, 1);
     mbar_init(bar_recv, 1);
-    mbar_init(bar_ml, CS > 1 ? (CS - 1) * HN : 1);
+    mbar_init(bar_ml, 1);
     fence_mbar_init();
-    if (CS > 1) mbar_arrive_expect_tx(bar_recv, static_cast<uint32_t>((CS - 1) * slot_bytes));
+    if (CS > 1) {
+      mbar_arrive_expect_tx(bar_recv, static_cast<uint32_t>((CS - 1) * slot_bytes));
+      mbar_arrive_expect_tx(bar_ml, static_cast<uint32_t>((CS - 1) * HN * 8));
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_holder, kTmemCols);
@@ -245,7 +257,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (CS > 1) cluster_sync();            // every CTA's barriers are initialised before any remote arrival
+  if (CS > 1) cluster_arrive();          // this CTA's barriers are initialised; waited for before anything remote
   const uint32_t tmem = *tmem_holder;
   bool ok = true;                        // no wait of this thread has run out
 
@@ -406,6 +418,12 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       __syncwarp();
       ++token;
     }
+    if (CS > 1) {
+      ok = ok && warp_wait(bar_o, 0);    // the MMAs no longer read the tiles
+      tc_fence_after();
+      cluster_wait();
+      cluster_arrive();
+    }
   } else if (warp >= kMmaWarp) {
     // =========================== MMA warp ===========================
     regs_dec<kRegsMma>();
@@ -509,6 +527,11 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       }
       cp_async_wait();
     }
+    __syncwarp();
+    if (CS > 1) {
+      cluster_wait();
+      cluster_arrive();
+    }
   } else {
     // =========================== softmax warps ===========================
     regs_inc<kRegsCompute>();
@@ -521,6 +544,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     named_barrier_sync(kBarCompute4, kComputeThreads);
     int chunk = 0, token = 0, n_item = 0;
     bool alive = true;                                      // the same in all compute threads
+    bool arrived = false;                                   // at the cluster's second barrier
     for (int item = item0; item < n_items; item += item_step, ++n_item) {
       const int t = item / groups, h0 = (item - t * groups) * HN;
       const int hreal = min(HN, p.H - h0);
@@ -637,6 +661,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         waited = true;
       }
       named_barrier_sync(kBarCompute4, kComputeThreads);
+      if (CS > 1) cluster_wait();        // every CTA's barriers are initialised
       float m_mine = -1e30f, l_mine = 0.f;
       if (tid < HN) {
         m_mine = m_used[tid];
@@ -646,11 +671,18 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
 #pragma unroll 1
           for (int o = 0; o < CS; ++o) {
             if (o == crank) continue;
-            st_cluster_v2f32(cluster_map(smem_u32(mlr + crank * HN + tid), static_cast<uint32_t>(o)), m_mine, l_mine);
-            mbar_arrive_remote(cluster_map(smem_u32(bar_ml), static_cast<uint32_t>(o)));
+            st_async_v2f32(cluster_map(smem_u32(mlr + crank * HN + tid), static_cast<uint32_t>(o)), m_mine, l_mine,
+                           cluster_map(smem_u32(bar_ml), static_cast<uint32_t>(o)));
           }
-          ok = bar_wait(bar_ml, 0) && ok;
         }
+      }
+      if (CS > 1) {
+        __syncwarp();
+        cluster_arrive();                // see the merge below
+        arrived = true;
+      }
+      if (tid < HN) {
+        if (CS > 1) ok = bar_wait(bar_ml, 0) && ok;
         auto ml_of = [&](int c) { return c == crank ? make_float2(m_mine, l_mine) : mlr[c * HN + tid]; };
         const float sink2 = sink * kLog2e;
         float M = sink2;
@@ -671,13 +703,13 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         if (p.lse && crank == 0 && tid < hreal)
           p.lse[static_cast<int64_t>(t) * p.H + h0 + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
       }
+      if (CS > 1) break;                 // merged below, by all warps of the cluster
       bool bad = false;
       if (tid == 0) bad = !bar_wait(bar_o, n_item & 1);
       alive = !any_of(bad, kBarCompute4, kComputeThreads);      // also publishes the factors
       tc_fence_after();
       if (!alive) break;
       if (tid == 0) mbar_arrive(bar_item);                      // the MMA warp has read the end's token, too
-      if (CS > 1) break;                 // merged below, by all warps of the cluster
       // ---- output, 16 heads at a time: thread = dim, staged in the P buffer as words of
       // (head, head + 1), [8][512], read back eight dims a thread and stored 16 bytes a head
       const float4* rrow = rope_row(p, t);
@@ -734,51 +766,53 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       named_barrier_sync(kBarCompute4, kComputeThreads);        // m_used, red, fac and the P buffers are free again
     }
     ok = ok && alive;
+    if (CS > 1 && !arrived) {
+      cluster_wait();
+      cluster_arrive();
+    }
   }
 
   if (CS > 1) {
     // =========================== cluster merge ===========================
+    // Every thread has arrived at the cluster's second barrier, the gather warps once
+    // their CTA's MMAs were complete: when it completes, every CTA's tiles are idle.
     // Receive slots of the other CS - 1 splits at [0, R), this CTA's outgoing ones
     // at [R, 2 R), R = (CS - 1) slot_bytes, inside the idle tiles.  A slot is
     // [dim][HN] fp32; its 16-byte units are permuted within 128 bytes by the dim, so
-    // that the lanes of a warp (neighbouring dims) hit every bank.
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    cluster_arrive();                    // this CTA's tiles are idle: the other CTAs may copy into them
+    // that the lanes of a warp (neighbouring dims) hit every bank.  The 16 gather
+    // warps move the data, each a quarter of the heads of 32 dims at a time, while the
+    // softmax warps wait for the others' (m, l) and form the factors.
+    constexpr int HQ = HN / 4;
     const int R = (CS - 1) * slot_bytes;
     const int t = item0 / groups, h0 = (item0 - t * groups) * HN;
     const int hreal = min(HN, p.H - h0);
-    const uint32_t g = warp & 3u, hh = warp >> 2;
+    const bool mover = warp >= 8 && warp < kMmaWarp;
+    const uint32_t g = warp & 3u;
+    const int hq = (static_cast<int>(warp) - 8) / 4 * HQ;       // a mover's first head
     const uint32_t ta = tmem + ((g * 32u) << 16);
     auto unit_at = [](uint8_t* slot, int dl, int u) {
       const int s = HN >= 32 ? (u ^ (dl & 7)) : (u ^ ((dl >> 1) & 3));
       return reinterpret_cast<float4*>(slot + dl * (HN * 4)) + s;
     };
-    const bool compute = warp < 8;
     // fac is zero where this split attended to nothing; its O may then hold anything
-    if (compute) {
+    if (mover) {
 #pragma unroll 1
-      for (int b = 0; b < 2; ++b) {
-        const int blk = static_cast<int>(hh) * 2 + b;
+      for (int blk = 0; blk < 4; ++blk) {
         const int d = blk * 128 + static_cast<int>(g * 32 + lane);
         const int owner = d / slice;     // warp-uniform: a slice is at least 64 aligned dims
         if (owner == crank) continue;
         uint8_t* slot = smem + R + (owner < crank ? owner : owner - 1) * slot_bytes;
-#pragma unroll 1
-        for (int j0 = 0; j0 < HN; j0 += 16) {
-          float v[16];
-          tmem_load_cols<16>(ta + kColO + blk * HN + j0, v);
+        float v[HQ];
+        tmem_load_cols<HQ>(ta + kColO + blk * HN + hq, v);
 #pragma unroll
-          for (int x = 0; x < 16; x += 4)
-            *unit_at(slot, d - owner * slice, (j0 + x) / 4) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
-        }
+        for (int x = 0; x < HQ; x += 4)
+          *unit_at(slot, d - owner * slice, (hq + x) / 4) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
       }
+      fence_proxy_async_smem();          // the staged slots are read by the bulk-copy engine
+      named_barrier_sync(kBarGather4, kGatherThreads);
     }
-    fence_proxy_async_smem();            // the staged slots are read by the bulk-copy engine
-    __syncthreads();
     cluster_wait();                      // every CTA's tiles are idle
-    if (tid == 0) {
+    if (tid == kComputeThreads) {
       for (int o = 0; o < CS; ++o) {
         if (o == crank) continue;
         const int at = crank < o ? crank : crank - 1;
@@ -787,10 +821,11 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
                              cluster_map(smem_u32(bar_recv), static_cast<uint32_t>(o)));
       }
     }
-    ok = bar_wait(bar_recv, 0) && ok;   // the other splits' slots have landed here
+    __syncthreads();                     // the factors are there
+    if (mover) ok = ok && warp_wait(bar_recv, 0);   // the other splits' slots have landed here
     cluster_arrive();                    // ... so their copies out of the senders are complete
-    if (compute) {
-      const float4* rrow = rope_row(p, t);
+    if (mover) {
+      const float4* rrow = rope_row_of(p, t, tid == kComputeThreads);
 #pragma unroll 1
       for (int blk = crank * slice / 128; blk < (crank * slice + slice + 127) / 128; ++blk) {
         const int d = blk * 128 + static_cast<int>(g * 32 + lane), dl = d - crank * slice;
@@ -798,41 +833,39 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         uint16_t* orow = p.out + (static_cast<int64_t>(t) * p.H + h0) * 512 + (d & ~1);
         const bool rot = rrow != nullptr && d >= 512 - 64;
         const float2 cs = rot ? __ldg(reinterpret_cast<const float2*>(rrow) + ((d - (512 - 64)) >> 1)) : make_float2(1.f, 0.f);
+        float v[HQ];
+        tmem_load_cols<HQ>(ta + kColO + blk * HN + hq, v);
+#pragma unroll
+        for (int x = 0; x < HQ; ++x) {
+          const float f = fac[crank * HN + hq + x];
+          v[x] = f == 0.f ? 0.f : v[x] * f;
+        }
 #pragma unroll 1
-        for (int j0 = static_cast<int>(hh) * HW; j0 < (static_cast<int>(hh) + 1) * HW; j0 += 8) {
-          float v[8];
-          tmem_load_cols<8>(ta + kColO + blk * HN + j0, v);
+        for (int c = 0; c < CS; ++c) {
+          if (c == crank) continue;
+          uint8_t* slot = smem + (c < crank ? c : c - 1) * slot_bytes;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float f = fac[crank * HN + j0 + x];
-            v[x] = f == 0.f ? 0.f : v[x] * f;
+          for (int x = 0; x < HQ; x += 4) {
+            const float4 u = *unit_at(slot, dl, (hq + x) / 4);
+            const float4 f = *reinterpret_cast<const float4*>(fac + c * HN + hq + x);
+            if (f.x != 0.f) v[x] = fmaf(u.x, f.x, v[x]);
+            if (f.y != 0.f) v[x + 1] = fmaf(u.y, f.y, v[x + 1]);
+            if (f.z != 0.f) v[x + 2] = fmaf(u.z, f.z, v[x + 2]);
+            if (f.w != 0.f) v[x + 3] = fmaf(u.w, f.w, v[x + 3]);
           }
-#pragma unroll 1
-          for (int c = 0; c < CS; ++c) {
-            if (c == crank) continue;
-            uint8_t* slot = smem + (c < crank ? c : c - 1) * slot_bytes;
+        }
+        // lanes (d, d + 1) pair up: even lanes take head x, odd lanes head x + 1, of both dims
 #pragma unroll
-            for (int x = 0; x < 8; x += 4) {
-              const float4 u = *unit_at(slot, dl, (j0 + x) / 4);
-              const float4 f = *reinterpret_cast<const float4*>(fac + c * HN + j0 + x);
-              if (f.x != 0.f) v[x] = fmaf(u.x, f.x, v[x]);
-              if (f.y != 0.f) v[x + 1] = fmaf(u.y, f.y, v[x + 1]);
-              if (f.z != 0.f) v[x + 2] = fmaf(u.z, f.z, v[x + 2]);
-              if (f.w != 0.f) v[x + 3] = fmaf(u.w, f.w, v[x + 3]);
-            }
+        for (int x = 0; x < HQ; x += 2) {
+          const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[x] : v[x + 1], 1);
+          float lo = (lane & 1) ? got : v[x], hi = (lane & 1) ? v[x + 1] : got;
+          if (rot) {
+            const float2 z = rotate_back(lo, hi, cs.x, cs.y);
+            lo = z.x;
+            hi = z.y;
           }
-#pragma unroll
-          for (int x = 0; x < 8; x += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[x] : v[x + 1], 1);
-            float lo = (lane & 1) ? got : v[x], hi = (lane & 1) ? v[x + 1] : got;
-            if (rot) {
-              const float2 z = rotate_back(lo, hi, cs.x, cs.y);
-              lo = z.x;
-              hi = z.y;
-            }
-            const int h = j0 + x + static_cast<int>(lane & 1);
-            if (h < hreal && ok) *reinterpret_cast<uint32_t*>(orow + static_cast<int64_t>(h) * 512) = pack_bf16x2(lo, hi);
-          }
+          const int h = hq + x + static_cast<int>(lane & 1);
+          if (h < hreal && ok) *reinterpret_cast<uint32_t*>(orow + h * 512) = pack_bf16x2(lo, hi);
         }
       }
     }
