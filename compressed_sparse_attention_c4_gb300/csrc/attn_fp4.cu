@@ -274,8 +274,6 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     const int cw = share_of(p.kw, crank, CS), total = cw + share_of(p.kc, crank, CS);   // this CTA's positions of an item
     for (int item = item0, n_item = 0; item < n_items; item += item_step, ++n_item) {
       const int t = item / groups;
-      const int seq = __ldg(p.q_seq + t);
-      const int wpos = p.idx_w || p.kw == 0 ? 0 : __ldg(p.win_pos + t);
       int cursor = 0, count = 0;                // positions looked up, rows in the ring
       // look up the next positions, one a thread of half of them
       auto locate = [&]() {
@@ -286,12 +284,13 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
           const bool window = pos < cw;
           const int j = share_at(window ? pos : pos - cw, crank, CS);
           int32_t e;
+          const int seq = __ldg(p.q_seq + t);   // in flight together with the entry
           if (!window) {
             e = __ldg(p.idx_c + static_cast<int64_t>(t) * p.idx_c_stride + j);
           } else if (p.idx_w) {
             e = __ldg(p.idx_w + static_cast<int64_t>(t) * p.idx_w_stride + j);
           } else {
-            const int64_t pw = static_cast<int64_t>(wpos) - p.kw + 1 + j;
+            const int64_t pw = static_cast<int64_t>(__ldg(p.win_pos + t)) - p.kw + 1 + j;
             e = pw < 0 ? -1 : static_cast<int32_t>(p.win_ring > 0 ? pw % p.win_ring : pw);
           }
           if (e >= 0) {
@@ -686,16 +685,19 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         auto ml_of = [&](int c) { return c == crank ? make_float2(m_mine, l_mine) : mlr[c * HN + tid]; };
         const float sink2 = sink * kLog2e;
         float M = sink2;
+#pragma unroll 1
         for (int c = 0; c < CS; ++c) {
           const float2 ml = ml_of(c);
           if (!(ml.y == 0.f)) M = fmaxf(M, ml.x);
         }
         float L = sink2 > -INFINITY ? exp2f(sink2 - M) : 0.f;   // a sink of -inf adds nothing
+#pragma unroll 1
         for (int c = 0; c < CS; ++c) {
           const float2 ml = ml_of(c);
           if (!(ml.y == 0.f)) L += ml.y * exp2f(ml.x - M);
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;             // an empty denominator gives zeros
+#pragma unroll 1
         for (int c = 0; c < CS; ++c) {
           const float2 ml = ml_of(c);
           fac[c * HN + tid] = ml.y == 0.f ? 0.f : exp2f(ml.x - M) * inv;
@@ -833,39 +835,40 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         uint16_t* orow = p.out + (static_cast<int64_t>(t) * p.H + h0) * 512 + (d & ~1);
         const bool rot = rrow != nullptr && d >= 512 - 64;
         const float2 cs = rot ? __ldg(reinterpret_cast<const float2*>(rrow) + ((d - (512 - 64)) >> 1)) : make_float2(1.f, 0.f);
-        float v[HQ];
-        tmem_load_cols<HQ>(ta + kColO + blk * HN + hq, v);
-#pragma unroll
-        for (int x = 0; x < HQ; ++x) {
-          const float f = fac[crank * HN + hq + x];
-          v[x] = f == 0.f ? 0.f : v[x] * f;
-        }
+        // four heads at a time, not unrolled: code that runs once a launch is fetched from
+        // L2 as it runs, so short loops beat straight lines
 #pragma unroll 1
-        for (int c = 0; c < CS; ++c) {
-          if (c == crank) continue;
-          uint8_t* slot = smem + (c < crank ? c : c - 1) * slot_bytes;
-#pragma unroll
-          for (int x = 0; x < HQ; x += 4) {
-            const float4 u = *unit_at(slot, dl, (hq + x) / 4);
-            const float4 f = *reinterpret_cast<const float4*>(fac + c * HN + hq + x);
-            if (f.x != 0.f) v[x] = fmaf(u.x, f.x, v[x]);
-            if (f.y != 0.f) v[x + 1] = fmaf(u.y, f.y, v[x + 1]);
-            if (f.z != 0.f) v[x + 2] = fmaf(u.z, f.z, v[x + 2]);
-            if (f.w != 0.f) v[x + 3] = fmaf(u.w, f.w, v[x + 3]);
+        for (int j0 = hq; j0 < hq + HQ; j0 += 4) {
+          float v[4];
+          tmem_load_cols<4>(ta + kColO + blk * HN + j0, v);
+          const float4 fm = *reinterpret_cast<const float4*>(fac + crank * HN + j0);
+          v[0] = fm.x == 0.f ? 0.f : v[0] * fm.x;
+          v[1] = fm.y == 0.f ? 0.f : v[1] * fm.y;
+          v[2] = fm.z == 0.f ? 0.f : v[2] * fm.z;
+          v[3] = fm.w == 0.f ? 0.f : v[3] * fm.w;
+#pragma unroll 1
+          for (int c = 0; c < CS; ++c) {
+            if (c == crank) continue;
+            const float4 u = *unit_at(smem + (c < crank ? c : c - 1) * slot_bytes, dl, j0 / 4);
+            const float4 f = *reinterpret_cast<const float4*>(fac + c * HN + j0);
+            if (f.x != 0.f) v[0] = fmaf(u.x, f.x, v[0]);
+            if (f.y != 0.f) v[1] = fmaf(u.y, f.y, v[1]);
+            if (f.z != 0.f) v[2] = fmaf(u.z, f.z, v[2]);
+            if (f.w != 0.f) v[3] = fmaf(u.w, f.w, v[3]);
           }
-        }
-        // lanes (d, d + 1) pair up: even lanes take head x, odd lanes head x + 1, of both dims
+          // lanes (d, d + 1) pair up: even lanes take head x, odd lanes head x + 1, of both dims
 #pragma unroll
-        for (int x = 0; x < HQ; x += 2) {
-          const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[x] : v[x + 1], 1);
-          float lo = (lane & 1) ? got : v[x], hi = (lane & 1) ? v[x + 1] : got;
-          if (rot) {
-            const float2 z = rotate_back(lo, hi, cs.x, cs.y);
-            lo = z.x;
-            hi = z.y;
+          for (int x = 0; x < 4; x += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[x] : v[x + 1], 1);
+            float lo = (lane & 1) ? got : v[x], hi = (lane & 1) ? v[x + 1] : got;
+            if (rot) {
+              const float2 z = rotate_back(lo, hi, cs.x, cs.y);
+              lo = z.x;
+              hi = z.y;
+            }
+            const int h = j0 + x + static_cast<int>(lane & 1);
+            if (h < hreal && ok) *reinterpret_cast<uint32_t*>(orow + h * 512) = pack_bf16x2(lo, hi);
           }
-          const int h = hq + x + static_cast<int>(lane & 1);
-          if (h < hreal && ok) *reinterpret_cast<uint32_t*>(orow + h * 512) = pack_bf16x2(lo, hi);
         }
       }
     }
