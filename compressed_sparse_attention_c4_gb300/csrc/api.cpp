@@ -57,6 +57,20 @@ bool cache_ok(const dsv4sa_cache_desc* c) {
          aligned(c->page_table, 4) && c->use && aligned(c->use, 16);
 }
 
+// Whether a byte range lies apart from a cache's table, counts and pools.
+bool apart(const dsv4sa_cache_desc* c, const void* a, uint64_t bytes) {
+  if (overlap(a, bytes, c->page_table, static_cast<uint64_t>(c->rows) * c->pt_stride * 4) ||
+      overlap(a, bytes, c->use, static_cast<uint64_t>(c->pools[0].num_pages) * 4))
+    return false;
+  for (int32_t k = 0; k < c->n_pools; ++k)
+    if (overlap(a, bytes, c->pools[k].base, dsv4sa_pool_bytes(c->pools[k].kind, c->pools[k].num_pages))) return false;
+  return true;
+}
+
+// Bytes from the first to the last value of n BF16 rows, `stride` values apart.
+uint64_t row_span(int64_t n, int64_t stride, int32_t dim) {
+  return (static_cast<uint64_t>(n - 1) * static_cast<uint64_t>(stride) + static_cast<uint64_t>(dim)) * 2;
+}
 
 }  // namespace
 
@@ -299,6 +313,7 @@ static int attn_validate(int32_t mode, const dsv4sa_attn_args* a) {
     if (!pool_ok(a->win, kind) || !a->win_pt || (!a->idx_w && !a->win_pos)) return DSV4SA_ERR_INVALID_ARG;
     if ((a->idx_w && a->idx_w_stride < a->kw) || a->win_pt_stride < 1 || a->win_ring < 0) return DSV4SA_ERR_INVALID_ARG;
   }
+  if (fp4 && static_cast<int64_t>(a->kc) + a->kw > (1 << 30)) return DSV4SA_ERR_UNSUPPORTED;
   if (a->rope_cs && (!a->rope_pos || a->rope_rows < 1 || !aligned(a->rope_cs, 16))) return DSV4SA_ERR_INVALID_ARG;
   const size_t need = fp4 ? 0 : dsv4sa_attn_workspace_size(mode, a->T, a->H, a->kc, a->kw);
   if (need > 0 && (!a->ws || a->ws_bytes < need || !aligned(a->ws, 16))) return DSV4SA_ERR_WORKSPACE;
@@ -393,6 +408,10 @@ DSV4SA_API int dsv4sa_cache_fork(const dsv4sa_cache_desc* cache, const int32_t* 
   if (n > (1 << 28)) return DSV4SA_ERR_UNSUPPORTED;
   if (n == 0) return DSV4SA_OK;
   if (!src_row || !dst_row || !length || !new_page) return DSV4SA_ERR_INVALID_ARG;
+  const uint64_t bytes = static_cast<uint64_t>(n) * 4;   // new_page is written while the others are read
+  if (!apart(cache, new_page, bytes) || overlap(new_page, bytes, src_row, bytes) ||
+      overlap(new_page, bytes, dst_row, bytes) || overlap(new_page, bytes, length, bytes))
+    return DSV4SA_ERR_INVALID_ARG;
   return dsv4sa::launch_cache_fork(cache, src_row, dst_row, length, n, new_page, stream);
 }
 
@@ -402,21 +421,22 @@ DSV4SA_API int dsv4sa_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_c
   if (src->n_pools != dst->n_pools || src->rows != dst->rows || src->pt_stride != dst->pt_stride)
     return DSV4SA_ERR_INVALID_ARG;
   const uint64_t entries = static_cast<uint64_t>(src->rows) * src->pt_stride * 4;
+  const uint64_t ids = static_cast<uint64_t>(src->pools[0].num_pages) * 4;
+  if (!apart(src, new_id, ids) || !apart(dst, new_id, ids) || !apart(src, n_used, 4) || !apart(dst, n_used, 4) ||
+      overlap(new_id, ids, n_used, 4))
+    return DSV4SA_ERR_INVALID_ARG;
   bool same = src->page_table == dst->page_table && src->use == dst->use;
   for (int32_t k = 0; k < src->n_pools; ++k) {
     if (src->pools[k].kind != dst->pools[k].kind) return DSV4SA_ERR_INVALID_ARG;
     same = same && src->pools[k].base == dst->pools[k].base && src->pools[k].num_pages == dst->pools[k].num_pages;
   }
   if (!same) {   // in place altogether, or apart altogether
-    if (overlap(src->page_table, entries, dst->page_table, entries) ||
-        overlap(src->use, static_cast<uint64_t>(src->pools[0].num_pages) * 4, dst->use,
-                static_cast<uint64_t>(dst->pools[0].num_pages) * 4))
+    if (!apart(src, dst->page_table, entries) ||
+        !apart(src, dst->use, static_cast<uint64_t>(dst->pools[0].num_pages) * 4))
       return DSV4SA_ERR_INVALID_ARG;
-    for (int32_t k = 0; k < src->n_pools; ++k)
-      for (int32_t j = 0; j < dst->n_pools; ++j)
-        if (overlap(src->pools[k].base, dsv4sa_pool_bytes(src->pools[k].kind, src->pools[k].num_pages),
-                    dst->pools[j].base, dsv4sa_pool_bytes(dst->pools[j].kind, dst->pools[j].num_pages)))
-          return DSV4SA_ERR_INVALID_ARG;
+    for (int32_t k = 0; k < dst->n_pools; ++k)
+      if (!apart(src, dst->pools[k].base, dsv4sa_pool_bytes(dst->pools[k].kind, dst->pools[k].num_pages)))
+        return DSV4SA_ERR_INVALID_ARG;
   }
   return dsv4sa::launch_cache_compact(src, dst, new_id, n_used, stream);
 }
@@ -434,6 +454,22 @@ DSV4SA_API int dsv4sa_rmsnorm_quant(const void* x, int64_t x_stride, const void*
   if (!x || !norm_w || !aligned(x, 16) || !aligned(residual, 16) || !aligned(norm_w, 16) || !aligned(residual_out, 16) ||
       !aligned(y, 16) || !aligned(codes, 16) || !aligned(scale, 4))
     return DSV4SA_ERR_INVALID_ARG;
+  // outputs apart from the inputs and from one another; the sum may replace its input
+  const uint64_t whole = static_cast<uint64_t>(n) * dim * 2;
+  const struct { const void* p; uint64_t bytes; } in[3] = {{x, row_span(n, x_stride, dim)},
+                                                           {residual, residual ? row_span(n, residual_stride, dim) : 0},
+                                                           {norm_w, static_cast<uint64_t>(dim) * 4}},
+      out[4] = {{residual_out, whole}, {y, whole}, {codes, whole / 2}, {scale, whole / 2 / group * 4}};
+  const int64_t in_stride[2] = {x_stride, residual_stride};
+  for (int o = 0; o < 4; ++o) {
+    if (!out[o].p) continue;
+    for (int i = 0; i < 3; ++i) {
+      const bool replaced = o == 0 && i < 2 && out[o].p == in[i].p && (in_stride[i] == dim || n == 1);
+      if (in[i].p && !replaced && overlap(out[o].p, out[o].bytes, in[i].p, in[i].bytes)) return DSV4SA_ERR_INVALID_ARG;
+    }
+    for (int k = 0; k < o; ++k)
+      if (out[k].p && overlap(out[o].p, out[o].bytes, out[k].p, out[k].bytes)) return DSV4SA_ERR_INVALID_ARG;
+  }
   return dsv4sa::launch_rmsnorm_quant(x, x_stride, residual, residual_stride, norm_w, eps, n, dim, group, residual_out,
                                       y, codes, scale, stream);
 }

@@ -438,6 +438,7 @@ def dsv4sa_pages_copy(pools, src_page, dst_page, stream=None):
     """Copy pages src_page[i] -> dst_page[i] of every pool in the list (int32 [n]; -1: skip)."""
     if src_page.shape != dst_page.shape:
         raise ValueError("src_page and dst_page differ in length")
+    _on_current_device(src_page, "src_page")
     arr = _pool_array(pools)
     _check("dsv4sa_pages_copy", lib().dsv4sa_pages_copy(
         arr, len(pools), _dev(src_page, "src_page", torch.int32), _dev(dst_page, "dst_page", torch.int32),
@@ -446,6 +447,7 @@ def dsv4sa_pages_copy(pools, src_page, dst_page, stream=None):
 
 def dsv4sa_cache_release(cache: CacheDesc, row, stream=None):
     """Release rows (int32 [n]) of the page table: entries -1, their pages' counts down by one."""
+    _on_current_device(row, "row")
     _check("dsv4sa_cache_release", lib().dsv4sa_cache_release(
         ctypes.byref(cache), _dev(row, "row", torch.int32), row.numel(), _stream(stream)))
 
@@ -456,6 +458,7 @@ def dsv4sa_cache_fork(cache: CacheDesc, src_row, dst_row, length, new_page, stre
     n = src_row.numel()
     if dst_row.numel() != n or length.numel() != n or new_page.numel() != n:
         raise ValueError("src_row, dst_row, length and new_page differ in length")
+    _on_current_device(src_row, "src_row")
     _check("dsv4sa_cache_fork", lib().dsv4sa_cache_fork(
         ctypes.byref(cache), _dev(src_row, "src_row", torch.int32), _dev(dst_row, "dst_row", torch.int32),
         _dev(length, "length", torch.int32), n, _dev(new_page, "new_page", torch.int32), _stream(stream)))
@@ -466,6 +469,7 @@ def dsv4sa_cache_compact(src: CacheDesc, dst: CacheDesc, new_id, n_used, stream=
     with dst's table and counts by the new ids.  new_id int32 [src pages], n_used int32 [1]."""
     if new_id.numel() != src.pools[0].num_pages or n_used.numel() != 1:
         raise ValueError("new_id must have one entry per page, n_used one")
+    _on_current_device(new_id, "new_id")
     _check("dsv4sa_cache_compact", lib().dsv4sa_cache_compact(
         ctypes.byref(src), ctypes.byref(dst), _dev(new_id, "new_id", torch.int32), _dev(n_used, "n_used", torch.int32),
         _stream(stream)))
@@ -602,6 +606,7 @@ def _attn_args(q, sink, q_seq, comp, comp_pt, idx_c, win, win_pt, idx_w, out, so
     if q.shape[2] != HEAD_DIM:
         raise ValueError("q must be [T, H, 512]")
     qp = _dev(q, "q", torch.bfloat16)
+    _on_current_device(q, "q")
     cd = cpt = ic = wd = wpt = iw = wpos = rcs = rpos = None
     cpt_stride = kc = wpt_stride = n_w = iw_stride = ring = rope_rows = 0
     if idx_c is not None:
@@ -738,14 +743,34 @@ def _arena_views(buf, layout):
     return {name: buf[o:o + nb].view(dtype).view(shape) for name, o, nb, shape, dtype in layout}
 
 
-def upload(w, device="cuda", mode=None) -> DeviceWorkload:
-    """Copy a workloads.Workload to the GPU in the library's formats."""
+def requantize_kv_pool_fp4(pool: PoolDesc, device="cuda", stream=None):
+    """A KV pool's rows, all of them, as a KV_FP4 pool of as many pages -> (device byte
+    tensor, PoolDesc): read back as BF16 and written again, 1024 pages at a time."""
+    pages = int(pool.num_pages)
+    buf = _alloc_pool(POOL_KV_FP4, pages, device)
+    desc = dsv4sa_pool_desc_init(POOL_KV_FP4, buf, pages)
+    table = torch.arange(pages, dtype=torch.int32, device=device).view(1, pages)
+    for p0 in range(0, pages, 1024):
+        entry = torch.arange(p0 * PAGE, min(pages, p0 + 1024) * PAGE, dtype=torch.int32, device=device)
+        seq = torch.zeros_like(entry)
+        rows = torch.empty(entry.shape[0], HEAD_DIM, dtype=torch.bfloat16, device=device)
+        dsv4sa_cache_read(pool, table, seq, entry, rows, stream)
+        dsv4sa_cache_write(desc, table, seq, entry, rows, stream)
+    return buf, desc
+
+
+def upload(w, device="cuda", mode=None, kv_fp4=False) -> DeviceWorkload:
+    """Copy a workloads.Workload to the GPU in the library's formats; with kv_fp4 the
+    KV pools are requantised into KV_FP4 pools."""
     dev = torch.device(device)
     if mode is None:
         mode = ATTN_PREFILL if w.T > 4 * w.B else ATTN_DECODE
     comp_buf, comp = pack_kv_pool(w.comp_pool["nope_codes"], w.comp_pool["nope_scale"], w.comp_pool["rope_bits"], dev)
     key_buf, keys = pack_key_pool(w.key_pool["codes"], w.key_pool["scale"], dev)
     win_buf, win = pack_kv_pool(w.win_pool["nope_codes"], w.win_pool["nope_scale"], w.win_pool["rope_bits"], dev)
+    if kv_fp4:
+        comp_buf, comp = requantize_kv_pool_fp4(comp, dev)
+        win_buf, win = requantize_kv_pool_fp4(win, dev)
 
     def t(x, dt):
         return torch.from_numpy(np.ascontiguousarray(x)).to(dt).to(dev)
@@ -754,7 +779,7 @@ def upload(w, device="cuda", mode=None) -> DeviceWorkload:
     n_max = max(1, int(w.n_max))
     logits_stride = (n_max + 3) // 4 * 4
     topk_ws_bytes = dsv4sa_topk_workspace_size(w.T, n_max, w.k)
-    attn_ws_bytes = dsv4sa_attn_workspace_size(mode, w.T, w.H, w.kc, w.kw)
+    attn_ws_bytes = 0 if kv_fp4 else dsv4sa_attn_workspace_size(mode, w.T, w.H, w.kc, w.kw)
     # the per-step inputs and outputs each live in one buffer, so a step moves
     # them with one host-to-device and one device-to-host copy
     host = {
@@ -817,8 +842,11 @@ def run_path(d: DeviceWorkload, stream=None, fused_window=False, before_attentio
             win_pos=d.pos if fused_window else None, kw=w.kw if fused_window else None,
             win_ring=w.win_ring if fused_window else 0, flags=ATTN_EARLY_WINDOW if fused_window else 0)
         return
-    # the top-k also prefetches the selected compressed rows into L2 for the attention
-    dsv4sa_topk_prefetch(d.logits, d.n_vis_idx, n_max, w.k, d.idx_c, d.comp, d.comp_pt, d.q_seq, d.topk_ws, stream)
+    if d.comp.kind == POOL_KV:
+        # the top-k also prefetches the selected compressed rows into L2 for the attention
+        dsv4sa_topk_prefetch(d.logits, d.n_vis_idx, n_max, w.k, d.idx_c, d.comp, d.comp_pt, d.q_seq, d.topk_ws, stream)
+    else:
+        dsv4sa_topk(d.logits, d.n_vis_idx, n_max, w.k, d.idx_c, d.topk_ws, stream)
     if before_attention is not None:
         before_attention()
     fn = dsv4sa_sparse_attn_prefill if d.mode == ATTN_PREFILL else dsv4sa_sparse_attn_decode

@@ -322,7 +322,7 @@ DSV4SA_API int dsv4sa_compress_indices(const int32_t* n_vis, int32_t T, int32_t 
  * The pools are two of kind DSV4SA_POOL_KV, or two of kind DSV4SA_POOL_KV_FP4
  * (a 4-bit cache; one of each is DSV4SA_ERR_UNSUPPORTED).  FP4 rows dequantise
  * to BF16 exactly, partial results are exchanged in fp32, and no workspace is
- * needed (ws may be null in either mode).
+ * needed (ws may be null in either mode); kc + kw <= 2^30.
  */
 typedef struct {
   const void*  q;              /* device bf16 [T][H][512], 16-byte aligned                 */
@@ -487,7 +487,9 @@ DSV4SA_API int dsv4sa_cache_read(const dsv4sa_pool_desc* pool, const int32_t* pa
  * agree when they are called:
  *   use[p] = table entries equal to p;  0: page p is free
  * Entries of the table are page ids, or -1.  A caller that adds pages to a row
- * itself sets their counts.
+ * itself sets their counts.  Calls on one cache are ordered by the caller, in one
+ * stream or by events; calls on different caches may run at once (none of them
+ * needs a workspace).
  */
 typedef struct {
   const dsv4sa_pool_desc* pools;  /* host array [n_pools], all with the same num_pages (< 2^31) */
@@ -525,8 +527,10 @@ DSV4SA_API int dsv4sa_cache_release(const dsv4sa_cache_desc* cache, const int32_
  * src_row[i].  Full pages are shared, their counts go up; a last page that is
  * not full is copied -- its first length % 64 slots, in every pool -- into a
  * free page, so the two sequences can go on apart.  The lowest free pages are
- * taken, in the order of the forks.
- *   new_page   device int32 [n]: the page fork i took, -1 when it needs none
+ * taken, in the order of the forks.  An entry of the src row before its last page
+ * that is no page id is copied as -1 and sets DSV4SA_ERR_INDEX_OOB.
+ *   new_page   device int32 [n], apart from the cache and the other arrays: the page
+ *              fork i took, -1 when it needs none
  * Refused forks, with their row left as it was: -3 and DSV4SA_ERR_INDEX_OOB on
  * the device for a row, length or page id out of range, a dst row that was not
  * released (its first entry is a page), one that an earlier fork of the call
@@ -548,6 +552,7 @@ DSV4SA_API int dsv4sa_cache_fork(const dsv4sa_cache_desc* cache, const int32_t* 
  * set on the device.  dst pages past the used ones are not written.
  *   new_id   device int32 [src num_pages]: the page's new id, -1 for a free page
  *   n_used   device int32 [1]: pages in use
+ * Both lie apart from the two caches.
  */
 DSV4SA_API int dsv4sa_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* dst, int32_t* new_id,
                                     int32_t* n_used, cudaStream_t stream);
@@ -570,7 +575,8 @@ DSV4SA_API int dsv4sa_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_c
  *   codes, scale  optional, together: uint8 [n][dim] and fp32 [n][dim / group]
  *   dim           a multiple of 8 and, with codes, of group; <= DSV4SA_MAX_NORM_DIM
  *   group         64 or 128
- * At least one output is given; other outputs must not overlap the inputs.
+ * At least one output is given; but for residual_out as said, outputs lie apart from
+ * one another and from the inputs (from their first to their last value).
  */
 DSV4SA_API int dsv4sa_rmsnorm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                                     const float* norm_w, float eps, int32_t n, int32_t dim, int32_t group,

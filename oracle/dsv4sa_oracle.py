@@ -52,6 +52,9 @@ against scipy's Hadamard matrix, torch's BF16 rounding, and fp32 evaluations in
 several orders that stay inside ``hadamard_rotate_fp32_bound``).  The
 FP4 key writes (plain and rotated) have CUDA counterparts; the FP4 scores
 (``indexer_logits_row_fp4``) have none yet.
+The FP4 KV cache, the pages of a cache and the norm with a quantised output are
+pinned in ``tests/test_oracle_pins_cache.py`` (hand cases, torch's decoders and
+norm, brute-force loops, invariants).
 """
 from __future__ import annotations
 
