@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       }
       named_barrier_sync(kBarCompute4, kComputeThreads);
       if (CS > 1) cluster_wait();        // every CTA's barriers are initialised
-      float m_mine = -1e30f, l_mine = 0.f;
+      float m_mine = -1e30f, l_mine = 0.f, M = 0.f, L = 0.f;
       if (tid < HN) {
         m_mine = m_used[tid];
         const float4 q = *reinterpret_cast<const float4*>(red + tid * 4);
@@ -684,28 +684,33 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         if (CS > 1) ok = bar_wait(bar_ml, 0) && ok;
         auto ml_of = [&](int c) { return c == crank ? make_float2(m_mine, l_mine) : mlr[c * HN + tid]; };
         const float sink2 = sink * kLog2e;
-        float M = sink2;
+        M = sink2;
 #pragma unroll 1
         for (int c = 0; c < CS; ++c) {
           const float2 ml = ml_of(c);
           if (!(ml.y == 0.f)) M = fmaxf(M, ml.x);
         }
-        float L = sink2 > -INFINITY ? exp2f(sink2 - M) : 0.f;   // a sink of -inf adds nothing
+        L = sink2 > -INFINITY ? ex2_approx(sink2 - M) : 0.f;    // a sink of -inf adds nothing
 #pragma unroll 1
         for (int c = 0; c < CS; ++c) {
           const float2 ml = ml_of(c);
-          if (!(ml.y == 0.f)) L += ml.y * exp2f(ml.x - M);
+          if (!(ml.y == 0.f)) L += ml.y * ex2_approx(ml.x - M);
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;             // an empty denominator gives zeros
+        const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);  // an empty denominator gives zeros
 #pragma unroll 1
         for (int c = 0; c < CS; ++c) {
           const float2 ml = ml_of(c);
-          fac[c * HN + tid] = ml.y == 0.f ? 0.f : exp2f(ml.x - M) * inv;
+          fac[c * HN + tid] = ml.y == 0.f ? 0.f : ex2_approx(ml.x - M) * inv;
         }
+      }
+      auto write_lse = [&]() {           // after the output, which waits for the factors only
         if (p.lse && crank == 0 && tid < hreal)
           p.lse[static_cast<int64_t>(t) * p.H + h0 + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      };
+      if (CS > 1) {
+        write_lse();
+        break;                           // merged below, by all warps of the cluster
       }
-      if (CS > 1) break;                 // merged below, by all warps of the cluster
       bool bad = false;
       if (tid == 0) bad = !bar_wait(bar_o, n_item & 1);
       alive = !any_of(bad, kBarCompute4, kComputeThreads);      // also publishes the factors
@@ -763,6 +768,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         }
         named_barrier_sync(kBarCompute4, kComputeThreads);      // the buffer has been read out
       }
+      write_lse();
       if (tid < HN) m_used[tid] = -1e30f;                       // read above by the same thread
       tc_fence_before();                 // O has been read; the next item's PV follows its bar_p
       named_barrier_sync(kBarCompute4, kComputeThreads);        // m_used, red, fac and the P buffers are free again
