@@ -11,32 +11,39 @@
 // Work.  An item is one query and a group of HN = 16, 32 or 64 heads.  With one
 // CTA per item the grid is persistent and each CTA walks items; else the CS
 // CTAs of a thread-block cluster share an item, CTA r taking every CS-th run of
-// 32 list positions, and merge at the end.
+// 32 list positions, and merge at the end.  plan4 below chooses HN and CS.
 //
 // Pipeline of a CTA.  The valid rows of the lists are packed -- J is a multiset,
 // their order is free -- into chunks of 128, so -1 entries cost no tensor work:
 //   gather warps (16): index -> page id -> row, 256 positions at a time, the valid
 //     ones appended to a ring; a chunk's rows (four threads a row) are loaded into
 //     registers while the chunk before is worked on, then widened to BF16 and
-//     stored in the 128 x 512 tile (128-byte swizzle) when its PV has read it.
+//     stored in the 128 x 512 tile (128-byte swizzle) when its PV has read it.  The
+//     nope dims lie in the tile in the order that costs least to widen (dim_of), and
+//     so do Q's and O's.
 //   MMA warp: S^T = KV . Q^T (M = 128 rows, N = HN, K = 512), then O^T += V^T . P^T
 //     (M = 128 dims x 4, N = HN, K = 128): the tile is read K-major for S and
 //     MN-major for PV.
+//   Q warps (3): the next item's Q, once the last S of this one is complete.
 //   softmax warps (8): thread = row, half of the heads.  P is BF16 against a max
 //     that is only moved (and O rescaled) when a score passes it by 2^8: a vote
 //     replaces the max's reduction in nearly every chunk but the first.  The sum
 //     of the probabilities stays with its row's thread until the end.  At an
 //     item's end these warps write the output while the next item's first chunk
 //     is gathered and scored.
-// What bounds it: shared memory, and the hand-overs.  An MMA of M = 128, N = 64, K = 16
-// reads 6 KB and takes 48 cycles, the 128 bytes a clock of shared memory (measured),
-// so while MMAs run other accesses hardly proceed, and the phases of a chunk (3072
-// cycles of MMAs, 1024 of stores) follow one another however they are arranged:
-// handing the tile over by quarters (9900 cycles a chunk, each wait draining the
-// tensor pipe) and two tiles of 64 rows in turn with M = 64 (2 x 5400) were slower.
+// What bounds it.  64 heads: shared memory and the hand-overs.  An MMA of M = 128, N = 64,
+// K = 16 reads 6 KB and takes 48 cycles, the 128 bytes a clock of shared memory
+// (measured), so while MMAs run other accesses hardly proceed, and the phases of a
+// chunk (3072 cycles of MMAs, 1024 of stores, the widening's 7168 words of eight codes)
+// follow one another: 4096 queries of 640 rows take 606 us, 567 TFLOP/s.  The tile is
+// handed over in two halves of its dims: as a whole that call took 687 us, by quarters
+// 629 (a wait drains the tensor pipe).  16 heads: the widening (2.9 us a chunk).  One
+// query: the chain of latencies -- lists, page ids, rows, S, softmax, PV, merge.
 // Widening is exact (fp4.cuh).  P is the one operand rounded (BF16, 2^-8 of a
 // probability at most); S, O, maxima, sums and the partial results that a cluster
 // exchanges are fp32.
+#include <atomic>
+
 #include "attn_common.cuh"
 #include "fp4.cuh"
 
@@ -82,7 +89,7 @@ struct Smem4 {
   static constexpr int kCnt = kMl + kMaxClusterSplits * HN * 8;   // int [16]
   static constexpr int kMeta = kCnt + 64;                // int [4]
   static constexpr int kBar = kMeta + 16;                // barriers, see below
-  static constexpr int kTmem = kBar + (2 * kParts + 11) * 8 + 8;
+  static constexpr int kTmem = kBar + (2 * kParts + 12) * 8;
   static constexpr int kBytes = kTmem + 16;
 };
 
@@ -177,8 +184,14 @@ __device__ __forceinline__ void st_async_v2f32(uint32_t addr, float a, float b, 
                : "memory");
 }
 
+// Where the tile's column `d` belongs: the nope part is widened in the order 0, 4, 1, 5, 2,
+// 6, 3, 7 within eight dims (fp4.cuh), Q is put into that order, too, and O comes out in it.
+__device__ __forceinline__ int dim_of(int d) {
+  return d < DSV4SA_NOPE_DIM ? (d & ~7) | ((d & 7) >> 1) | ((d & 1) << 2) : d;
+}
+
 // Positions of a list of n that CTA r of CS takes, and the k-th of them.
-__device__ __forceinline__ int share_of(int n, int r, int CS) {
+__host__ __device__ __forceinline__ int share_of(int n, int r, int CS) {
   const int whole = n / (kRun * CS), rest = n - whole * kRun * CS - r * kRun;
   return whole * kRun + min(max(rest, 0), kRun);
 }
@@ -209,10 +222,11 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   uint64_t* bar_s = bar_tok + 4;         // S is complete
   uint64_t* bar_p = bar_s + 1;           // P is written
   uint64_t* bar_o = bar_s + 2;           // every PV of the item is complete
-  uint64_t* bar_q = bar_s + 3;           // the item's Q is in place
+  uint64_t* bar_q = bar_s + 3;           // the item's Q has been copied
   uint64_t* bar_item = bar_s + 4;        // the end of the item has been seen
   uint64_t* bar_recv = bar_s + 5;        // merge: the other splits' partials landed
   uint64_t* bar_ml = bar_s + 6;          // merge: the other splits' (m, l) landed
+  uint64_t* bar_q0 = bar_s + 7;          // the first item's Q is in order
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::kTmem);
 
   constexpr int HW = HN / 2;             // heads of a softmax thread
@@ -240,6 +254,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     mbar_init(bar_item, 1);
     mbar_init(bar_recv, 1);
     mbar_init(bar_ml, 1);
+    mbar_init(bar_q0, kComputeThreads / 32);
     fence_mbar_init();
     if (CS > 1) {
       mbar_arrive_expect_tx(bar_recv, static_cast<uint32_t>((CS - 1) * slot_bytes));
@@ -261,6 +276,25 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   const uint32_t tmem = *tmem_holder;
   bool ok = true;                        // no wait of this thread has run out
 
+  // Q's nope part into the order of the tile's columns, when it has arrived: the first
+  // item's by the softmax warps, idle then, the others' by the gather warps.  (By the three
+  // warps that copy it, it delayed the first S: decode of 32 x 640 rows 22.3 us, 4096 x 640
+  // 630 us; here 20.9 and 606.)
+  auto order_q = [&](int n_item, int first, int step) {
+    const bool there = warp_wait(bar_q, n_item & 1);
+#pragma unroll 1
+    for (int u = first; u < HN * (DSV4SA_NOPE_DIM / 8); u += step) {
+      const int h = u / (DSV4SA_NOPE_DIM / 8), v = u - h * (DSV4SA_NOPE_DIM / 8);
+      uint4* at = reinterpret_cast<uint4*>(qs + (v >> 3) * (HN * 128) + sw128_offset(h, v & 7));
+      const uint4 x = *at;
+      *at = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                       __byte_perm(x.y, x.w, 0x7632));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    return there;
+  };
+
   if (warp >= 8 && warp < kMmaWarp) {
     // =========================== gather warps ===========================
     // A wait that runs out is not repeated: the loop, whose length the lists
@@ -275,6 +309,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     for (int item = item0, n_item = 0; item < n_items; item += item_step, ++n_item) {
       const int t = item / groups;
       int cursor = 0, count = 0;                // positions looked up, rows in the ring
+      bool q_ordered = false;
       // look up the next positions, one a thread of half of them
       auto locate = [&]() {
         const int end = min(cursor + kLocate, waited ? total : cw);
@@ -377,14 +412,14 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
             for (int i = 0; i < 4; ++i) {
               const uint32_t w = piece >= 2 ? c4[i ^ 2] : c4[i];
               const uint32_t x = static_cast<uint32_t>(i) ^ (piece & 2);
-              uint4 v = widen8(w, bs.first);
+              uint4 v = widen8_split(w, bs.first);
               if (bs.more) v = scale_up(v, bs.more);
               *reinterpret_cast<uint4*>(blk + sw128_offset(row, static_cast<uint32_t>(4 * (piece & 1)) + x)) = v;
             }
           } else {
             const BlockScale bs = block_scale((sw[3] >> (8 * (piece >> 1))) & 0xFFu);
             const uint32_t u = static_cast<uint32_t>(2 * piece);
-            uint4 v0 = widen8(code3.x, bs.first), v1 = widen8(code3.y, bs.first);
+            uint4 v0 = widen8_split(code3.x, bs.first), v1 = widen8_split(code3.y, bs.first);
             if (bs.more) {
               v0 = scale_up(v0, bs.more);
               v1 = scale_up(v1, bs.more);
@@ -395,6 +430,8 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
             *reinterpret_cast<uint4*>(kv + 7 * kKvBlock + sw128_offset(row, u + 1)) = rope[1];
           }
           if ((b + 1) % (4 / kParts) == 0) {
+            if (!q_ordered && n_item > 0 && ok) ok = order_q(n_item, gt, kGatherThreads);   // Q comes once the last S is complete
+            q_ordered = true;
             fence_proxy_async_smem();      // the tile is read by the tensor core
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_full + b / (4 / kParts));
@@ -407,6 +444,10 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         __syncwarp();
         ++chunk;
         ++token;
+      }
+      if (!q_ordered) {                         // an item without rows: its phase of the barrier passes, too,
+        ok = ok && warp_wait(bar_q, n_item & 1);
+        named_barrier_sync(kBarGather4, kGatherThreads);   // ... for every warp before the next Q may come
       }
       // ---- the item's end, once the end before it has been seen
       if (gt == 0) {
@@ -437,7 +478,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       const uint32_t pd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(ps), HN == 64 ? kRows * 128 : 16, 1024));
       int chunk = 0, token = 0, n_item = 0;
       for (int item = item0; item < n_items && ok; item += item_step, ++n_item) {
-        ok = warp_wait(bar_q, n_item & 1);
+        if (n_item == 0) ok = warp_wait(bar_q0, 0);   // a later item's Q is in order when its tile is
         bool first = true;
         while (ok) {
           ok = warp_wait(bar_tok + (token & 3), (token >> 2) & 1);
@@ -517,6 +558,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
             ++chunk;
           }
           if (ok && !sent && (word < 0 || (word & kLastChunk) != 0)) {
+            ok = warp_wait(bar_q0, 0);   // an empty first item: its Q is still put in order
             load_q(next);
             q_ready();
             sent = true;
@@ -540,6 +582,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     const uint32_t ta = tmem + ((g * 32u) << 16);
     bool waited = !p.early_window;
     if (tid < HN) m_used[tid] = -1e30f;
+    if (item0 < n_items && order_q(0, tid, kComputeThreads) && lane == 0) mbar_arrive(bar_q0);
     named_barrier_sync(kBarCompute4, kComputeThreads);
     int chunk = 0, token = 0, n_item = 0;
     bool alive = true;                                      // the same in all compute threads
@@ -750,7 +793,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
             }
           }
 #pragma unroll
-          for (int x = 0; x < 8; ++x) stage[x * 512 + d] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+          for (int x = 0; x < 8; ++x) stage[x * 512 + dim_of(d)] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
         }
         named_barrier_sync(kBarCompute4, kComputeThreads);
 #pragma unroll
@@ -838,7 +881,10 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       for (int blk = crank * slice / 128; blk < (crank * slice + slice + 127) / 128; ++blk) {
         const int d = blk * 128 + static_cast<int>(g * 32 + lane), dl = d - crank * slice;
         if (d / slice != crank) continue;                       // warp-uniform (half a block when slice is 64)
-        uint16_t* orow = p.out + (static_cast<int64_t>(t) * p.H + h0) * 512 + (d & ~1);
+        // neighbouring dims lie two lanes apart in the nope part, one in the rope part (warp-uniform)
+        const uint32_t apart = d < DSV4SA_NOPE_DIM ? 2u : 1u;
+        const bool odd = (lane & apart) != 0;
+        uint16_t* orow = p.out + (static_cast<int64_t>(t) * p.H + h0) * 512 + (dim_of(d) & ~1);
         const bool rot = rrow != nullptr && d >= 512 - 64;
         const float2 cs = rot ? __ldg(reinterpret_cast<const float2*>(rrow) + ((d - (512 - 64)) >> 1)) : make_float2(1.f, 0.f);
         // four heads at a time, not unrolled: code that runs once a launch is fetched from
@@ -862,17 +908,17 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
             if (f.z != 0.f) v[2] = fmaf(u.z, f.z, v[2]);
             if (f.w != 0.f) v[3] = fmaf(u.w, f.w, v[3]);
           }
-          // lanes (d, d + 1) pair up: even lanes take head x, odd lanes head x + 1, of both dims
+          // the lanes of dims (2 i, 2 i + 1) pair up: one takes head x, the other head x + 1, of both dims
 #pragma unroll
           for (int x = 0; x < 4; x += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[x] : v[x + 1], 1);
-            float lo = (lane & 1) ? got : v[x], hi = (lane & 1) ? v[x + 1] : got;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[x] : v[x + 1], apart);
+            float lo = odd ? got : v[x], hi = odd ? v[x + 1] : got;
             if (rot) {
               const float2 z = rotate_back(lo, hi, cs.x, cs.y);
               lo = z.x;
               hi = z.y;
             }
-            const int h = j0 + x + static_cast<int>(lane & 1);
+            const int h = j0 + x + (odd ? 1 : 0);
             if (h < hreal && ok) *reinterpret_cast<uint32_t*>(orow + h * 512) = pack_bf16x2(lo, hi);
           }
         }
@@ -889,25 +935,106 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
 }
 
 template <int HN>
-int launch_hn4(const AttnParams& p, int groups, int sms, cudaStream_t stream) {
-  constexpr int bytes = Smem4<HN>::kBytes + 1024;   // + alignment slack
-  static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-  if (p.nsplit > 1 && 2 * (p.nsplit - 1) * (512 / p.nsplit) * HN * 4 > Smem4<HN>::kTiles) return DSV4SA_ERR_UNSUPPORTED;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSV4SA_ERR_CUDA;
-  if (!smem_attr_once(dev, 5 + HN / 32, reinterpret_cast<const void*>(sparse_attn_fp4_kernel<HN>), bytes))
-    return DSV4SA_ERR_CUDA;
+constexpr int smem_bytes4() {
+  return Smem4<HN>::kBytes + 1024;       // + alignment slack
+}
+static_assert(smem_bytes4<64>() <= 227 * 1024, "shared memory of one CTA");
+
+template <int HN>
+bool prepare4(int dev) {
+  return smem_attr_once(dev, 5 + HN / 32, reinterpret_cast<const void*>(sparse_attn_fp4_kernel<HN>), smem_bytes4<HN>());
+}
+
+// How many clusters of cs CTAs the device runs at once (their CTAs have to be on SMs that
+// are wired together, so fewer than the SMs would suggest: of eight CTAs eight clusters ran
+// at once, sixteen took twice as long).  Asked once for each device.
+template <int HN>
+int cluster_slots(int dev, int cs) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][4];
+  const int at = cs == 2 ? 1 : (cs == 4 ? 2 : 3);
+  if (dev < 0 || dev >= kDevices) return 0;
+  const int have = known[dev][at].load(std::memory_order_relaxed);
+  if (have > 0) return have - 1;
+  if ((cs - 1) * (512 / cs) * HN * 8 > Smem4<HN>::kTiles || !prepare4<HN>(dev)) return 0;   // the merge's slots, in and out
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cs));
+  cfg.blockDim = dim3(kThreads4);
+  cfg.dynamicSmemBytes = smem_bytes4<HN>();
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, sparse_attn_fp4_kernel<HN>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[dev][at].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+template <int HN>
+int launch_hn4(const AttnParams& p, int groups, int dev, int sms, cudaStream_t stream) {
+  if (!prepare4<HN>(dev)) return DSV4SA_ERR_CUDA;
   const int64_t items = static_cast<int64_t>(p.T) * groups;
   if (items * p.nsplit > INT32_MAX) return DSV4SA_ERR_UNSUPPORTED;
   cudaError_t e;
   if (p.nsplit == 1) {
     e = launch_pdl(sparse_attn_fp4_kernel<HN>, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads4),
-                   bytes, stream, p, groups);
+                   smem_bytes4<HN>(), stream, p, groups);
   } else {
     e = launch_cluster_pdl(sparse_attn_fp4_kernel<HN>, dim3(static_cast<unsigned>(items * p.nsplit)), dim3(kThreads4),
-                           bytes, p.nsplit, stream, p, groups);
+                           smem_bytes4<HN>(), p.nsplit, stream, p, groups);
   }
   return e == cudaSuccess ? DSV4SA_OK : DSV4SA_ERR_CUDA;
+}
+
+// Heads of an item and CTAs that share it, by the time they should take: the fixed part of
+// a call, a chunk of 128 rows, the step from one item to the next and a cluster's merge, in
+// us, as measured for each size of item (calls of 128 to 2176 rows, 1 to 128 queries, 16 to
+// 128 heads; the estimates are within a tenth of the times).  Few heads an item cost less
+// each -- S, P and O shrink with them, and the merge moves less -- but every item widens its
+// rows anew.  So few queries run as many small items, e.g. one query of 64 heads over 640
+// rows: 4 items x 8 CTAs 10.5 us, 1 x 4 19.7; 32 of them: 2 x 2 18.5, 1 x 4 21.5, 4 x 1 20.4;
+// and many queries as large ones, 128 of them: 1 x 1 27.6 us, 4 x 1 69.
+struct Cost4 {
+  float fixed, chunk, next, merge;
+};
+constexpr Cost4 kCost4[3] = {{4.9f, 2.95f, 1.7f, 2.5f}, {5.5f, 3.2f, 3.1f, 3.2f}, {7.7f, 3.7f, 4.4f, 4.2f}};
+constexpr int kHeads4[3] = {16, 32, 64};
+
+struct Plan4 {
+  int hn, groups, cs;
+};
+Plan4 plan4(int32_t mode, const AttnParams& p, int dev, int sms) {
+  Plan4 best{64, (p.H + 63) / 64, 1};
+  float least = 3.4e38f;
+  for (int i = 0; i < 3; ++i) {
+    if (i > 0 && p.H <= kHeads4[i - 1]) break;               // the smaller item holds all heads
+    const int hn = kHeads4[i], groups = (p.H + hn - 1) / hn;
+    const int64_t items = static_cast<int64_t>(p.T) * groups;
+    for (int cs = 1; cs <= kMaxClusterSplits; cs *= 2) {
+      const int rows = share_of(p.kw, 0, cs) + share_of(p.kc, 0, cs), chunks = (rows + kRows - 1) / kRows;
+      int slots = sms;
+      if (cs > 1) {
+        if (mode != DSV4SA_ATTN_DECODE || p.kw + p.kc <= kRows || items > sms / cs) break;
+        slots = i == 0 ? cluster_slots<16>(dev, cs) : (i == 1 ? cluster_slots<32>(dev, cs) : cluster_slots<64>(dev, cs));
+        if (items > slots) break;
+      }
+      const Cost4& c = kCost4[i];
+      const float rounds = static_cast<float>((items + slots - 1) / slots);
+      const float us = c.fixed + rounds * static_cast<float>(chunks) * c.chunk + (rounds - 1.f) * c.next + (cs > 1 ? c.merge : 0.f);
+      if (us < least) {
+        least = us;
+        best = Plan4{hn, groups, cs};
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -918,19 +1045,12 @@ int launch_fp4(int32_t mode, AttnParams& p, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSV4SA_ERR_CUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DSV4SA_ERR_CUDA;
-  int hn = p.H <= 16 ? 16 : (p.H <= 32 ? 32 : 64);
-  int groups = (p.H + hn - 1) / hn;
-  p.nsplit = 1;
-  const int rows = p.kc + p.kw;
-  if (mode == DSV4SA_ATTN_DECODE && rows > kRows) {
-    const int64_t items = static_cast<int64_t>(p.T) * groups;
-    const int most = hn == 64 ? 4 : 8;   // the merge's slots of 64 heads fit in the tiles up to 4 splits
-    while (p.nsplit < most && items * p.nsplit * 2 <= sms) p.nsplit *= 2;
-  }
-  switch (hn) {
-    case 16: return launch_hn4<16>(p, groups, sms, stream);
-    case 32: return launch_hn4<32>(p, groups, sms, stream);
-    default: return launch_hn4<64>(p, groups, sms, stream);
+  const Plan4 plan = plan4(mode, p, dev, sms);
+  p.nsplit = plan.cs;
+  switch (plan.hn) {
+    case 16: return launch_hn4<16>(p, plan.groups, dev, sms, stream);
+    case 32: return launch_hn4<32>(p, plan.groups, dev, sms, stream);
+    default: return launch_hn4<64>(p, plan.groups, dev, sms, stream);
   }
 }
 

@@ -38,6 +38,21 @@ __device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t first) {
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
+// The same in the order 0, 4, 1, 5, 2, 6, 3, 7: codes 16 bits apart share a register from
+// the start, so one masked word times 2^6 + 2^12 (or 2^2 + 2^8, a nibble further on) places
+// magnitude and sign of both: 17 instructions instead of 24.
+__device__ __forceinline__ uint4 widen8_split(uint32_t w, uint32_t first) {
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&first);
+  uint32_t v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t part = j < 2 ? w : w >> 8;
+    const uint32_t x = ((j & 1) ? (part & 0x00F000F0u) * 0x0104u : (part & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), s);
+    v[j] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
 // Eight values times 2^more (rarely called).
 __device__ __forceinline__ uint4 scale_up(uint4 v, uint32_t more) {
   // in two steps: 2^more may pass BF16's range although the product does not

@@ -120,6 +120,23 @@ def test_rows_that_no_list_names_may_hold_anything(L, H, T):
     assert L.dsv4sa_check_errors() == (0, 0)
 
 
+@pytest.mark.parametrize("T,H,kc", [(1, 16, 2048), (8, 16, 500), (32, 16, 500), (64, 16, 1000), (3, 40, 2048), (4, 64, 2048),
+                                    (16, 64, 500), (32, 64, 500), (64, 64, 500), (32, 64, 2048), (64, 64, 2048), (130, 64, 2048),
+                                    (5, 128, 130), (200, 20, 300)])
+def test_every_split_of_heads_and_rows(L, T, H, kc):
+    """Batches and lists over which the work is dealt out differently: items of 16, 32 and
+    64 heads, alone or over clusters of 2, 4 and 8 (and several items a CTA)."""
+    c = Case(L, T, H, kc, 128, seed=T + H + kc, ring=128, entries=3000, empty=(T // 3,))
+    out, lse = c.run(L, L.dsv4sa_sparse_attn_decode)
+    assert L.dsv4sa_check_errors() == (0, 0)
+    c.check(out, lse, rows=sorted({0, 1 % T, T // 3, T // 2, T - 1}))
+    pre, lse_p = c.run(L, L.dsv4sa_sparse_attn_prefill)         # never over clusters
+    c.check(pre, lse_p, rows=sorted({0, T // 3, T - 1}))
+    # everywhere: the two differ by no more than their bounds, 2^-6 of the largest value being far above both
+    assert (out.double() - pre.double()).abs().max() <= 2.0 ** -6 * float(out.abs().max())
+    assert (lse.double() - lse_p.double()).abs().max() <= 2.0 ** -12 * float(lse.abs().max().clamp(min=1.0))
+
+
 def test_long_window_without_a_list_and_long_sequences(L):
     """Entries far up a sequence: page-table columns past 2^15, entries past 2^21."""
     rng = np.random.default_rng(4)
