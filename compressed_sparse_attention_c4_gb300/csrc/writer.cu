@@ -267,12 +267,22 @@ __global__ void __launch_bounds__(kThreads) fp4_key_write_kernel(const WriterPar
 // exponent as one byte (the last two bytes of the scale row are padding, never
 // written).  A block that holds an infinity or a NaN gets the exponent byte 255
 // (E8M0 NaN) and codes 0, so it reads back as NaN.  kRowsW rows per warp are in
-// flight: the row loads are independent of the entry -> page look-ups.
+// flight: the row loads are independent of the entry -> page look-ups (65529 rows 15.0 us,
+// 13.5 being the bytes at the measured copy bandwidth; 15.4 with one row, 14.8 with four,
+// but 32 rows take 1.6, 2.1 and 2.5 us).  The integer pipe is nearly as busy (73%).
 constexpr int kRowsW = 2;
 
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
-  uint32_t r;   // nearest, ties to even, saturating: the codes e2m1_code counts out
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+// Eight values -> eight codes, nearest, ties to even, saturating (as e2m1_code counts out).
+__device__ __forceinline__ uint32_t e2m1x8(const float2* y) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(y[0].x), "f"(y[0].y), "f"(y[1].x), "f"(y[1].y), "f"(y[2].x), "f"(y[2].y), "f"(y[3].x), "f"(y[3].y));
   return r;
 }
 
@@ -292,18 +302,18 @@ __device__ __forceinline__ uint32_t quantise_unit(const uint4 v, uint32_t& expon
   m2 = max2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
   const uint32_t mag = max(m2 << 16, m2 & 0x7FFF0000u);   // as fp32 bits
   const bool finite = mag < 0x7F800000u;
-  const float t = __fmul_rn(fmaxf(__uint_as_float(finite ? mag : 0u), kFp4AmaxFloor), kFp4MaxInv);
-  const uint32_t tb = __float_as_uint(t);                 // normal: t >= 2^-126
-  const int e = static_cast<int>((tb >> 23) & 0xFFu) - 127 + ((tb & 0x7FFFFFu) != 0u ? 1 : 0);   // <= 126
-  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);                       // 2^-e
-  uint32_t codes = 0;
+  // e = ceil(log2(max(amax, 6 * 2^-126) * fp32(1/6))).  amax has eight significant bits, so
+  // the product is at most a power of two exactly when amax's are at most 1.5: the exponent
+  // field goes up by one above that, and by two less than the field's in any case.
+  const uint32_t top = max(finite ? mag : 0u, 0x01C00000u);       // 6 * 2^-126
+  const uint32_t e = ((top + 0x003FFFFFu) >> 23) - 2u;            // the E8M0 byte: 1 .. 253
+  const float inv = __uint_as_float((254u - e) << 23);            // 2^-(e - 127)
+  float2 y[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 y = mul2(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), make_float2(inv, inv));
-    codes |= e2m1x2(y.x, y.y) << (8 * j);
-  }
-  exponent = finite ? static_cast<uint32_t>(e + 127) : 255u;
-  return finite ? codes : 0u;
+  for (int j = 0; j < 4; ++j)
+    y[j] = mul2(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), make_float2(inv, inv));
+  exponent = finite ? e : 255u;
+  return finite ? e2m1x8(y) : 0u;
 }
 
 __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterParams p) {
@@ -359,8 +369,11 @@ __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterPara
 // BF16, or e2m1(code) * 2^(b - 127), which BF16 holds exactly (2 significant
 // bits; past its range an infinity, as a product of the two rounds to).  A warp per
 // row, lane c writing the 16-byte units c and 32 + c of it as in the writer; kRowsR
-// rows per warp in flight, since each is three dependent loads (entry, page id, row).
-constexpr int kRowsR = 4;
+// rows per warp in flight.  One: a row is three dependent loads (entry, page id, row), but
+// many warps hide them as well as many rows a warp do (65529 FP4 rows 16.8 us with 1 row,
+// 17.5 with 2, 16.9 with 4, 20.1 with 8) and few rows are read sooner (32 rows 1.7 us, 2.1,
+// 2.7, 3.5).
+constexpr int kRowsR = 1;
 
 struct ReaderParams {
   WriterParams w;          // rows unused
