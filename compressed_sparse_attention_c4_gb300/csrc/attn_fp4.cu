@@ -34,7 +34,7 @@
 // What bounds it.  64 heads: shared memory and the hand-overs.  An MMA of M = 128, N = 64,
 // K = 16 reads 6 KB and takes 48 cycles, the 128 bytes a clock of shared memory
 // (measured), so while MMAs run other accesses hardly proceed, and the phases of a
-// chunk (3072 cycles of MMAs, 1024 of stores, the widening's 7168 words of eight codes)
+// chunk (about 3000 cycles of MMAs, 1000 of stores, the widening's 7168 words of eight codes)
 // follow one another: 4096 queries of 640 rows take 606 us, 567 TFLOP/s.  The tile is
 // handed over in two halves of its dims: as a whole that call took 687 us, by quarters
 // 629 (a wait drains the tensor pipe).  16 heads: the widening (2.9 us a chunk).  One
