@@ -37,8 +37,10 @@
 // chunk (about 3000 cycles of MMAs, 1000 of stores, the widening's 7168 words of eight codes)
 // follow one another: 4096 queries of 640 rows take 606 us, 567 TFLOP/s.  The tile is
 // handed over in two halves of its dims: as a whole that call took 687 us, by quarters
-// 629 (a wait drains the tensor pipe).  16 heads: the widening (2.9 us a chunk).  One
-// query: the chain of latencies -- lists, page ids, rows, S, softmax, PV, merge.
+// 629 (a wait drains the tensor pipe).  Two tiles of 64 rows in turn, a group of gather warps
+// for each, took 726: each step from one kind of warp to the next costs 400 to 1600 cycles
+// whatever the tile's size.  16 heads: the widening (2.8 us a chunk).  One query: the chain of
+// latencies -- lists, page ids, rows, S, softmax, PV, merge.
 // Widening is exact (fp4.cuh).  P is the one operand rounded (BF16, 2^-8 of a
 // probability at most); S, O, maxima, sums and the partial results that a cluster
 // exchanges are fp32.
@@ -63,7 +65,7 @@ constexpr int kRun = 32;                 // list positions a CTA of a cluster ta
 constexpr int kFp4RopeOff = 14336;       // KV_FP4 page layout (see dsv4sa.h)
 constexpr int kFp4ScaleOff = 22528;
 constexpr float kSlack = 8.f;            // log2 units a score may pass the max in use by
-constexpr int kParts = 2;                // the tile is handed over in this many parts of its dims (1, 2 or 4)
+constexpr int kHalf = 4 * kKvBlock;      // bytes of a half of the tile: 128 rows x 256 dims
 constexpr int kLastChunk = 256;          // meta: rows of the chunk (<= 128), and this for an item's last
 // Registers per thread (setmaxnreg): the launch gives 896 x 72 = 64512, the three
 // kinds of warpgroup then hold 256 x 96 + 512 x 64 + 128 x 56 = 64512.
@@ -76,10 +78,15 @@ constexpr uint32_t kBarGather4 = 2;
 
 template <int HN>
 struct Smem4 {
+  // Halves of tiles.  With 16 heads a third one fits: the next chunk's first half is
+  // widened before the current one's PV (128 queries of 8 heads, up to 1152 rows: 31.6 us,
+  // 32.5 with two).
+  static constexpr int kSlots = HN == 16 ? 3 : 2;
+  static constexpr int kStage = HN == 16 ? 8 : 16;       // heads of an output step
   static constexpr int kKv = 0;
-  static constexpr int kQ = kKvBytes;                    // 8 column blocks x HN rows x 128 B
+  static constexpr int kQ = kSlots * kHalf;              // 8 column blocks x HN rows x 128 B
   static constexpr int kP = kQ + 8 * HN * 128;           // 128 rows x 128 B, or 2 blocks x HN rows x 128 B; output staging
-  static constexpr int kTiles = kP + kRows * 128;        // end of the tiles (the merge may use all of them)
+  static constexpr int kTiles = kP + kStage * 1024;      // end of the tiles (the merge may use all of them)
   static constexpr int kRing_ = kTiles;                  // uint64 [kRing]
   static constexpr int kRed = kRing_ + kRing * 8;        // float [HN][4]
   static constexpr int kM = kRed + HN * 16;              // float [HN] each
@@ -89,7 +96,7 @@ struct Smem4 {
   static constexpr int kCnt = kMl + kMaxClusterSplits * HN * 8;   // int [16]
   static constexpr int kMeta = kCnt + 64;                // int [4]
   static constexpr int kBar = kMeta + 16;                // barriers, see below
-  static constexpr int kTmem = kBar + (2 * kParts + 12) * 8;
+  static constexpr int kTmem = kBar + (2 * kSlots + 13) * 8;
   static constexpr int kBytes = kTmem + 16;
 };
 
@@ -216,9 +223,9 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   float2* mlr = reinterpret_cast<float2*>(smem + S::kMl);
   int* wcnt = reinterpret_cast<int*>(smem + S::kCnt);
   volatile int* meta = reinterpret_cast<volatile int*>(smem + S::kMeta);
-  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + S::kBar);   // [kParts]: that part of the chunk's dims is in the tile
-  uint64_t* bar_free = bar_full + kParts;    // [kParts]: ... has been read by PV
-  uint64_t* bar_tok = bar_free + kParts;     // [4]: a chunk's (or an item's end's) meta is written
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + S::kBar);   // [slots]: half of a chunk's dims is in place
+  uint64_t* bar_free = bar_full + S::kSlots; // [slots]: ... has been read by PV
+  uint64_t* bar_tok = bar_free + S::kSlots;  // [4]: a chunk's (or an item's end's) meta is written
   uint64_t* bar_s = bar_tok + 4;         // S is complete
   uint64_t* bar_p = bar_s + 1;           // P is written
   uint64_t* bar_o = bar_s + 2;           // every PV of the item is complete
@@ -227,6 +234,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   uint64_t* bar_recv = bar_s + 5;        // merge: the other splits' partials landed
   uint64_t* bar_ml = bar_s + 6;          // merge: the other splits' (m, l) landed
   uint64_t* bar_q0 = bar_s + 7;          // the first item's Q is in order
+  uint64_t* bar_qfree = bar_s + 8;       // every S of the item is complete
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::kTmem);
 
   constexpr int HW = HN / 2;             // heads of a softmax thread
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
   const int slot_bytes = slice * HN * 4;
 
   if (tid == 0) {
-    for (int i = 0; i < kParts; ++i) {
+    for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(bar_full + i, kGatherThreads / 32);
       mbar_init(bar_free + i, 1);
     }
@@ -255,6 +263,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     mbar_init(bar_recv, 1);
     mbar_init(bar_ml, 1);
     mbar_init(bar_q0, kComputeThreads / 32);
+    mbar_init(bar_qfree, 1);
     fence_mbar_init();
     if (CS > 1) {
       mbar_arrive_expect_tx(bar_recv, static_cast<uint32_t>((CS - 1) * slot_bytes));
@@ -303,7 +312,8 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     const int gt = tid - kComputeThreads;
     const int row = gt >> 2, piece = gt & 3;
     bool waited = !p.early_window;
-    int chunk = 0, token = 0;
+    int slot = 0, token = 0;                    // the next half's
+    uint32_t round = 0;                         // how often all slots have been filled
     int head = 0;                               // ring: first located row not yet loaded
     const int cw = share_of(p.kw, crank, CS), total = cw + share_of(p.kc, crank, CS);   // this CTA's positions of an item
     for (int item = item0, n_item = 0; item < n_items; item += item_step, ++n_item) {
@@ -396,17 +406,18 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         const bool last = count == 0 && cursor >= total;
         // ---- look ahead while the loads are in flight
         if (count < kRows && cursor < total && (waited || cursor < cw)) locate();
-        // ---- into the tile, part by part, when the previous chunk's PV has read it
+        // ---- into the tile, half by half, when the half that was there has been read by its PV
         const uint32_t sw[4] = {scl.x, scl.y, scl.z, scl.w};
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          if (b % (4 / kParts) == 0 && chunk > 0 && ok) ok = warp_wait(bar_free + b / (4 / kParts), (chunk - 1) & 1);
+          if ((b & 1) == 0 && round > 0 && ok) ok = warp_wait(bar_free + slot, (round - 1) & 1);
+          uint8_t* half = kv + slot * kHalf;
           if (b < 3) {
             // 32 values: units 4 (piece & 1) + x of column block 2 b + (piece >> 1).  The
             // upper two pieces take x in the order 2, 3, 0, 1, so that the eight lanes of
             // two rows hit eight different bank groups.
             const BlockScale bs = block_scale((sw[b] >> (8 * piece)) & 0xFFu);
-            uint8_t* blk = kv + (2 * b + (piece >> 1)) * kKvBlock;
+            uint8_t* blk = half + (2 * (b & 1) + (piece >> 1)) * kKvBlock;
             const uint32_t c4[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -424,17 +435,19 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
               v0 = scale_up(v0, bs.more);
               v1 = scale_up(v1, bs.more);
             }
-            *reinterpret_cast<uint4*>(kv + 6 * kKvBlock + sw128_offset(row, u)) = v0;
-            *reinterpret_cast<uint4*>(kv + 6 * kKvBlock + sw128_offset(row, u + 1)) = v1;
-            *reinterpret_cast<uint4*>(kv + 7 * kKvBlock + sw128_offset(row, u)) = rope[0];
-            *reinterpret_cast<uint4*>(kv + 7 * kKvBlock + sw128_offset(row, u + 1)) = rope[1];
+            *reinterpret_cast<uint4*>(half + 2 * kKvBlock + sw128_offset(row, u)) = v0;
+            *reinterpret_cast<uint4*>(half + 2 * kKvBlock + sw128_offset(row, u + 1)) = v1;
+            *reinterpret_cast<uint4*>(half + 3 * kKvBlock + sw128_offset(row, u)) = rope[0];
+            *reinterpret_cast<uint4*>(half + 3 * kKvBlock + sw128_offset(row, u + 1)) = rope[1];
           }
-          if ((b + 1) % (4 / kParts) == 0) {
+          if ((b & 1) == 1) {
             if (!q_ordered && n_item > 0 && ok) ok = order_q(n_item, gt, kGatherThreads);   // Q comes once the last S is complete
             q_ordered = true;
             fence_proxy_async_smem();      // the tile is read by the tensor core
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_full + b / (4 / kParts));
+            if (lane == 0) mbar_arrive(bar_full + slot);
+            slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+            round += slot == 0 ? 1u : 0u;
           }
           if (b == 0 && gt == 0) {         // the meta slot's last token, four ago, has been read
             meta[token & 3] = n | (last ? kLastChunk : 0);
@@ -442,7 +455,6 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
           }
         }
         __syncwarp();
-        ++chunk;
         ++token;
       }
       if (!q_ordered) {                         // an item without rows: its phase of the barrier passes, too,
@@ -477,42 +489,57 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       // P: [row][64 heads] (N contiguous) for 64 heads, else [head][64 rows] x 2
       const uint32_t pd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(ps), HN == 64 ? kRows * 128 : 16, 1024));
       int chunk = 0, token = 0, n_item = 0;
+      int slot = 0;
+      uint32_t round = 0;
       for (int item = item0; item < n_items && ok; item += item_step, ++n_item) {
         if (n_item == 0) ok = warp_wait(bar_q0, 0);   // a later item's Q is in order when its tile is
-        bool first = true;
+        bool first = true, q_freed = false;
         while (ok) {
           ok = warp_wait(bar_tok + (token & 3), (token >> 2) & 1);
           if (!ok) break;
           const int word = meta[token & 3];
           ++token;
           if (word < 0) break;
-#pragma unroll 1
-          for (int b = 0; b < 8; ++b) {    // not unrolled: 32 pairs of descriptors would not fit in registers
-            if (b % (8 / kParts) == 0) {
-              ok = ok && warp_wait(bar_full + b / (8 / kParts), chunk & 1);
-              tc_fence_after();
-            }
+          int at[2];                       // the chunk's halves
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_elect(tmem + kColS, kvk + ((b * kKvBlock + kk * 32) >> 4), qk + ((b * HN * 128 + kk * 32) >> 4), hi, idesc_s,
-                            b > 0 || kk > 0 ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && warp_wait(bar_full + slot, round & 1);
+            tc_fence_after();
+            at[h] = slot * kHalf;
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {  // not unrolled: the descriptors would not fit in registers
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16_elect(tmem + kColS, kvk + ((at[h] + b * kKvBlock + kk * 32) >> 4), qk + (((4 * h + b) * HN * 128 + kk * 32) >> 4),
+                              hi, idesc_s, h > 0 || b > 0 || kk > 0 ? 1u : 0u);
+            }
+            slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+            round += slot == 0 ? 1u : 0u;
           }
           mma_commit_elect(bar_s);
+          if ((word & kLastChunk) != 0) {
+            mma_commit_elect(bar_qfree);
+            q_freed = true;
+          }
           ok = ok && warp_wait(bar_p, chunk & 1);
           tc_fence_after();
-#pragma unroll 1
-          for (int mb = 0; mb < 4; ++mb) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t bo = (HN == 64 ? kk * 2048 : (kk >> 2) * (HN * 128) + (kk & 3) * 32) >> 4;
-              mma_f16_elect(tmem + kColO + mb * HN, kvm + ((2 * mb * kKvBlock + kk * 2048) >> 4), pd + bo, hi, idesc_o,
-                            (!first || kk > 0) ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+            for (int mb = 0; mb < 2; ++mb) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t bo = (HN == 64 ? kk * 2048 : (kk >> 2) * (HN * 128) + (kk & 3) * 32) >> 4;
+                mma_f16_elect(tmem + kColO + (2 * h + mb) * HN, kvm + ((at[h] + 2 * mb * kKvBlock + kk * 2048) >> 4), pd + bo, hi,
+                              idesc_o, (!first || kk > 0) ? 1u : 0u);
+              }
             }
-            if ((mb + 1) % (4 / kParts) == 0) mma_commit_elect(bar_free + mb / (4 / kParts));
+            mma_commit_elect(bar_free + at[h] / kHalf);
           }
           first = false;
           ++chunk;
         }
+        if (!q_freed) mma_commit_elect(bar_qfree);
         mma_commit_elect(bar_o);
       }
     } else {
@@ -540,30 +567,16 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         load_q(item0);
         q_ready();
       }
-      int chunk = 0, token = 0;
-      for (int item = item0; item < n_items && ok; item += item_step) {
+      for (int item = item0, n_item = 0; item + item_step < n_items && ok; item += item_step, ++n_item) {
         const int next = item + item_step;
-        if (next < n_items && qt == 0) {
+        if (qt == 0) {
           const int t = next / groups, h0 = (next - t * groups) * HN;
           prefetch_l2(p.q + (static_cast<int64_t>(t) * p.H + h0) * 512, static_cast<uint32_t>(min(HN, p.H - h0)) * 1024u);
         }
-        bool sent = next >= n_items;
-        while (ok) {
-          ok = warp_wait(bar_tok + (token & 3), (token >> 2) & 1);
-          if (!ok) break;
-          const int word = meta[token & 3];
-          ++token;
-          if (word >= 0) {
-            ok = warp_wait(bar_s, chunk & 1);
-            ++chunk;
-          }
-          if (ok && !sent && (word < 0 || (word & kLastChunk) != 0)) {
-            ok = warp_wait(bar_q0, 0);   // an empty first item: its Q is still put in order
-            load_q(next);
-            q_ready();
-            sent = true;
-          }
-          if (word < 0) break;
+        ok = warp_wait(bar_qfree, n_item & 1);
+        if (ok) {
+          load_q(next);
+          q_ready();
         }
       }
       cp_async_wait();
@@ -760,44 +773,45 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       tc_fence_after();
       if (!alive) break;
       if (tid == 0) mbar_arrive(bar_item);                      // the MMA warp has read the end's token, too
-      // ---- output, 16 heads at a time: thread = dim, staged in the P buffer as words of
-      // (head, head + 1), [8][512], read back eight dims a thread and stored 16 bytes a head
+      // ---- output, 8 or 16 heads at a time: thread = dim, staged in the P buffer as words of
+      // (head, head + 1), [4 or 8][512], read back eight dims a thread and stored 16 bytes a head
       const float4* rrow = rope_row(p, t);
       uint32_t* stage = reinterpret_cast<uint32_t*>(ps);
+      constexpr int kStage = S::kStage;
 #pragma unroll 1
-      for (int j0 = 0; j0 < hreal; j0 += 16) {
-        float f[16];
+      for (int j0 = 0; j0 < hreal; j0 += kStage) {
+        float f[kStage];
 #pragma unroll
-        for (int x = 0; x < 16; x += 4) {
+        for (int x = 0; x < kStage; x += 4) {
           const float4 q = *reinterpret_cast<const float4*>(fac + j0 + x);
           f[x] = q.x, f[x + 1] = q.y, f[x + 2] = q.z, f[x + 3] = q.w;
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          float v[16];
+          float v[kStage];
           if (have_o) {
-            tmem_load_cols<16>(ta + kColO + (hh * 2 + b) * HN + j0, v);
+            tmem_load_cols<kStage>(ta + kColO + (hh * 2 + b) * HN + j0, v);
           } else {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) v[x] = 0.f;
+            for (int x = 0; x < kStage; ++x) v[x] = 0.f;
           }
           const int d = (static_cast<int>(hh) * 2 + b) * 128 + r;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] *= f[x];
+          for (int x = 0; x < kStage; ++x) v[x] *= f[x];
           if (rrow != nullptr && d >= 512 - 64) {               // warp-uniform: dims (d, d ^ 1) are a pair, lanes (l, l ^ 1)
             const float2 cs = __ldg(reinterpret_cast<const float2*>(rrow) + ((d - (512 - 64)) >> 1));
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
+            for (int x = 0; x < kStage; ++x) {
               const float other = __shfl_xor_sync(0xffffffffu, v[x], 1);
               v[x] = (lane & 1) ? fmaf(v[x], cs.x, -(other * cs.y)) : fmaf(v[x], cs.x, other * cs.y);
             }
           }
 #pragma unroll
-          for (int x = 0; x < 8; ++x) stage[x * 512 + dim_of(d)] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+          for (int x = 0; x < kStage / 2; ++x) stage[x * 512 + dim_of(d)] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
         }
         named_barrier_sync(kBarCompute4, kComputeThreads);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kStage / 8; ++i) {
           const int hp = (tid >> 6) + 4 * i, h = j0 + 2 * hp;   // heads h, h + 1; dims 8 (tid & 63) ..
           const uint4 a = *reinterpret_cast<const uint4*>(stage + hp * 512 + (tid & 63) * 8);
           const uint4 c = *reinterpret_cast<const uint4*>(stage + hp * 512 + (tid & 63) * 8 + 4);
@@ -938,7 +952,7 @@ template <int HN>
 constexpr int smem_bytes4() {
   return Smem4<HN>::kBytes + 1024;       // + alignment slack
 }
-static_assert(smem_bytes4<64>() <= 227 * 1024, "shared memory of one CTA");
+static_assert(smem_bytes4<16>() <= 227 * 1024 && smem_bytes4<64>() <= 227 * 1024, "shared memory of one CTA");
 
 template <int HN>
 bool prepare4(int dev) {
