@@ -35,12 +35,12 @@
 // K = 16 reads 6 KB and takes 48 cycles, the 128 bytes a clock of shared memory
 // (measured), so while MMAs run other accesses hardly proceed, and the phases of a
 // chunk (about 3000 cycles of MMAs, 1000 of stores, the widening's 7168 words of eight codes)
-// follow one another: 4096 queries of 640 rows take 606 us, 567 TFLOP/s.  The tile is
+// follow one another: 4096 queries of 640 rows take 594 us, 578 TFLOP/s.  The tile is
 // handed over in two halves of its dims: as a whole that call took 687 us, by quarters
-// 629 (a wait drains the tensor pipe).  Two tiles of 64 rows in turn, a group of gather warps
-// for each, took 726: each step from one kind of warp to the next costs 400 to 1600 cycles
-// whatever the tile's size.  16 heads: the widening (2.8 us a chunk).  One query: the chain of
-// latencies -- lists, page ids, rows, S, softmax, PV, merge.
+// 629, by halves 617 then (a wait drains the tensor pipe).  Two tiles of 64 rows in turn, a
+// group of gather warps for each, took 726 against 610: each step from one kind of warp to
+// the next costs 400 to 1600 cycles whatever the tile's size.  16 heads: the widening (2.8 us
+// a chunk).  One query: the chain of latencies -- lists, page ids, rows, S, softmax, PV, merge.
 // Widening is exact (fp4.cuh).  P is the one operand rounded (BF16, 2^-8 of a
 // probability at most); S, O, maxima, sums and the partial results that a cluster
 // exchanges are fp32.
@@ -68,10 +68,15 @@ constexpr float kSlack = 8.f;            // log2 units a score may pass the max 
 constexpr int kHalf = 4 * kKvBlock;      // bytes of a half of the tile: 128 rows x 256 dims
 constexpr int kLastChunk = 256;          // meta: rows of the chunk (<= 128), and this for an item's last
 // Registers per thread (setmaxnreg): the launch gives 896 x 72 = 64512, the three
-// kinds of warpgroup then hold 256 x 96 + 512 x 64 + 128 x 56 = 64512.
-constexpr int kRegsCompute = 96, kRegsGather = 64, kRegsMma = 56;
-static_assert(kComputeThreads * kRegsCompute + kGatherThreads * kRegsGather + 128 * kRegsMma <= kThreads4 * 72,
-              "the register shares fit in the launch's");
+// kinds of warpgroup then hold 256 x 96 + 512 x 64 + 128 x 56 = 64512, or, for 64 heads,
+// whose softmax threads have 32 scores and sums each, 256 x 112 + 512 x 56 + 128 x 56 (4096
+// queries of 64 heads 594 us, 607 with the first shares; 128 of 8 heads 33.7 us, 31.6).
+template <int HN>
+struct Regs4 {
+  static constexpr int kCompute = HN == 64 ? 112 : 96, kGather = HN == 64 ? 56 : 64, kMma = 56;
+  static_assert(kComputeThreads * kCompute + kGatherThreads * kGather + 128 * kMma <= kThreads4 * 72,
+                "the register shares fit in the launch's");
+};
 
 constexpr uint32_t kBarCompute4 = 1;     // named barriers
 constexpr uint32_t kBarGather4 = 2;
@@ -308,7 +313,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     // =========================== gather warps ===========================
     // A wait that runs out is not repeated: the loop, whose length the lists
     // alone decide, goes on without waiting.
-    regs_dec<kRegsGather>();
+    regs_dec<Regs4<HN>::kGather>();
     const int gt = tid - kComputeThreads;
     const int row = gt >> 2, piece = gt & 3;
     bool waited = !p.early_window;
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     }
   } else if (warp >= kMmaWarp) {
     // =========================== MMA warp ===========================
-    regs_dec<kRegsMma>();
+    regs_dec<Regs4<HN>::kMma>();
     if (warp == kMmaWarp) {
       const uint32_t idesc_s = make_idesc(kFmtBF16, kFmtBF16, 0, 0, 128, HN);
       const uint32_t idesc_o = make_idesc(kFmtBF16, kFmtBF16, 1, HN == 64 ? 1 : 0, 128, HN);
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     }
   } else {
     // =========================== softmax warps ===========================
-    regs_inc<kRegsCompute>();
+    regs_inc<Regs4<HN>::kCompute>();
     const uint32_t g = warp & 3u, hh = warp >> 2;
     const int r = static_cast<int>(g * 32 + lane);          // row of the chunk, and TMEM lane
     const int hb = static_cast<int>(hh) * HW;               // first head of this thread
