@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256, kTpr <= 32 && kUnits 
         // block is below the floor): three roundings from the sum to the code, where
         // norm, weight, scale and quotient in turn take five.  The quotient is the
         // hardware's estimate with its residual added; the conversion saturates.
-        const float r = __fdividef(1.f, amax), k0 = 448.f * r;
+        // (Of amax / 256: above 2^126 the hardware's quotient would be 0.)
+        const float r = __fdividef(0x1p-8f, amax * 0x1p-8f), k0 = 448.f * r;
         const float inv = amax * rstd > kAmaxFloor ? fmaf(fmaf(-amax, k0, 448.f), r, k0) : rstd * (448.f / kAmaxFloor);
         const float2 inv2 = make_float2(inv, inv);
         uint32_t q[2];

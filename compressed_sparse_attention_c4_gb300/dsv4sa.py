@@ -377,6 +377,7 @@ def dsv4sa_cache_write(pool: PoolDesc, page_table, row_seq, row_entry, rows, str
     want = HEAD_DIM if pool.kind in (POOL_KV, POOL_KV_FP4) else 128
     if rows.dim() != 2 or rows.shape[1] != want:
         raise ValueError(f"rows must be [n, {want}]")
+    _on_current_device(rows, "rows")
     n = rows.shape[0]
     _check("dsv4sa_cache_write", lib().dsv4sa_cache_write(
         ctypes.byref(pool), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
