@@ -162,9 +162,13 @@ def _check(fn, status):
         raise DSV4SAError(fn, status)
 
 
+# a small call is bound by the host: names of this module instead of attributes of torch
+_Tensor, _int32, _bf16 = torch.Tensor, torch.int32, torch.bfloat16
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None):
     """The address of a contiguous CUDA tensor (of that dtype), or an error."""
-    if type(t) is torch.Tensor and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+    if type(t) is _Tensor and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -375,14 +379,15 @@ def dsv4sa_window_indices(pos, window: int, ring: int, idx_w, stream=None):
 def dsv4sa_cache_write(pool: PoolDesc, page_table, row_seq, row_entry, rows, stream=None):
     """Quantise BF16 rows [n, 512] (KV and KV_FP4 pools) or [n, 128] (indexer-key pools) into the pool."""
     want = HEAD_DIM if pool.kind in (POOL_KV, POOL_KV_FP4) else 128
-    if rows.dim() != 2 or rows.shape[1] != want:
+    shape = rows.shape
+    if len(shape) != 2 or shape[1] != want:
         raise ValueError(f"rows must be [n, {want}]")
     _on_current_device(rows, "rows")
-    n = rows.shape[0]
-    _check("dsv4sa_cache_write", lib().dsv4sa_cache_write(
-        ctypes.byref(pool), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
-        _dev(row_seq, "row_seq", torch.int32), _dev(row_entry, "row_entry", torch.int32),
-        _dev(rows, "rows", torch.bfloat16), n, _stream(stream)))
+    st = lib().dsv4sa_cache_write(
+        ctypes.byref(pool), _dev(page_table, "page_table", _int32), page_table.shape[-1], _dev(row_seq, "row_seq", _int32),
+        _dev(row_entry, "row_entry", _int32), _dev(rows, "rows", _bf16), shape[0], _stream(stream))
+    if st:
+        raise DSV4SAError("dsv4sa_cache_write", st)
 
 
 def dsv4sa_cache_write_rotated(pool: PoolDesc, page_table, row_seq, row_entry, rows, stream=None):
@@ -400,12 +405,13 @@ def dsv4sa_cache_read(pool: PoolDesc, page_table, row_seq, row_entry, rows, stre
     """Rows of a KV or KV_FP4 pool into BF16 rows [n, 512]: the values the attention reads."""
     n = row_entry.shape[0]
     _on_current_device(rows, "rows")
-    if rows.dim() != 2 or rows.shape[1] != HEAD_DIM or rows.shape[0] != n or row_seq.shape[0] != n:
+    if rows.shape != (n, HEAD_DIM) or row_seq.shape[0] != n:
         raise ValueError("rows must be [n, 512] for n entries")
-    _check("dsv4sa_cache_read", lib().dsv4sa_cache_read(
-        ctypes.byref(pool), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
-        _dev(row_seq, "row_seq", torch.int32), _dev(row_entry, "row_entry", torch.int32),
-        _dev(rows, "rows", torch.bfloat16), n, _stream(stream)))
+    st = lib().dsv4sa_cache_read(
+        ctypes.byref(pool), _dev(page_table, "page_table", _int32), page_table.shape[-1], _dev(row_seq, "row_seq", _int32),
+        _dev(row_entry, "row_entry", _int32), _dev(rows, "rows", _bf16), n, _stream(stream))
+    if st:
+        raise DSV4SAError("dsv4sa_cache_read", st)
 
 
 # ---------------------------------------------------------------- pages of a cache
@@ -449,8 +455,9 @@ def dsv4sa_pages_copy(pools, src_page, dst_page, stream=None):
 def dsv4sa_cache_release(cache: CacheDesc, row, stream=None):
     """Release rows (int32 [n]) of the page table: entries -1, their pages' counts down by one."""
     _on_current_device(row, "row")
-    _check("dsv4sa_cache_release", lib().dsv4sa_cache_release(
-        ctypes.byref(cache), _dev(row, "row", torch.int32), row.numel(), _stream(stream)))
+    st = lib().dsv4sa_cache_release(ctypes.byref(cache), _dev(row, "row", _int32), row.numel(), _stream(stream))
+    if st:
+        raise DSV4SAError("dsv4sa_cache_release", st)
 
 
 def dsv4sa_cache_fork(cache: CacheDesc, src_row, dst_row, length, new_page, stream=None):
@@ -460,9 +467,11 @@ def dsv4sa_cache_fork(cache: CacheDesc, src_row, dst_row, length, new_page, stre
     if dst_row.numel() != n or length.numel() != n or new_page.numel() != n:
         raise ValueError("src_row, dst_row, length and new_page differ in length")
     _on_current_device(src_row, "src_row")
-    _check("dsv4sa_cache_fork", lib().dsv4sa_cache_fork(
-        ctypes.byref(cache), _dev(src_row, "src_row", torch.int32), _dev(dst_row, "dst_row", torch.int32),
-        _dev(length, "length", torch.int32), n, _dev(new_page, "new_page", torch.int32), _stream(stream)))
+    st = lib().dsv4sa_cache_fork(
+        ctypes.byref(cache), _dev(src_row, "src_row", _int32), _dev(dst_row, "dst_row", _int32),
+        _dev(length, "length", _int32), n, _dev(new_page, "new_page", _int32), _stream(stream))
+    if st:
+        raise DSV4SAError("dsv4sa_cache_fork", st)
 
 
 def dsv4sa_cache_compact(src: CacheDesc, dst: CacheDesc, new_id, n_used, stream=None):
@@ -478,15 +487,17 @@ def dsv4sa_cache_compact(src: CacheDesc, dst: CacheDesc, new_id, n_used, stream=
 
 # ---------------------------------------------------------------- norm
 
-def _bf16_rows(t: torch.Tensor, name: str, n: int, dim: int):
+def _bf16_rows(t: torch.Tensor, name: str, shape):
     """A BF16 CUDA tensor [n, dim] whose rows may be strided -> (pointer, row stride)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _bf16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.shape != (n, dim) or (dim > 1 and t.stride(1) != 1):
+    n, dim = shape
+    row, col = t.stride() if t.shape == shape else (0, 0)
+    if col != 1 and dim > 1:
         raise ValueError(f"{name} must be [{n}, {dim}] with consecutive values in a row")
-    return t.data_ptr(), (t.stride(0) if n > 1 else dim)
+    return t.data_ptr(), (row if n > 1 else dim)
 
 
 def dsv4sa_rmsnorm_quant(x, norm_w, codes=None, scale=None, group: int = 128, residual=None, residual_out=None, y=None,
@@ -494,23 +505,34 @@ def dsv4sa_rmsnorm_quant(x, norm_w, codes=None, scale=None, group: int = 128, re
     """RMSNorm of BF16 rows x [n, dim] (+ residual) with fp32 weights [dim]: E4M3 codes
     uint8 [n, dim] with fp32 scales [n, dim / group], the sum x + residual and
     the norm's output as BF16 [n, dim], each where a tensor is given (see dsv4sa.h)."""
-    n, dim = x.shape
+    shape = x.shape
+    n, dim = shape
     _on_current_device(x, "x")
     if norm_w.shape != (dim,):
         raise ValueError("norm_w must be [dim]")
-    xp, xs = _bf16_rows(x, "x", n, dim)
-    rp, rs = _bf16_rows(residual, "residual", n, dim) if residual is not None else (None, 0)
-    for t, name, shape in ((residual_out, "residual_out", (n, dim)), (y, "y", (n, dim)), (codes, "codes", (n, dim))):
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{name} must be [n, dim]")
-    if scale is not None and (group < 1 or scale.shape != (n, dim // group)):
-        raise ValueError("scale must be [n, dim / group]")
-    _check("dsv4sa_rmsnorm_quant", lib().dsv4sa_rmsnorm_quant(
-        xp, xs, rp, rs, _dev(norm_w, "norm_w", torch.float32), float(eps), n, dim, group,
-        _dev(residual_out, "residual_out", torch.bfloat16) if residual_out is not None else None,
-        _dev(y, "y", torch.bfloat16) if y is not None else None,
-        _dev(codes, "codes", torch.uint8) if codes is not None else None,
-        _dev(scale, "scale", torch.float32) if scale is not None else None, _stream(stream)))
+    xp, xs = _bf16_rows(x, "x", shape)
+    rp, rs = _bf16_rows(residual, "residual", shape) if residual is not None else (None, 0)
+    op = yp = cp = sp = None
+    if residual_out is not None:
+        if residual_out.shape != shape:
+            raise ValueError("residual_out must be [n, dim]")
+        op = _dev(residual_out, "residual_out", _bf16)
+    if y is not None:
+        if y.shape != shape:
+            raise ValueError("y must be [n, dim]")
+        yp = _dev(y, "y", _bf16)
+    if codes is not None:
+        if codes.shape != shape:
+            raise ValueError("codes must be [n, dim]")
+        cp = _dev(codes, "codes", torch.uint8)
+    if scale is not None:
+        if group < 1 or scale.shape != (n, dim // group):
+            raise ValueError("scale must be [n, dim / group]")
+        sp = _dev(scale, "scale", torch.float32)
+    st = lib().dsv4sa_rmsnorm_quant(xp, xs, rp, rs, _dev(norm_w, "norm_w", torch.float32), eps, n, dim, group, op, yp, cp, sp,
+                                    _stream(stream))
+    if st:
+        raise DSV4SAError("dsv4sa_rmsnorm_quant", st)
 
 
 def dsv4sa_compress_windows(kv, score, first_tok, prev_tok, position, ratio: int, overlap: bool, ape, norm_w,
