@@ -8,7 +8,7 @@
 //
 // Everything here moves bytes: the bound is HBM for whole pages (compacting 29490 pages of
 // 27904 bytes takes 274 us, 244 at the measured copy bandwidth) and latency for a few table
-// rows (four forks of one sequence, released before, 8.2 us in three kernels; 256 forks of
+// rows (four forks of one sequence, released before, 7.8 us in two kernels; 256 forks of
 // 64 sequences 13.6, their bytes 2).  Counts are 32-bit integers changed by atomic additions,
 // whose order does not change the result; page ids are handed out by scans in
 // id order, so a call gives the same ids every time.
@@ -199,11 +199,9 @@ constexpr int kAllocChunk = 8 * kAllocThreads;
 // be the smaller the earlier, put into the row's first entry by an atomic
 // minimum.  A parent that is a row of this same call is thereby empty, too, and
 // refused.
-__global__ void __launch_bounds__(kAllocThreads) cache_fork_alloc_kernel(const CacheParams p, const ForkParams f) {
+__device__ __forceinline__ void fork_alloc(const CacheParams& p, const ForkParams& f) {   // by a CTA of kAllocThreads
   __shared__ int buf[32];
   __shared__ int32_t free_ids[kAllocChunk];
-  griddep_launch();
-  griddep_wait();
   const int tid = static_cast<int>(threadIdx.x);
   int avail = 0, pos = 0, next = 0;            // ids listed, ids given out, next page to look at
   uint32_t ready = free_bits(p, tid * 8);      // the first chunk's free pages, while the forks are looked at
@@ -265,12 +263,11 @@ __global__ void __launch_bounds__(kAllocThreads) cache_fork_alloc_kernel(const C
   }
 }
 
-// Fork i by `pieces` CTAs: the row of dst is the parent's full pages (their
-// counts go up) and the new page, whose first len % 64 slots are copied.
-__global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(const CacheParams p, const ForkParams f, int pieces) {
-  griddep_launch();
-  griddep_wait();
-  const int i = blockIdx.x / pieces, piece = blockIdx.x % pieces, tid = static_cast<int>(threadIdx.x);
+// Piece `piece` of `pieces` of fork i, by a CTA of kThreads: the row of dst is the parent's
+// full pages (their counts go up) and the new page, whose first len % 64 slots are copied.
+template <int kThreads>
+__device__ __forceinline__ void fork_rows(const CacheParams& p, const ForkParams& f, int i, int piece, int pieces) {
+  const int tid = static_cast<int>(threadIdx.x);
   const int32_t d = __ldg(f.dst + i), s = __ldg(f.src + i), len = __ldg(f.len + i), page = f.new_page[i];
   if (page == kUntouched) return;              // flagged by the first kernel
   int32_t* drow = p.pt + static_cast<int64_t>(d) * p.pt_stride;
@@ -302,7 +299,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(const CachePar
 #pragma unroll
     for (int i = 0; i < kForkBatch; ++i) {
       bytes[i] = 0;
-      int at = u + i * kCopyThreads;
+      int at = u + i * kThreads;
       if (at >= u_end) continue;
       for (int k = 0; k < p.n_pools && bytes[i] == 0; ++k) {
 #pragma unroll
@@ -320,7 +317,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(const CachePar
       }
     }
     if (!table_done) {
-      for (int j = piece * kCopyThreads + tid; j < p.pt_stride; j += pieces * kCopyThreads) {
+      for (int j = piece * kThreads + tid; j < p.pt_stride; j += pieces * kThreads) {
         int32_t e = -1;
         if (j < full) {
           e = srow[j];
@@ -348,8 +345,31 @@ __global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(const CachePar
           if (4 * x < bytes[i]) reinterpret_cast<uint32_t*>(to[i])[x] = w[x];
       }
     }
-    u += kForkBatch * kCopyThreads;
+    u += kForkBatch * kThreads;
   } while (u - tid < u_end);               // the same for all threads
+}
+
+__global__ void __launch_bounds__(kAllocThreads) cache_fork_alloc_kernel(const CacheParams p, const ForkParams f) {
+  griddep_launch();
+  griddep_wait();
+  fork_alloc(p, f);
+}
+__global__ void __launch_bounds__(kCopyThreads) cache_fork_kernel(const CacheParams p, const ForkParams f, int pieces) {
+  griddep_launch();
+  griddep_wait();
+  fork_rows<kCopyThreads>(p, f, blockIdx.x / pieces, blockIdx.x % pieces, pieces);
+}
+// Both in one kernel for up to eight forks, a cluster of CTAs: the first hands the pages out,
+// then all of them copy.  The device takes as long (8 forks 7.9 us, 8.2 in two kernels), the
+// host 2 us less; 16 forks took 10.5 us against 8.4.
+constexpr int kForkCtas = 8;
+__global__ void __launch_bounds__(kAllocThreads) cache_fork_few_kernel(const CacheParams p, const ForkParams f, int pieces) {
+  griddep_launch();
+  griddep_wait();
+  const int r = static_cast<int>(cluster_ctarank());
+  if (r == 0) fork_alloc(p, f);
+  cluster_sync();                              // what the first CTA wrote is seen by the others
+  for (int k = r; k < f.n * pieces; k += kForkCtas) fork_rows<kAllocThreads>(p, f, k / pieces, k % pieces, pieces);
 }
 
 // ---------------------------------------------------------------- compact
@@ -581,6 +601,11 @@ int launch_cache_fork(const dsv4sa_cache_desc* c, const int32_t* src, const int3
   const ForkParams f{src, dst, len, new_page, n};
   int sms = 0;
   if (const int rc = sm_count(&sms); rc != DSV4SA_OK) return rc;
+  if (n <= kForkCtas) {
+    int few = 1;                               // pieces of a fork, so that every CTA has one
+    while (few < kForkCtas && n * few < kForkCtas) few *= 2;
+    return done(launch_cluster_pdl(cache_fork_few_kernel, dim3(kForkCtas), dim3(kAllocThreads), 0, kForkCtas, stream, p, f, few));
+  }
   if (launch_pdl(cache_fork_alloc_kernel, dim3(1), dim3(kAllocThreads), 0, stream, p, f) != cudaSuccess)
     return DSV4SA_ERR_CUDA;
   const int pieces = copy_pieces(n, sms);
