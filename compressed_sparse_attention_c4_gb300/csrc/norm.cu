@@ -10,14 +10,14 @@
 // 512 threads for 16384), each holding kUnits 16-byte units, unit i of a thread
 // being unit i kTpr + (its index) of the row, so loads and stores are coalesced
 // and a block's 8 or 16 units are neighbouring lanes of one warp: its absmax is
-// three or four shuffles.  The grid is resident and walks the rows; the weights
+// three or four shuffles.  A CTA walks several rows; the weights
 // of a thread's columns are loaded once, and the next row's units before the
 // current row is reduced, so reads stay in flight.  Rows of up to 512 are bound by
 // their instructions as much as by HBM: two units a thread instead of one halve the
 // shuffles and addresses a value, packed fp32 the arithmetic, and 64 registers leave
 // 32 warps a multiprocessor (262144 rows of 128: 41 us before these, 20.4 with them,
 // 15.2 at the measured copy bandwidth; several rows a thread at once took 23 to 31).  Long
-// rows are bound by HBM: 8191 rows of 7168 with residual, sum and BF16 output 84.8 us,
+// rows are bound by HBM: 8191 rows of 7168 with residual, sum and BF16 output 81.1 us,
 // 78.3 at the copy's bandwidth.
 #include <atomic>
 
@@ -211,7 +211,11 @@ int launch_norm_r(const NormParams& p, cudaStream_t stream) {
     cached.store(resident, std::memory_order_relaxed);
   }
   const int64_t want = (static_cast<int64_t>(p.n) + kRowsPerCta - 1) / kRowsPerCta;
-  const int64_t full = static_cast<int64_t>(sms) * resident;
+  // long rows: more CTAs than run at once, a few rows each, so that none is left with more
+  // to do than the others (8191 rows of 7168: 81.1 us with eight times the resident ones,
+  // 84.8 with these alone); short rows keep their weights and the next row's loads longer
+  // (262144 rows of 128: 20.4 us, 23.5 with eight times)
+  const int64_t full = static_cast<int64_t>(sms) * resident * (kTpr > 32 ? 8 : 1);
   return launch_pdl(rmsnorm_quant_kernel<kTpr, kUnits, kRes>,
                     dim3(static_cast<unsigned>(want < full ? want : full)), dim3(kThreads), 0, stream, p) == cudaSuccess
              ? DSV4SA_OK

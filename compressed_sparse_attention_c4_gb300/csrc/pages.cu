@@ -7,7 +7,7 @@
 // the device, so a beam step or a clean-up costs the host no round trip.
 //
 // Everything here moves bytes: the bound is HBM for whole pages (compacting 29490 pages of
-// 27904 bytes takes 274 us, 244 at the measured copy bandwidth) and latency for a few table
+// 27904 bytes takes 244 us, the measured copy bandwidth) and latency for a few table
 // rows (four forks of one sequence, released before, 7.8 us in two kernels; 256 forks of
 // 64 sequences 13.6, their bytes 2).  Counts are 32-bit integers changed by atomic additions,
 // whose order does not change the result; page ids are handed out by scans in
@@ -42,7 +42,7 @@ struct CacheParams {
 
 // Copy `units` 16-byte units, up to eight loads in flight per thread (a page is five
 // to ten units a thread, so a loop of whole batches alone would run one at a time:
-// that took 370 us for the compaction of 49151 pages, this 274).
+// a compaction that took 370 us so took 294 with batches of eight).
 __device__ __forceinline__ void copy_units(uint4* dst, const uint4* src, int units, int tid, int threads) {
   for (int u0 = tid; u0 < units; u0 += 8 * threads) {
     uint4 v[8];
@@ -627,7 +627,10 @@ int launch_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* 
                   : launch_cluster_pdl(cache_plan_kernel, dim3(kPlanCtas), dim3(kAllocThreads), 0, kPlanCtas, stream, c)) !=
       cudaSuccess)
     return DSV4SA_ERR_CUDA;
-  const int64_t full = static_cast<int64_t>(sms) * 8;
+  // far more CTAs than run at once, a page or two each: those that run then differ in where
+  // they are, and none is left with more to do (29490 pages: 244 us; 8 CTAs an SM, all
+  // resident, 275, 32 an SM 251, one for every page 259)
+  const int64_t full = static_cast<int64_t>(sms) * 128;
   const int64_t want = c.src.num_pages;
   return done(launch_pdl(cache_move_kernel, dim3(static_cast<unsigned>(want < full ? want : full)), dim3(kCopyThreads),
                          0, stream, c));
