@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(kThreads) fp4_key_write_kernel(const WriterPar
 // exponent as one byte (the last two bytes of the scale row are padding, never
 // written).  A block that holds an infinity or a NaN gets the exponent byte 255
 // (E8M0 NaN) and codes 0, so it reads back as NaN.  kRowsW rows per warp are in
-// flight: the row loads are independent of the entry -> page look-ups (65529 rows 15.0 us,
-// 13.5 being the bytes at the measured copy bandwidth; 15.4 with one row, 14.8 with four,
+// flight: the row loads are independent of the entry -> page look-ups (65529 rows 14.8 us,
+// 13.5 being the bytes at the measured copy bandwidth; 15.4 with one row, 14.6 with four,
 // but 32 rows take 1.6, 2.1 and 2.5 us).  The integer pipe is nearly as busy (73%).
 constexpr int kRowsW = 2;
 
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterPara
 // bits; past its range an infinity, as a product of the two rounds to).  A warp per
 // row, lane c writing the 16-byte units c and 32 + c of it as in the writer; kRowsR
 // rows per warp in flight.  One: a row is three dependent loads (entry, page id, row), but
-// many warps hide them as well as many rows a warp do (65529 FP4 rows 16.8 us with 1 row,
+// many warps hide them as well as many rows a warp do (65529 FP4 rows, each warp once: 16.8 us with 1 row,
 // 17.5 with 2, 16.9 with 4, 20.1 with 8) and few rows are read sooner (32 rows 1.7 us, 2.1,
 // 2.7, 3.5).
 constexpr int kRowsR = 1;
@@ -466,14 +466,16 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReaderParams
   }
 }
 
-// CTAs of `rows_per_block` rows over n rows; only past 64 a multiprocessor do they
-// take more than one batch each (short CTAs even out better than a resident grid).
+// CTAs of `rows_per_block` rows over n rows, at most 20 a multiprocessor (six run at once):
+// enough that none is left with more to do, few enough that starting them does not show
+// (65529 FP4 rows written and read: 30.4 us; 64 a multiprocessor, one batch each, 31.8,
+// 12 31.4, 8 32.1).
 template <class P>
 cudaError_t launch_rows(void (*kernel)(P), const P& p, int64_t n, int64_t rows_per_block, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cudaErrorUnknown;
-  const int64_t want = (n + rows_per_block - 1) / rows_per_block, cap = static_cast<int64_t>(sms) * 64;
+  const int64_t want = (n + rows_per_block - 1) / rows_per_block, cap = static_cast<int64_t>(sms) * 20;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(kThreads), 0, stream, p);
 }
 
