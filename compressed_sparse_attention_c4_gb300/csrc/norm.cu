@@ -16,8 +16,9 @@
 // their instructions as much as by HBM: two units a thread instead of one halve the
 // shuffles and addresses a value, packed fp32 the arithmetic, and 64 registers leave
 // 32 warps a multiprocessor (262144 rows of 128: 41 us before these, 20.4 with them,
-// 15.2 at the measured copy bandwidth; several rows a thread at once took 23 to 31).  Long
-// rows are bound by HBM: 8191 rows of 7168 with residual, sum and BF16 output 81.1 us,
+// 18.3 with 32-bit rows and the hardware's reciprocals, 15.2 at the measured copy bandwidth;
+// several rows a thread at once took 23 to 31).  Long
+// rows are bound by HBM: 8191 rows of 7168 with residual, sum and BF16 output 80.9 us,
 // 78.3 at the copy's bandwidth.
 #include <atomic>
 
@@ -46,6 +47,18 @@ struct NormParams {
   float inv_dim;
   float eps;
 };
+
+// 1 / x and 1 / sqrt(x) by the hardware (relative 2^-22 or so; x normal).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 __device__ __forceinline__ void unpack8(const uint4 v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -83,21 +96,21 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256, kTpr <= 32 && kUnits 
     w[i][2] = make_float2(b.x, b.y), w[i][3] = make_float2(b.z, b.w);
   }
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRowsPerCta;
-  auto load = [&](int64_t row, uint4 (&xv)[kUnits], uint4 (&rv)[kUnits]) {
-    const bool live = row < p.n;
+  const uint32_t n = static_cast<uint32_t>(p.n), step = gridDim.x * kRowsPerCta;   // row + step < 2^32
+  auto load = [&](uint32_t row, uint4 (&xv)[kUnits], uint4 (&rv)[kUnits]) {
+    const bool live = row < n;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int u = i * kTpr + c;
       const bool in = live && u < p.units;
-      xv[i] = in ? __ldcs(p.x + row * p.x_stride + u) : zero;
-      if constexpr (kRes) rv[i] = in ? __ldcs(p.r + row * p.r_stride + u) : zero;
+      xv[i] = in ? __ldcs(p.x + static_cast<int64_t>(row) * p.x_stride + u) : zero;
+      if constexpr (kRes) rv[i] = in ? __ldcs(p.r + static_cast<int64_t>(row) * p.r_stride + u) : zero;
     }
   };
   int buf = 0;
   // one row, from the units in xv and rv; `next` loads the row after it in between
-  auto process = [&](int64_t row, uint4 (&xv)[kUnits], uint4 (&rv)[kUnits], int64_t next) {
-    const bool live = row < p.n;
+  auto process = [&](uint32_t row, uint4 (&xv)[kUnits], uint4 (&rv)[kUnits], uint32_t next) {
+    const bool live = row < n;
     float2 s[kUnits][4];
     float2 sq2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -126,10 +139,10 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256, kTpr <= 32 && kUnits 
     }
     // 1 / sqrt by the hardware's estimate and one Newton step (relative 2^-23)
     const float ms = fmaf(sq, p.inv_dim, p.eps);
-    const float r0 = rsqrtf(ms);
+    const float r0 = rsqrt_approx(ms);
     const float rstd = ms > 0.f && ms < INFINITY ? r0 * fmaf(-0.5f * ms * r0, r0, 1.5f) : r0;
     const float2 rstd2 = make_float2(rstd, rstd);
-    const int64_t out0 = row * p.units + c;                  // this thread's first unit of the outputs
+    const int64_t out0 = static_cast<int64_t>(row) * p.units + c;                  // this thread's first unit of the outputs
     float top[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -171,7 +184,7 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256, kTpr <= 32 && kUnits 
         // norm, weight, scale and quotient in turn take five.  The quotient is the
         // hardware's estimate with its residual added; the conversion saturates.
         // (Of amax / 256: above 2^126 the hardware's quotient would be 0.)
-        const float r = __fdividef(0x1p-8f, amax * 0x1p-8f), k0 = 448.f * r;
+        const float r = rcp_approx(amax * 0x1p-8f) * 0x1p-8f, k0 = 448.f * r;
         const float inv = amax * rstd > kAmaxFloor ? fmaf(fmaf(-amax, k0, 448.f), r, k0) : rstd * (448.f / kAmaxFloor);
         const float2 inv2 = make_float2(inv, inv);
         uint32_t q[2];
@@ -183,16 +196,16 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256, kTpr <= 32 && kUnits 
         }
         if (in) {
           __stcs(p.codes + out0 + i * kTpr, make_uint2(q[0], q[1]));
-          if ((u & (p.group_units - 1)) == 0) p.scale[(row * p.units + u) >> (p.group_units == 16 ? 4 : 3)] = scale;
+          if ((u & (p.group_units - 1)) == 0) p.scale[(out0 + i * kTpr) >> (p.group_units == 16 ? 4 : 3)] = scale;
         }
       }
     }
   };
   // the first row of the CTA decides: every thread takes part in shuffles and barriers
-  int64_t first = static_cast<int64_t>(blockIdx.x) * kRowsPerCta;
+  uint32_t first = blockIdx.x * kRowsPerCta;
   uint4 xv[kUnits], rv[kUnits];
   load(first + sub, xv, rv);
-  for (; first < p.n; first += step) process(first + sub, xv, rv, first + sub + step);
+  for (; first < n; first += step) process(first + sub, xv, rv, first + sub + step);
 }
 
 template <int kTpr, int kUnits, bool kRes>
@@ -214,7 +227,7 @@ int launch_norm_r(const NormParams& p, cudaStream_t stream) {
   // long rows: more CTAs than run at once, a few rows each, so that none is left with more
   // to do than the others (8191 rows of 7168: 81.1 us with eight times the resident ones,
   // 84.8 with these alone); short rows keep their weights and the next row's loads longer
-  // (262144 rows of 128: 20.4 us, 23.5 with eight times)
+  // (262144 rows of 128: 20.4 us with the resident ones, 23.5 with eight times)
   const int64_t full = static_cast<int64_t>(sms) * resident * (kTpr > 32 ? 8 : 1);
   return launch_pdl(rmsnorm_quant_kernel<kTpr, kUnits, kRes>,
                     dim3(static_cast<unsigned>(want < full ? want : full)), dim3(kThreads), 0, stream, p) == cudaSuccess
