@@ -35,7 +35,7 @@
 // K = 16 reads 6 KB and takes 48 cycles, the 128 bytes a clock of shared memory
 // (measured), so while MMAs run other accesses hardly proceed, and the phases of a
 // chunk (about 3000 cycles of MMAs, 1000 of stores, the widening's 7168 words of eight codes)
-// follow one another: 4096 queries of 640 rows take 594 us, 578 TFLOP/s.  The tile is
+// follow one another: 4096 queries of 640 rows take 580 us, 592 TFLOP/s.  The tile is
 // handed over in two halves of its dims: as a whole that call took 687 us, by quarters
 // 629, by halves 617 then (a wait drains the tensor pipe).  Two tiles of 64 rows in turn, a
 // group of gather warps for each, took 726 against 610: each step from one kind of warp to
@@ -69,11 +69,12 @@ constexpr int kHalf = 4 * kKvBlock;      // bytes of a half of the tile: 128 row
 constexpr int kLastChunk = 256;          // meta: rows of the chunk (<= 128), and this for an item's last
 // Registers per thread (setmaxnreg): the launch gives 896 x 72 = 64512, the three
 // kinds of warpgroup then hold 256 x 96 + 512 x 64 + 128 x 56 = 64512, or, for 64 heads,
-// whose softmax threads have 32 scores and sums each, 256 x 112 + 512 x 56 + 128 x 56 (4096
-// queries of 64 heads 594 us, 607 with the first shares; 128 of 8 heads 33.7 us, 31.6).
+// whose softmax threads have 32 scores and sums each, 256 x 120 + 512 x 56 + 128 x 40 (4096
+// queries of 64 heads 580 us, with 112, 56 and 56 584, with the first shares 597; 128 of 8
+// heads 31.2 us, with 112, 56 and 56 33.7).
 template <int HN>
 struct Regs4 {
-  static constexpr int kCompute = HN == 64 ? 112 : 96, kGather = HN == 64 ? 56 : 64, kMma = 56;
+  static constexpr int kCompute = HN == 64 ? 120 : 96, kGather = HN == 64 ? 56 : 64, kMma = HN == 64 ? 40 : 56;
   static_assert(kComputeThreads * kCompute + kGatherThreads * kGather + 128 * kMma <= kThreads4 * 72,
                 "the register shares fit in the launch's");
 };
@@ -84,7 +85,7 @@ constexpr uint32_t kBarGather4 = 2;
 template <int HN>
 struct Smem4 {
   // Halves of tiles.  With 16 heads a third one fits: the next chunk's first half is
-  // widened before the current one's PV (128 queries of 8 heads, up to 1152 rows: 31.6 us,
+  // widened before the current one's PV (128 queries of 8 heads, up to 1152 rows: 31.2 us,
   // 32.5 with two).
   static constexpr int kSlots = HN == 16 ? 3 : 2;
   static constexpr int kStage = HN == 16 ? 8 : 16;       // heads of an output step
@@ -373,6 +374,33 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         count += all;
         cursor = end;
       };
+      // ---- a chunk's rows in registers: the four threads of a row take its 16-byte code pieces
+      // 4 b + piece (a scale block each) of the first three quarters, 8 bytes of codes and 32
+      // of rope values of the last; rows past the chunk's are zero
+      uint4 code[3], rope[2], scl;
+      uint2 code3;
+      const uint8_t* page = nullptr;
+      int rs = -1;                              // the row's slot in its page, -1: none
+      auto take = [&](int n) {                  // the next n rows of the ring
+        const uint64_t rp = row < n ? ring[(head + row) & (kRing - 1)] : 0;
+        page = reinterpret_cast<const uint8_t*>(rp & ~uint64_t(63));
+        rs = row < n ? static_cast<int>(rp & 63) : -1;
+        head += n;
+        count -= n;
+      };
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      auto load_scales = [&]() { return rs >= 0 ? __ldg(reinterpret_cast<const uint4*>(page + kFp4ScaleOff + rs * 16)) : zero; };
+      auto load_quarter = [&](int b) {
+        const uint8_t* cp = page + rs * 224;
+        if (b < 3) {
+          code[b] = rs >= 0 ? __ldg(reinterpret_cast<const uint4*>(cp) + 4 * b + piece) : zero;
+        } else {
+          const uint4* rpp = reinterpret_cast<const uint4*>(page + kFp4RopeOff + rs * 128) + 2 * piece;
+          code3 = rs >= 0 ? __ldg(reinterpret_cast<const uint2*>(cp + 192) + piece) : make_uint2(0u, 0u);
+          rope[0] = rs >= 0 ? __ldg(rpp) : zero;
+          rope[1] = rs >= 0 ? __ldg(rpp + 1) : zero;
+        }
+      };
       while (true) {
         // ---- enough rows for a chunk, or the end of the lists
         while (count < kRows && cursor < total) {
@@ -385,32 +413,14 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         }
         const int n = min(count, kRows);
         if (n == 0) break;
-        // ---- load: the four threads of a row take its 16-byte code pieces 4 b + piece
-        // (a scale block each) of the first three quarters, 8 bytes of codes and 32 of
-        // rope values of the last; rows past n are zero
-        uint4 code[3], rope[2], scl;
-        uint2 code3;
-        {
-          const bool in = row < n;
-          const uint64_t rp = in ? ring[(head + row) & (kRing - 1)] : 0;
-          const uint8_t* page = reinterpret_cast<const uint8_t*>(rp & ~uint64_t(63));
-          const int slot = static_cast<int>(rp & 63);
-          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          const uint8_t* cp = page + slot * 224;
-          const uint4* rpp = reinterpret_cast<const uint4*>(page + kFp4RopeOff + slot * 128) + 2 * piece;
-          scl = in ? __ldg(reinterpret_cast<const uint4*>(page + kFp4ScaleOff + slot * 16)) : zero;
+        take(n);
+        scl = load_scales();
 #pragma unroll
-          for (int b = 0; b < 3; ++b) code[b] = in ? __ldg(reinterpret_cast<const uint4*>(cp) + 4 * b + piece) : zero;
-          code3 = in ? __ldg(reinterpret_cast<const uint2*>(cp + 192) + piece) : make_uint2(0u, 0u);
-          rope[0] = in ? __ldg(rpp) : zero;
-          rope[1] = in ? __ldg(rpp + 1) : zero;
-        }
-        head += n;
-        count -= n;
-        // no row of the item is left to come: the softmax may replace Q once this chunk's S is complete
-        const bool last = count == 0 && cursor >= total;
+        for (int b = 0; b < 4; ++b) load_quarter(b);
         // ---- look ahead while the loads are in flight
         if (count < kRows && cursor < total && (waited || cursor < cw)) locate();
+        // no row of the item is left to come: the softmax may replace Q once this chunk's S is complete
+        const bool last = count == 0 && cursor >= total;
         // ---- into the tile, half by half, when the half that was there has been read by its PV
         const uint32_t sw[4] = {scl.x, scl.y, scl.z, scl.w};
 #pragma unroll
