@@ -35,7 +35,7 @@
 // K = 16 reads 6 KB and takes 48 cycles, the 128 bytes a clock of shared memory
 // (measured), so while MMAs run other accesses hardly proceed, and the phases of a
 // chunk (about 3000 cycles of MMAs, 1000 of stores, the widening's 7168 words of eight codes)
-// follow one another: 4096 queries of 640 rows take 580 us, 592 TFLOP/s.  The tile is
+// follow one another: 4096 queries of 640 rows take 578 us, 594 TFLOP/s.  The tile is
 // handed over in two halves of its dims: as a whole that call took 687 us, by quarters
 // 629, by halves 617 then (a wait drains the tensor pipe).  Two tiles of 64 rows in turn, a
 // group of gather warps for each, took 726 against 610: each step from one kind of warp to
@@ -422,7 +422,9 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         // no row of the item is left to come: the softmax may replace Q once this chunk's S is complete
         const bool last = count == 0 && cursor >= total;
         // ---- into the tile, half by half, when the half that was there has been read by its PV
-        const uint32_t sw[4] = {scl.x, scl.y, scl.z, scl.w};
+        // the four bytes of the scales that this thread's pieces need
+        const uint32_t sb = __byte_perm(__byte_perm(scl.x, scl.y, piece * 0x11 + 0x40),
+                                        __byte_perm(scl.z, scl.w, piece + ((piece >> 1) + 4) * 0x10), 0x5410);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           if ((b & 1) == 0 && round > 0 && ok) ok = warp_wait(bar_free + slot, (round - 1) & 1);
@@ -430,8 +432,9 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
           if (b < 3) {
             // 32 values: units 4 (piece & 1) + x of column block 2 b + (piece >> 1).  The
             // upper two pieces take x in the order 2, 3, 0, 1, so that the eight lanes of
-            // two rows hit eight different bank groups.
-            const BlockScale bs = block_scale((sw[b] >> (8 * piece)) & 0xFFu);
+            // two rows hit eight different bank groups.  (Eight lanes with eight rows of the
+            // same piece would, too, but load eight half-used sectors: 644 us for 578.)
+            const BlockScale bs = block_scale((sb >> (8 * b)) & 0xFFu);
             uint8_t* blk = half + (2 * (b & 1) + (piece >> 1)) * kKvBlock;
             const uint32_t c4[4] = {code[b].x, code[b].y, code[b].z, code[b].w};
 #pragma unroll
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
               *reinterpret_cast<uint4*>(blk + sw128_offset(row, static_cast<uint32_t>(4 * (piece & 1)) + x)) = v;
             }
           } else {
-            const BlockScale bs = block_scale((sw[3] >> (8 * (piece >> 1))) & 0xFFu);
+            const BlockScale bs = block_scale(sb >> 24);
             const uint32_t u = static_cast<uint32_t>(2 * piece);
             uint4 v0 = widen8_split(code3.x, bs.first), v1 = widen8_split(code3.y, bs.first);
             if (bs.more) {
