@@ -84,10 +84,10 @@ constexpr uint32_t kBarGather4 = 2;
 
 template <int HN>
 struct Smem4 {
-  // Halves of tiles.  With 16 heads a third one fits: the next chunk's first half is
-  // widened before the current one's PV (128 queries of 8 heads, up to 1152 rows: 31.2 us,
-  // 32.5 with two).
-  static constexpr int kSlots = HN == 16 ? 3 : 2;
+  // Halves of tiles.  (With 16 heads a third one fits, so that the next chunk is widened
+  // while this one is scored: 128 queries of 8 heads, up to 1152 rows, 31.2 us for 32.1 in
+  // a graph of such calls, but 37.2 for 33.3 launched one by one.)
+  static constexpr int kSlots = 2;
   static constexpr int kStage = HN == 16 ? 8 : 16;       // heads of an output step
   static constexpr int kKv = 0;
   static constexpr int kQ = kSlots * kHalf;              // 8 column blocks x HN rows x 128 B
