@@ -13,6 +13,7 @@ ABI for tests and the benchmark.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -204,6 +205,25 @@ def _stream(stream):
             return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+@contextlib.contextmanager
+def _running_on(stream):
+    """Torch's work and the library's inside the block run on `stream` (a torch stream or a
+    handle; None: the current one), after what the current stream holds already; the
+    current stream then waits for it.  Tensors made inside belong to `stream`, so their
+    memory is not used again before its kernels have read them."""
+    if stream is None:
+        yield
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    caller = torch.cuda.current_stream()
+    s.wait_stream(caller)
+    try:
+        with torch.cuda.stream(s):
+            yield
+    finally:
+        caller.wait_stream(s)
 
 
 def _on_current_device(t: torch.Tensor, name: str):
@@ -768,17 +788,19 @@ def _arena_views(buf, layout):
 
 def requantize_kv_pool_fp4(pool: PoolDesc, device="cuda", stream=None):
     """A KV pool's rows, all of them, as a KV_FP4 pool of as many pages -> (device byte
-    tensor, PoolDesc): read back as BF16 and written again, 1024 pages at a time."""
+    tensor, PoolDesc): read back as BF16 and written again, 1024 pages at a time.  With a
+    stream the work runs there, after the current stream's and before what follows on it."""
     pages = int(pool.num_pages)
     buf = _alloc_pool(POOL_KV_FP4, pages, device)
     desc = dsv4sa_pool_desc_init(POOL_KV_FP4, buf, pages)
-    table = torch.arange(pages, dtype=torch.int32, device=device).view(1, pages)
-    for p0 in range(0, pages, 1024):
-        entry = torch.arange(p0 * PAGE, min(pages, p0 + 1024) * PAGE, dtype=torch.int32, device=device)
-        seq = torch.zeros_like(entry)
-        rows = torch.empty(entry.shape[0], HEAD_DIM, dtype=torch.bfloat16, device=device)
-        dsv4sa_cache_read(pool, table, seq, entry, rows, stream)
-        dsv4sa_cache_write(desc, table, seq, entry, rows, stream)
+    with _running_on(stream):
+        table = torch.arange(pages, dtype=torch.int32, device=device).view(1, pages)
+        for p0 in range(0, pages, 1024):
+            entry = torch.arange(p0 * PAGE, min(pages, p0 + 1024) * PAGE, dtype=torch.int32, device=device)
+            seq = torch.zeros_like(entry)
+            rows = torch.empty(entry.shape[0], HEAD_DIM, dtype=torch.bfloat16, device=device)
+            dsv4sa_cache_read(pool, table, seq, entry, rows)
+            dsv4sa_cache_write(desc, table, seq, entry, rows)
     return buf, desc
 
 
