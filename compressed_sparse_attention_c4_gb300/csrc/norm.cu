@@ -60,6 +60,16 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
   return y;
 }
 
+// 1 / sqrt(sq inv_dim + eps) where that mean is below 2^-100, infinite or NaN.  The estimate
+// takes a mean below the smallest normal number for zero, so it is formed 2^64 times as large.
+constexpr uint32_t kLowMean = 0x0D800000u;   // 2^-100
+__device__ __forceinline__ float rsqrt_of_rare_mean(float sq, float inv_dim, float eps) {
+  const bool low = fmaf(sq, inv_dim, eps) < 0x1p-100f;
+  const float up = low ? 0x1p64f : 1.f, down = low ? 0x1p32f : 1.f;
+  const float ms = fmaf(sq * up, inv_dim, eps * up), r0 = rsqrt_approx(ms);
+  return ms > 0.f && ms < INFINITY ? r0 * fmaf(-0.5f * ms * r0, r0, 1.5f) * down : r0;
+}
+
 __device__ __forceinline__ void unpack8(const uint4 v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -140,7 +150,8 @@ __global__ void __launch_bounds__(kTpr > 256 ? kTpr : 256, kTpr <= 32 && kUnits 
     // 1 / sqrt by the hardware's estimate and one Newton step (relative 2^-23)
     const float ms = fmaf(sq, p.inv_dim, p.eps);
     const float r0 = rsqrt_approx(ms);
-    const float rstd = ms > 0.f && ms < INFINITY ? r0 * fmaf(-0.5f * ms * r0, r0, 1.5f) : r0;
+    float rstd = r0 * fmaf(-0.5f * ms * r0, r0, 1.5f);
+    if (__float_as_uint(ms) - kLowMean >= 0x7F800000u - kLowMean) rstd = rsqrt_of_rare_mean(sq, p.inv_dim, p.eps);
     const float2 rstd2 = make_float2(rstd, rstd);
     const int64_t out0 = static_cast<int64_t>(row) * p.units + c;                  // this thread's first unit of the outputs
     float top[kUnits];

@@ -566,8 +566,11 @@ DSV4SA_API int dsv4sa_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_c
  * and per `group` consecutive values of y: amax = max(max |y|, 1e-4), scale =
  * amax * fp32(1/448), codes = E4M3 round-to-nearest-even of clamp(y / scale).
  * With group 64 and dim 128 the outputs are dsv4sa_indexer_logits's q_fp8 and
- * q_scale (n = T * Hi rows).  A row whose squares leave the fp32 range, or that
- * holds a NaN, has no defined codes.
+ * q_scale (n = T * Hi rows).  The sum is fp32, and so are the values times norm_w, which
+ * are formed before the division by the root: a row whose sum of squares passes the fp32
+ * range, whose squares fall below 2^-126 where eps does not outweigh them, or of which a
+ * value times its weight leaves the normal fp32 range, has no defined y and codes, nor has
+ * one that holds an infinity or a NaN, or only zeros with eps = 0.
  *   x, residual   bf16, rows x_stride / residual_stride values apart, 16-byte
  *                 aligned, strides multiples of 8; residual may be null (s = x)
  *   norm_w        device fp32 [dim], 16-byte aligned
