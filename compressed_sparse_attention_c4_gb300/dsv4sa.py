@@ -47,6 +47,7 @@ class DSV4SAError(RuntimeError):
 
 
 class PoolDesc(ctypes.Structure):
+    device = None   # of the tensor it was made from
     _fields_ = [("kind", ctypes.c_int32), ("page_size", ctypes.c_int32), ("nope_dim", ctypes.c_int32),
                 ("rope_dim", ctypes.c_int32), ("scale_group", ctypes.c_int32), ("n_scales", ctypes.c_int32),
                 ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("nope_off", ctypes.c_int64),
@@ -72,6 +73,7 @@ class AttnArgs(ctypes.Structure):
 
 
 class CacheDesc(ctypes.Structure):
+    device = None   # of its tensors
     _fields_ = [("pools", ctypes.POINTER(PoolDesc)), ("n_pools", ctypes.c_int32), ("rows", ctypes.c_int32),
                 ("pt_stride", ctypes.c_int32), ("reserved", ctypes.c_int32), ("page_table", ctypes.c_void_p),
                 ("use", ctypes.c_void_p)]
@@ -164,12 +166,31 @@ def _check(fn, status):
 
 
 # a small call is bound by the host: names of this module instead of attributes of torch
-_Tensor, _int32, _bf16 = torch.Tensor, torch.int32, torch.bfloat16
+_Tensor, _int32, _bf16, _f32, _u8 = torch.Tensor, torch.int32, torch.bfloat16, torch.float32, torch.uint8
 
 
-def _dev(t: torch.Tensor, name: str, dtype=None):
-    """The address of a contiguous CUDA tensor (of that dtype), or an error."""
-    if type(t) is _Tensor and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _here() -> int:
+    """The current device; -2 (no tensor's) on a host without one."""
+    try:
+        return _current_device()
+    except RuntimeError:
+        return -2
+
+
+def _refuse_device(name: str, device: int):
+    """The library launches on the current device: memory of another one is refused."""
+    raise ValueError(f"{name} is on cuda:{device}, the current device is cuda:{_current_device()}")
+
+
+def _dev(t: torch.Tensor, name: str, dtype=None, here=None):
+    """The address of a contiguous tensor (of that dtype) on the current CUDA device, or an
+    error.  A call of many tensors looks the device up once and gives it as `here`."""
+    if here is None:
+        here = _here()
+    if type(t) is _Tensor and t.get_device() == here and (dtype is None or t.dtype is dtype) and t.is_contiguous():
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -179,30 +200,31 @@ def _dev(t: torch.Tensor, name: str, dtype=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != here:
+        _refuse_device(name, t.get_device())
     return t.data_ptr()
 
 
-def _dev_or_pinned(t: torch.Tensor, name: str, dtype=None):
+def _dev_or_pinned(t: torch.Tensor, name: str, dtype=None, here=None):
     """A CUDA tensor, or a pinned host tensor: with unified addressing its
     pointer is valid on the device and the kernel's stores cross the host link."""
-    if isinstance(t, torch.Tensor) and not t.is_cuda and t.is_pinned():
+    if isinstance(t, _Tensor) and not t.is_cuda and t.is_pinned():
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
-    return _dev(t, name, dtype)
+    return _dev(t, name, dtype, here)
 
 
 # The current stream's handle without a Stream object around it (3 us a call less).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _stream(stream):
+def _stream(stream, here=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(_current_device())
+            return _raw_stream(_current_device() if here is None else here)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -226,12 +248,6 @@ def _running_on(stream):
         caller.wait_stream(s)
 
 
-def _on_current_device(t: torch.Tensor, name: str):
-    """The library launches on the current device: a tensor of another one is refused."""
-    if t.is_cuda and t.get_device() != _current_device():
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{_current_device()}")
-
-
 # ---------------------------------------------------------------- pools
 
 def dsv4sa_pool_bytes(kind: int, num_pages: int) -> int:
@@ -239,10 +255,28 @@ def dsv4sa_pool_bytes(kind: int, num_pages: int) -> int:
 
 
 def dsv4sa_pool_desc_init(kind: int, base: int | torch.Tensor, num_pages: int) -> PoolDesc:
+    """The descriptor of a pool at `base`, a device tensor or an address.  It does not keep
+    the memory alive; calls refuse a pool made from a CUDA tensor that is not on the current
+    device (of an address, or of pinned host memory, there is nothing to compare)."""
     d = PoolDesc()
     ptr = base.data_ptr() if isinstance(base, torch.Tensor) else int(base)
     _check("dsv4sa_pool_desc_init", lib().dsv4sa_pool_desc_init(ctypes.byref(d), kind, ctypes.c_void_p(ptr), num_pages))
+    if isinstance(base, torch.Tensor) and base.is_cuda:
+        d.device = base.get_device()
     return d
+
+
+def _pool(d: PoolDesc, name: str, here=None) -> PoolDesc:
+    if d.device is not None and d.device != (_here() if here is None else here):
+        _refuse_device(name, d.device)
+    return d
+
+
+def _cache(c: "CacheDesc", name: str, here: int):
+    """A reference to a cache on the current device."""
+    if c.device is not None and c.device != here:
+        _refuse_device(name, c.device)
+    return ctypes.byref(c)
 
 
 def _layout(kind: int, num_pages: int) -> PoolDesc:
@@ -322,7 +356,7 @@ def dsv4sa_indexer_logits(kpool: PoolDesc, page_table, q_seq, n_vis, q_fp8, q_sc
                           stream=None):
     T, Hi = q_fp8.shape[0], q_fp8.shape[1]
     st = lib().dsv4sa_indexer_logits(
-        ctypes.byref(kpool), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
+        ctypes.byref(_pool(kpool, "kpool")), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
         _dev(q_seq, "q_seq", torch.int32), _dev(n_vis, "n_vis", torch.int32), _dev(q_fp8, "q_fp8", torch.uint8),
         _dev(q_scale, "q_scale", torch.float32), _dev(w, "w", torch.float32), T, Hi, n_max,
         _dev(logits, "logits", torch.float32), logits.shape[-1], _stream(stream))
@@ -341,7 +375,7 @@ def dsv4sa_indexer_logits_fp4(kpool: PoolDesc, page_table, q_seq, n_vis, q_fp4, 
     """q_fp4: device uint8 [T, Hi, 64] packed E2M1 codes; q_e8m0: uint8 [T, Hi, 4]."""
     T, Hi = q_fp4.shape[0], q_fp4.shape[1]
     st = lib().dsv4sa_indexer_logits_fp4(
-        ctypes.byref(kpool), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
+        ctypes.byref(_pool(kpool, "kpool")), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
         _dev(q_seq, "q_seq", torch.int32), _dev(n_vis, "n_vis", torch.int32), _dev(q_fp4, "q_fp4", torch.uint8),
         _dev(q_e8m0, "q_e8m0", torch.uint8), _dev(w, "w", torch.float32), T, Hi, n_max,
         _dev(logits, "logits", torch.float32), logits.shape[-1], _stream(stream))
@@ -371,7 +405,7 @@ def dsv4sa_topk_prefetch(logits, n_vis, n_max: int, k: int, idx, kv_pool: PoolDe
     wsp = _dev(ws, "ws", torch.uint8) if ws is not None else None
     st = lib().dsv4sa_topk_prefetch(_dev(logits, "logits", torch.float32), logits.shape[-1],
                                     _dev(n_vis, "n_vis", torch.int32), T, n_max, k, _dev(idx, "idx", torch.int32),
-                                    idx.shape[-1], wsp, 0 if ws is None else ws.numel(), ctypes.byref(kv_pool),
+                                    idx.shape[-1], wsp, 0 if ws is None else ws.numel(), ctypes.byref(_pool(kv_pool, "kv_pool")),
                                     _dev(kv_pt, "kv_pt", torch.int32), kv_pt.shape[-1],
                                     _dev(q_seq, "q_seq", torch.int32), _stream(stream))
     _check("dsv4sa_topk_prefetch", st)
@@ -402,10 +436,11 @@ def dsv4sa_cache_write(pool: PoolDesc, page_table, row_seq, row_entry, rows, str
     shape = rows.shape
     if len(shape) != 2 or shape[1] != want:
         raise ValueError(f"rows must be [n, {want}]")
-    _on_current_device(rows, "rows")
+    here = _here()
     st = lib().dsv4sa_cache_write(
-        ctypes.byref(pool), _dev(page_table, "page_table", _int32), page_table.shape[-1], _dev(row_seq, "row_seq", _int32),
-        _dev(row_entry, "row_entry", _int32), _dev(rows, "rows", _bf16), shape[0], _stream(stream))
+        ctypes.byref(_pool(pool, "pool", here)), _dev(page_table, "page_table", _int32, here), page_table.shape[-1],
+        _dev(row_seq, "row_seq", _int32, here), _dev(row_entry, "row_entry", _int32, here), _dev(rows, "rows", _bf16, here),
+        shape[0], _stream(stream, here))
     if st:
         raise DSV4SAError("dsv4sa_cache_write", st)
 
@@ -416,7 +451,7 @@ def dsv4sa_cache_write_rotated(pool: PoolDesc, page_table, row_seq, row_entry, r
     if rows.dim() != 2 or rows.shape[1] != 128:
         raise ValueError("rows must be [n, 128]")
     _check("dsv4sa_cache_write_rotated", lib().dsv4sa_cache_write_rotated(
-        ctypes.byref(pool), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
+        ctypes.byref(_pool(pool, "pool")), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
         _dev(row_seq, "row_seq", torch.int32), _dev(row_entry, "row_entry", torch.int32),
         _dev(rows, "rows", torch.bfloat16), rows.shape[0], _stream(stream)))
 
@@ -424,12 +459,13 @@ def dsv4sa_cache_write_rotated(pool: PoolDesc, page_table, row_seq, row_entry, r
 def dsv4sa_cache_read(pool: PoolDesc, page_table, row_seq, row_entry, rows, stream=None):
     """Rows of a KV or KV_FP4 pool into BF16 rows [n, 512]: the values the attention reads."""
     n = row_entry.shape[0]
-    _on_current_device(rows, "rows")
     if rows.shape != (n, HEAD_DIM) or row_seq.shape[0] != n:
         raise ValueError("rows must be [n, 512] for n entries")
+    here = _here()
     st = lib().dsv4sa_cache_read(
-        ctypes.byref(pool), _dev(page_table, "page_table", _int32), page_table.shape[-1], _dev(row_seq, "row_seq", _int32),
-        _dev(row_entry, "row_entry", _int32), _dev(rows, "rows", _bf16), n, _stream(stream))
+        ctypes.byref(_pool(pool, "pool", here)), _dev(page_table, "page_table", _int32, here), page_table.shape[-1],
+        _dev(row_seq, "row_seq", _int32, here), _dev(row_entry, "row_entry", _int32, here), _dev(rows, "rows", _bf16, here),
+        n, _stream(stream, here))
     if st:
         raise DSV4SAError("dsv4sa_cache_read", st)
 
@@ -439,16 +475,15 @@ def dsv4sa_cache_read(pool: PoolDesc, page_table, row_seq, row_entry, rows, stre
 def _pool_array(pools):
     if not 1 <= len(pools) <= MAX_POOLS:
         raise ValueError(f"a cache has 1 to {MAX_POOLS} pools")
-    return (PoolDesc * len(pools))(*pools)
+    return (PoolDesc * len(pools))(*[_pool(d, "pool") for d in pools])
 
 
 def page_cache(pools, page_table, use) -> CacheDesc:
     """The descriptor of a cache: pools that share page ids, the page table int32
     [rows, pt_stride] and the use counts int32 [num_pages] (table entries that
-    hold each page).  The tensors are kept alive by the descriptor."""
+    hold each page).  The descriptor keeps these two tensors alive, not the pools' memory."""
     if page_table.dim() != 2:
         raise ValueError("page_table must be [rows, pt_stride]")
-    _on_current_device(page_table, "page_table")
     if use.shape != (pools[0].num_pages,):
         raise ValueError("use must have one count per page")
     c = CacheDesc()
@@ -458,6 +493,7 @@ def page_cache(pools, page_table, use) -> CacheDesc:
     c.rows, c.pt_stride = page_table.shape
     c.page_table = _dev(page_table, "page_table", torch.int32)
     c.use = _dev(use, "use", torch.int32)
+    c.device = page_table.get_device()
     return c
 
 
@@ -465,7 +501,6 @@ def dsv4sa_pages_copy(pools, src_page, dst_page, stream=None):
     """Copy pages src_page[i] -> dst_page[i] of every pool in the list (int32 [n]; -1: skip)."""
     if src_page.shape != dst_page.shape:
         raise ValueError("src_page and dst_page differ in length")
-    _on_current_device(src_page, "src_page")
     arr = _pool_array(pools)
     _check("dsv4sa_pages_copy", lib().dsv4sa_pages_copy(
         arr, len(pools), _dev(src_page, "src_page", torch.int32), _dev(dst_page, "dst_page", torch.int32),
@@ -474,8 +509,9 @@ def dsv4sa_pages_copy(pools, src_page, dst_page, stream=None):
 
 def dsv4sa_cache_release(cache: CacheDesc, row, stream=None):
     """Release rows (int32 [n]) of the page table: entries -1, their pages' counts down by one."""
-    _on_current_device(row, "row")
-    st = lib().dsv4sa_cache_release(ctypes.byref(cache), _dev(row, "row", _int32), row.numel(), _stream(stream))
+    here = _here()
+    st = lib().dsv4sa_cache_release(_cache(cache, "cache", here), _dev(row, "row", _int32, here), row.numel(),
+                                    _stream(stream, here))
     if st:
         raise DSV4SAError("dsv4sa_cache_release", st)
 
@@ -486,10 +522,10 @@ def dsv4sa_cache_fork(cache: CacheDesc, src_row, dst_row, length, new_page, stre
     n = src_row.numel()
     if dst_row.numel() != n or length.numel() != n or new_page.numel() != n:
         raise ValueError("src_row, dst_row, length and new_page differ in length")
-    _on_current_device(src_row, "src_row")
+    here = _here()
     st = lib().dsv4sa_cache_fork(
-        ctypes.byref(cache), _dev(src_row, "src_row", _int32), _dev(dst_row, "dst_row", _int32),
-        _dev(length, "length", _int32), n, _dev(new_page, "new_page", _int32), _stream(stream))
+        _cache(cache, "cache", here), _dev(src_row, "src_row", _int32, here), _dev(dst_row, "dst_row", _int32, here),
+        _dev(length, "length", _int32, here), n, _dev(new_page, "new_page", _int32, here), _stream(stream, here))
     if st:
         raise DSV4SAError("dsv4sa_cache_fork", st)
 
@@ -499,18 +535,20 @@ def dsv4sa_cache_compact(src: CacheDesc, dst: CacheDesc, new_id, n_used, stream=
     with dst's table and counts by the new ids.  new_id int32 [src pages], n_used int32 [1]."""
     if new_id.numel() != src.pools[0].num_pages or n_used.numel() != 1:
         raise ValueError("new_id must have one entry per page, n_used one")
-    _on_current_device(new_id, "new_id")
+    here = _here()
     _check("dsv4sa_cache_compact", lib().dsv4sa_cache_compact(
-        ctypes.byref(src), ctypes.byref(dst), _dev(new_id, "new_id", torch.int32), _dev(n_used, "n_used", torch.int32),
-        _stream(stream)))
+        _cache(src, "src", here), _cache(dst, "dst", here), _dev(new_id, "new_id", _int32, here),
+        _dev(n_used, "n_used", _int32, here), _stream(stream, here)))
 
 
 # ---------------------------------------------------------------- norm
 
-def _bf16_rows(t: torch.Tensor, name: str, shape):
-    """A BF16 CUDA tensor [n, dim] whose rows may be strided -> (pointer, row stride)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+def _bf16_rows(t: torch.Tensor, name: str, shape, here):
+    """A BF16 tensor [n, dim] on the current CUDA device whose rows may be strided -> (pointer, row stride)."""
+    if t.get_device() != here:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        _refuse_device(name, t.get_device())
     if t.dtype is not _bf16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     n, dim = shape
@@ -527,30 +565,30 @@ def dsv4sa_rmsnorm_quant(x, norm_w, codes=None, scale=None, group: int = 128, re
     the norm's output as BF16 [n, dim], each where a tensor is given (see dsv4sa.h)."""
     shape = x.shape
     n, dim = shape
-    _on_current_device(x, "x")
     if norm_w.shape != (dim,):
         raise ValueError("norm_w must be [dim]")
-    xp, xs = _bf16_rows(x, "x", shape)
-    rp, rs = _bf16_rows(residual, "residual", shape) if residual is not None else (None, 0)
+    here = _here()
+    xp, xs = _bf16_rows(x, "x", shape, here)
+    rp, rs = _bf16_rows(residual, "residual", shape, here) if residual is not None else (None, 0)
     op = yp = cp = sp = None
     if residual_out is not None:
         if residual_out.shape != shape:
             raise ValueError("residual_out must be [n, dim]")
-        op = _dev(residual_out, "residual_out", _bf16)
+        op = _dev(residual_out, "residual_out", _bf16, here)
     if y is not None:
         if y.shape != shape:
             raise ValueError("y must be [n, dim]")
-        yp = _dev(y, "y", _bf16)
+        yp = _dev(y, "y", _bf16, here)
     if codes is not None:
         if codes.shape != shape:
             raise ValueError("codes must be [n, dim]")
-        cp = _dev(codes, "codes", torch.uint8)
+        cp = _dev(codes, "codes", _u8, here)
     if scale is not None:
         if group < 1 or scale.shape != (n, dim // group):
             raise ValueError("scale must be [n, dim / group]")
-        sp = _dev(scale, "scale", torch.float32)
-    st = lib().dsv4sa_rmsnorm_quant(xp, xs, rp, rs, _dev(norm_w, "norm_w", torch.float32), eps, n, dim, group, op, yp, cp, sp,
-                                    _stream(stream))
+        sp = _dev(scale, "scale", _f32, here)
+    st = lib().dsv4sa_rmsnorm_quant(xp, xs, rp, rs, _dev(norm_w, "norm_w", _f32, here), eps, n, dim, group, op, yp, cp, sp,
+                                    _stream(stream, here))
     if st:
         raise DSV4SAError("dsv4sa_rmsnorm_quant", st)
 
@@ -648,40 +686,40 @@ def _attn_args(q, sink, q_seq, comp, comp_pt, idx_c, win, win_pt, idx_w, out, so
                win_pos=None, kw=None, win_ring=0, flags=0, rope_cs=None, rope_pos=None):
     if q.shape[2] != HEAD_DIM:
         raise ValueError("q must be [T, H, 512]")
-    qp = _dev(q, "q", torch.bfloat16)
-    _on_current_device(q, "q")
+    here = _here()
+    qp = _dev(q, "q", _bf16, here)
     cd = cpt = ic = wd = wpt = iw = wpos = rcs = rpos = None
     cpt_stride = kc = wpt_stride = n_w = iw_stride = ring = rope_rows = 0
     if idx_c is not None:
-        cd = ctypes.pointer(comp)
-        cpt = _dev(comp_pt, "comp_pt", torch.int32)
+        cd = ctypes.pointer(_pool(comp, "comp", here))
+        cpt = _dev(comp_pt, "comp_pt", _int32, here)
         cpt_stride = comp_pt.shape[-1]
-        ic = _dev(idx_c, "idx_c", torch.int32)
+        ic = _dev(idx_c, "idx_c", _int32, here)
         kc = idx_c.shape[-1]
     if idx_w is not None:
-        iw = _dev(idx_w, "idx_w", torch.int32)
+        iw = _dev(idx_w, "idx_w", _int32, here)
         n_w = iw_stride = idx_w.shape[-1]
     elif win_pos is not None and kw:
         # window indices computed in the kernel from the positions
-        wpos = _dev(win_pos, "win_pos", torch.int32)
+        wpos = _dev(win_pos, "win_pos", _int32, here)
         n_w, ring = int(kw), int(win_ring)
     if idx_w is not None or wpos is not None:
-        wd = ctypes.pointer(win)
-        wpt = _dev(win_pt, "win_pt", torch.int32)
+        wd = ctypes.pointer(_pool(win, "win", here))
+        wpt = _dev(win_pt, "win_pt", _int32, here)
         wpt_stride = win_pt.shape[-1]
     if rope_cs is not None:
         # (cos, sin) table [rows, 32, 2] fp32: the inverse rotary embedding of the output
         if rope_cs.dim() != 3 or rope_cs.shape[1:] != (32, 2):
             raise ValueError("rope_cs must be [rows, 32, 2]")
-        rcs = _dev(rope_cs, "rope_cs", torch.float32)
-        rpos = _dev(rope_pos, "rope_pos", torch.int32)
+        rcs = _dev(rope_cs, "rope_cs", _f32, here)
+        rpos = _dev(rope_pos, "rope_pos", _int32, here)
         rope_rows = rope_cs.shape[0]
     # in the order of the fields: one construction costs a third of as many assignments
-    return AttnArgs(qp, q.shape[0], q.shape[1], float(softmax_scale), int(flags), _dev(sink, "attn_sink", torch.float32),
-                    _dev(q_seq, "q_seq", torch.int32), cd, cpt, cpt_stride, kc, ic, kc, n_w, wd, wpt, wpt_stride, iw_stride,
-                    iw, _dev_or_pinned(out, "out", torch.bfloat16),
-                    _dev_or_pinned(lse, "lse", torch.float32) if lse is not None else None,
-                    _dev(ws, "ws", torch.uint8) if ws is not None else None, ws.numel() if ws is not None else 0,
+    return AttnArgs(qp, q.shape[0], q.shape[1], float(softmax_scale), int(flags), _dev(sink, "attn_sink", _f32, here),
+                    _dev(q_seq, "q_seq", _int32, here), cd, cpt, cpt_stride, kc, ic, kc, n_w, wd, wpt, wpt_stride, iw_stride,
+                    iw, _dev_or_pinned(out, "out", _bf16, here),
+                    _dev_or_pinned(lse, "lse", _f32, here) if lse is not None else None,
+                    _dev(ws, "ws", _u8, here) if ws is not None else None, ws.numel() if ws is not None else 0,
                     wpos, ring, 0, rcs, rpos, rope_rows, 0)
 
 
@@ -998,7 +1036,7 @@ class NativeStep:
         sd.dev_in = d.in_arena.data_ptr()
         sd.in_bytes = d.in_arena.numel()
         sd.in_split = self.split
-        sd.kpool = ctypes.pointer(d.keys)
+        sd.kpool = ctypes.pointer(_pool(d.keys, "keys"))
         sd.page_table = _dev(d.comp_pt, "page_table", torch.int32)
         sd.pt_stride = d.comp_pt.shape[-1]
         sd.T = w.T
