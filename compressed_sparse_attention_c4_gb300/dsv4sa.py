@@ -430,12 +430,19 @@ def dsv4sa_window_indices(pos, window: int, ring: int, idx_w, stream=None):
     _check("dsv4sa_window_indices", st)
 
 
+def _one_for_each_row(row_seq, row_entry, n: int):
+    if row_seq.numel() < n or row_entry.numel() < n:
+        raise ValueError(f"row_seq and row_entry must have one entry for each of the {n} rows")
+
+
 def dsv4sa_cache_write(pool: PoolDesc, page_table, row_seq, row_entry, rows, stream=None):
-    """Quantise BF16 rows [n, 512] (KV and KV_FP4 pools) or [n, 128] (indexer-key pools) into the pool."""
+    """Quantise BF16 rows [n, 512] (KV and KV_FP4 pools) or [n, 128] (indexer-key pools) into the pool
+    (of longer lists the first n entries count)."""
     want = HEAD_DIM if pool.kind in (POOL_KV, POOL_KV_FP4) else 128
     shape = rows.shape
     if len(shape) != 2 or shape[1] != want:
         raise ValueError(f"rows must be [n, {want}]")
+    _one_for_each_row(row_seq, row_entry, shape[0])
     here = _here()
     st = lib().dsv4sa_cache_write(
         ctypes.byref(_pool(pool, "pool", here)), _dev(page_table, "page_table", _int32, here), page_table.shape[-1],
@@ -450,6 +457,7 @@ def dsv4sa_cache_write_rotated(pool: PoolDesc, page_table, row_seq, row_entry, r
     them into an FP4 indexer-key pool."""
     if rows.dim() != 2 or rows.shape[1] != 128:
         raise ValueError("rows must be [n, 128]")
+    _one_for_each_row(row_seq, row_entry, rows.shape[0])
     _check("dsv4sa_cache_write_rotated", lib().dsv4sa_cache_write_rotated(
         ctypes.byref(_pool(pool, "pool")), _dev(page_table, "page_table", torch.int32), page_table.shape[-1],
         _dev(row_seq, "row_seq", torch.int32), _dev(row_entry, "row_entry", torch.int32),
