@@ -14,7 +14,8 @@
 // 32 list positions, and merge at the end.  plan4 below chooses HN and CS.
 //
 // Pipeline of a CTA.  The valid rows of the lists are packed -- J is a multiset,
-// their order is free -- into chunks of 128, so -1 entries cost no tensor work:
+// their order is free -- into chunks of 128, so -1 entries cost no tensor work (the window's
+// into chunks of their own where full lists make no more chunks so, see window_apart):
 //   gather warps (16): index -> page id -> row, 256 positions at a time, the valid
 //     ones appended to a ring; a chunk's rows (four threads a row) are loaded into
 //     registers while the chunk before is worked on, then widened to BF16 and
@@ -208,6 +209,12 @@ __host__ __device__ __forceinline__ int share_of(int n, int r, int CS) {
   const int whole = n / (kRun * CS), rest = n - whole * kRun * CS - r * kRun;
   return whole * kRun + min(max(rest, 0), kRun);
 }
+// Whether the window's rows get chunks of their own: where full lists make no more chunks so.
+// Sizes alone decide, so a call that may work on the window before the compressed indices are
+// there (EARLY_WINDOW) forms the same chunks, and the same sums, as one that may not.
+__device__ __forceinline__ bool window_apart(int cw, int cc) {
+  return (cw + kRows - 1) / kRows + (cc + kRows - 1) / kRows == (cw + cc + kRows - 1) / kRows;
+}
 __device__ __forceinline__ int share_at(int k, int r, int CS) { return ((k / kRun) * CS + r) * kRun + k % kRun; }
 
 template <int HN>
@@ -322,9 +329,11 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
     uint32_t round = 0;                         // how often all slots have been filled
     int head = 0;                               // ring: first located row not yet loaded
     const int cw = share_of(p.kw, crank, CS), total = cw + share_of(p.kc, crank, CS);   // this CTA's positions of an item
+    const int cw_apart = window_apart(cw, total - cw) ? cw : 0;   // the window's, if it gets chunks of its own
     for (int item = item0, n_item = 0; item < n_items; item += item_step, ++n_item) {
       const int t = item / groups;
-      int cursor = 0, count = 0;                // positions looked up, rows in the ring
+      int cursor = 0;                           // positions looked up
+      int count = 0;                            // rows in the ring; 2^16 up, those of a window that gets chunks of its own
       bool q_ordered = false;
       // look up the next positions, one a thread of half of them
       auto locate = [&]() {
@@ -360,7 +369,8 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         }
         const uint32_t bits = __ballot_sync(0xffffffffu, rp != 0);
         const int w = static_cast<int>(warp) - 8;
-        if (lane == 0) wcnt[w] = __popc(bits);
+        const uint32_t own_bits = __ballot_sync(0xffffffffu, rp != 0 && pos < cw_apart);
+        if (lane == 0) wcnt[w] = __popc(bits) | __popc(own_bits) << 16;
         named_barrier_sync(kBarGather4, kGatherThreads);
         int before = 0, all = 0;
 #pragma unroll
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
           before += i < w ? n : 0;
           all += n;
         }
-        if (rp != 0) ring[(head + count + before + __popc(bits & ((1u << lane) - 1u))) & (kRing - 1)] = rp;
+        if (rp != 0) ring[(head + ((count + before) & 0xFFFF) + __popc(bits & ((1u << lane) - 1u))) & (kRing - 1)] = rp;
         named_barrier_sync(kBarGather4, kGatherThreads);
         count += all;
         cursor = end;
@@ -386,7 +396,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
         page = reinterpret_cast<const uint8_t*>(rp & ~uint64_t(63));
         rs = row < n ? static_cast<int>(rp & 63) : -1;
         head += n;
-        count -= n;
+        count -= count >= 0x10000 ? n << 16 | n : n;   // the window's come first
       };
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
       auto load_scales = [&]() { return rs >= 0 ? __ldg(reinterpret_cast<const uint4*>(page + kFp4ScaleOff + rs * 16)) : zero; };
@@ -403,22 +413,22 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
       };
       while (true) {
         // ---- enough rows for a chunk, or the end of the lists
-        while (count < kRows && cursor < total) {
-          if (!waited && cursor == cw) {
-            if (count > 0) break;               // the window's rows go first, before idx_c is there
-            griddep_wait();
+        while ((count & 0xFFFF) < kRows && cursor < total) {
+          if (cursor >= cw) {
+            if (count >= 0x10000) break;        // the window's rows go first, before idx_c is there
+            if (!waited) griddep_wait();
             waited = true;
           }
           locate();
         }
-        const int n = min(count, kRows);
+        const int n = min(count >= 0x10000 ? count >> 16 : count, kRows);
         if (n == 0) break;
         take(n);
         scl = load_scales();
 #pragma unroll
         for (int b = 0; b < 4; ++b) load_quarter(b);
         // ---- look ahead while the loads are in flight
-        if (count < kRows && cursor < total && (waited || cursor < cw)) locate();
+        if ((count & 0xFFFF) < kRows && cursor < total && (waited || cursor < cw)) locate();
         // no row of the item is left to come: the softmax may replace Q once this chunk's S is complete
         const bool last = count == 0 && cursor >= total;
         // ---- into the tile, half by half, when the half that was there has been read by its PV
