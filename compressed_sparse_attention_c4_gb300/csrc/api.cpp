@@ -19,6 +19,8 @@ constexpr int64_t kIdxFp4PageBytes = 64 * 64 + 64 * 4;            // 4352
 constexpr int64_t kKvFp4PageBytes = 64 * 224 + 64 * 128 + 64 * 16;   // 23552
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// A required array of 32-bit values.
+bool words(const void* p) { return p && aligned(p, 4); }
 
 // The kernels address pages with the default layout; a descriptor must match it.
 bool pool_ok(const dsv4sa_pool_desc* d, int32_t kind) {
@@ -53,8 +55,7 @@ bool pools_ok(const dsv4sa_pool_desc* pools, int32_t n_pools) {
 }
 
 bool cache_ok(const dsv4sa_cache_desc* c) {
-  return c && pools_ok(c->pools, c->n_pools) && c->rows >= 1 && c->pt_stride >= 1 && c->page_table &&
-         aligned(c->page_table, 4) && c->use && aligned(c->use, 16);
+  return c && pools_ok(c->pools, c->n_pools) && c->rows >= 1 && c->pt_stride >= 1 && words(c->page_table) && c->use && aligned(c->use, 16);
 }
 
 // Whether a byte range lies apart from a cache's table, counts and pools.
@@ -298,7 +299,7 @@ static int attn_validate(int32_t mode, const dsv4sa_attn_args* a) {
   if (a->H < 1 || a->H > DSV4SA_MAX_HEADS) return DSV4SA_ERR_UNSUPPORTED;
   if (a->kc > DSV4SA_MAX_TOPK || a->kw > 1024) return DSV4SA_ERR_UNSUPPORTED;
   if (a->T == 0) return DSV4SA_OK;
-  if (!a->q || !a->attn_sink || !a->q_seq || !a->out) return DSV4SA_ERR_INVALID_ARG;
+  if (!a->q || !words(a->attn_sink) || !words(a->q_seq) || !a->out || !aligned(a->lse, 4)) return DSV4SA_ERR_INVALID_ARG;
   if (!aligned(a->q, 16) || !aligned(a->out, 16)) return DSV4SA_ERR_INVALID_ARG;
   const bool fp4 = attn_fp4(a);
   const int32_t kind = fp4 ? DSV4SA_POOL_KV_FP4 : DSV4SA_POOL_KV;
@@ -306,15 +307,15 @@ static int attn_validate(int32_t mode, const dsv4sa_attn_args* a) {
       (a->comp->kind == DSV4SA_POOL_KV || fp4) && (a->win->kind == DSV4SA_POOL_KV || a->win->kind == DSV4SA_POOL_KV_FP4))
     return DSV4SA_ERR_UNSUPPORTED;   // one FP8 and one FP4 pool
   if (a->kc > 0) {
-    if (!pool_ok(a->comp, kind) || !a->comp_pt || !a->idx_c) return DSV4SA_ERR_INVALID_ARG;
+    if (!pool_ok(a->comp, kind) || !words(a->comp_pt) || !words(a->idx_c)) return DSV4SA_ERR_INVALID_ARG;
     if (a->idx_c_stride < a->kc || a->comp_pt_stride < 1) return DSV4SA_ERR_INVALID_ARG;
   }
   if (a->kw > 0) {
-    if (!pool_ok(a->win, kind) || !a->win_pt || (!a->idx_w && !a->win_pos)) return DSV4SA_ERR_INVALID_ARG;
+    if (!pool_ok(a->win, kind) || !words(a->win_pt) || !(a->idx_w ? aligned(a->idx_w, 4) : words(a->win_pos))) return DSV4SA_ERR_INVALID_ARG;
     if ((a->idx_w && a->idx_w_stride < a->kw) || a->win_pt_stride < 1 || a->win_ring < 0) return DSV4SA_ERR_INVALID_ARG;
   }
   if (fp4 && static_cast<int64_t>(a->kc) + a->kw > (1 << 30)) return DSV4SA_ERR_UNSUPPORTED;
-  if (a->rope_cs && (!a->rope_pos || a->rope_rows < 1 || !aligned(a->rope_cs, 16))) return DSV4SA_ERR_INVALID_ARG;
+  if (a->rope_cs && (!words(a->rope_pos) || a->rope_rows < 1 || !aligned(a->rope_cs, 16))) return DSV4SA_ERR_INVALID_ARG;
   const size_t need = fp4 ? 0 : dsv4sa_attn_workspace_size(mode, a->T, a->H, a->kc, a->kw);
   if (need > 0 && (!a->ws || a->ws_bytes < need || !aligned(a->ws, 16))) return DSV4SA_ERR_WORKSPACE;
   return DSV4SA_OK;
@@ -360,7 +361,7 @@ DSV4SA_API int dsv4sa_cache_write(const dsv4sa_pool_desc* pool, const int32_t* p
       !pool_ok(pool, DSV4SA_POOL_KV_FP4))
     return DSV4SA_ERR_INVALID_ARG;
   if (n == 0) return DSV4SA_OK;
-  if (!page_table || !row_seq || !row_entry || !rows || !aligned(rows, 16)) return DSV4SA_ERR_INVALID_ARG;
+  if (!words(page_table) || !words(row_seq) || !words(row_entry) || !rows || !aligned(rows, 16)) return DSV4SA_ERR_INVALID_ARG;
   return dsv4sa::launch_cache_write(pool, page_table, pt_stride, row_seq, row_entry, rows, n, false, stream);
 }
 
@@ -369,7 +370,7 @@ DSV4SA_API int dsv4sa_cache_write_rotated(const dsv4sa_pool_desc* pool, const in
                                           const void* rows, int32_t n, cudaStream_t stream) {
   if (n < 0 || pt_stride < 1 || !pool_ok(pool, DSV4SA_POOL_IDXK_FP4)) return DSV4SA_ERR_INVALID_ARG;
   if (n == 0) return DSV4SA_OK;
-  if (!page_table || !row_seq || !row_entry || !rows || !aligned(rows, 16)) return DSV4SA_ERR_INVALID_ARG;
+  if (!words(page_table) || !words(row_seq) || !words(row_entry) || !rows || !aligned(rows, 16)) return DSV4SA_ERR_INVALID_ARG;
   return dsv4sa::launch_cache_write(pool, page_table, pt_stride, row_seq, row_entry, rows, n, true, stream);
 }
 
@@ -379,7 +380,7 @@ DSV4SA_API int dsv4sa_cache_read(const dsv4sa_pool_desc* pool, const int32_t* pa
   if (n < 0 || pt_stride < 1) return DSV4SA_ERR_INVALID_ARG;
   if (!pool_ok(pool, DSV4SA_POOL_KV) && !pool_ok(pool, DSV4SA_POOL_KV_FP4)) return DSV4SA_ERR_INVALID_ARG;
   if (n == 0) return DSV4SA_OK;
-  if (!page_table || !row_seq || !row_entry || !rows || !aligned(rows, 16)) return DSV4SA_ERR_INVALID_ARG;
+  if (!words(page_table) || !words(row_seq) || !words(row_entry) || !rows || !aligned(rows, 16)) return DSV4SA_ERR_INVALID_ARG;
   if (overlap(rows, static_cast<uint64_t>(n) * 1024, pool->base, dsv4sa_pool_bytes(pool->kind, pool->num_pages)))
     return DSV4SA_ERR_INVALID_ARG;
   return dsv4sa::launch_cache_read(pool, page_table, pt_stride, row_seq, row_entry, rows, n, stream);
@@ -390,7 +391,7 @@ DSV4SA_API int dsv4sa_pages_copy(const dsv4sa_pool_desc* pools, int32_t n_pools,
   if (n < 0 || !pools_ok(pools, n_pools)) return DSV4SA_ERR_INVALID_ARG;
   if (n > (1 << 28)) return DSV4SA_ERR_UNSUPPORTED;
   if (n == 0) return DSV4SA_OK;
-  if (!src_page || !dst_page) return DSV4SA_ERR_INVALID_ARG;
+  if (!words(src_page) || !words(dst_page)) return DSV4SA_ERR_INVALID_ARG;
   return dsv4sa::launch_pages_copy(pools, n_pools, src_page, dst_page, n, stream);
 }
 
@@ -398,7 +399,7 @@ DSV4SA_API int dsv4sa_cache_release(const dsv4sa_cache_desc* cache, const int32_
                                     cudaStream_t stream) {
   if (n < 0 || !cache_ok(cache)) return DSV4SA_ERR_INVALID_ARG;
   if (n == 0) return DSV4SA_OK;
-  if (!row) return DSV4SA_ERR_INVALID_ARG;
+  if (!words(row)) return DSV4SA_ERR_INVALID_ARG;
   return dsv4sa::launch_cache_release(cache, row, n, stream);
 }
 
@@ -407,7 +408,7 @@ DSV4SA_API int dsv4sa_cache_fork(const dsv4sa_cache_desc* cache, const int32_t* 
   if (n < 0 || !cache_ok(cache)) return DSV4SA_ERR_INVALID_ARG;
   if (n > (1 << 28)) return DSV4SA_ERR_UNSUPPORTED;
   if (n == 0) return DSV4SA_OK;
-  if (!src_row || !dst_row || !length || !new_page) return DSV4SA_ERR_INVALID_ARG;
+  if (!words(src_row) || !words(dst_row) || !words(length) || !words(new_page)) return DSV4SA_ERR_INVALID_ARG;
   const uint64_t bytes = static_cast<uint64_t>(n) * 4;   // new_page is written while the others are read
   if (!apart(cache, new_page, bytes) || overlap(new_page, bytes, src_row, bytes) ||
       overlap(new_page, bytes, dst_row, bytes) || overlap(new_page, bytes, length, bytes))
@@ -417,7 +418,7 @@ DSV4SA_API int dsv4sa_cache_fork(const dsv4sa_cache_desc* cache, const int32_t* 
 
 DSV4SA_API int dsv4sa_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* dst, int32_t* new_id,
                                     int32_t* n_used, cudaStream_t stream) {
-  if (!cache_ok(src) || !cache_ok(dst) || !new_id || !n_used) return DSV4SA_ERR_INVALID_ARG;
+  if (!cache_ok(src) || !cache_ok(dst) || !words(new_id) || !words(n_used)) return DSV4SA_ERR_INVALID_ARG;
   if (src->n_pools != dst->n_pools || src->rows != dst->rows || src->pt_stride != dst->pt_stride)
     return DSV4SA_ERR_INVALID_ARG;
   const uint64_t entries = static_cast<uint64_t>(src->rows) * src->pt_stride * 4;
