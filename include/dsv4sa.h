@@ -322,9 +322,11 @@ DSV4SA_API int dsv4sa_compress_indices(const int32_t* n_vis, int32_t T, int32_t 
  * The pools are two of kind DSV4SA_POOL_KV, or two of kind DSV4SA_POOL_KV_FP4
  * (a 4-bit cache; one of each is DSV4SA_ERR_UNSUPPORTED).  FP4 rows dequantise
  * to BF16 exactly, partial results are exchanged in fp32, and no workspace is
- * needed (ws may be null in either mode); kc + kw <= 2^30.  Rows are weighed with up
- * to 2^8 before the division by the denominator: magnitudes whose sum over a query's rows
- * passes 2^120 may overflow.
+ * needed (ws may be null in either mode); kc + kw <= 2^30.  A query's bits do not depend on
+ * what the others hold, but T, H, kc and kw decide how the work is split and so in which
+ * order a query's sums are formed: its bits may differ between calls of other sizes.
+ * Rows are weighed with up to 2^8 before the division by the denominator: magnitudes whose
+ * sum over a query's rows passes 2^120 may overflow.
  */
 typedef struct {
   const void*  q;              /* device bf16 [T][H][512], 16-byte aligned                 */
