@@ -692,8 +692,12 @@ ATTN_EARLY_WINDOW = 1
 
 def _attn_args(q, sink, q_seq, comp, comp_pt, idx_c, win, win_pt, idx_w, out, softmax_scale, lse, ws,
                win_pos=None, kw=None, win_ring=0, flags=0, rope_cs=None, rope_pos=None):
-    if q.shape[2] != HEAD_DIM:
+    T, H, dim = q.shape
+    if dim != HEAD_DIM:
         raise ValueError("q must be [T, H, 512]")
+    # what the kernel reads and writes for T queries of H heads is there
+    if out.numel() < q.numel() or sink.numel() < H or q_seq.numel() < T or (lse is not None and lse.numel() < T * H):
+        raise ValueError(f"out, attn_sink, q_seq or lse is too small for {T} queries of {H} heads")
     here = _here()
     qp = _dev(q, "q", _bf16, here)
     cd = cpt = ic = wd = wpt = iw = wpos = rcs = rpos = None
@@ -704,13 +708,19 @@ def _attn_args(q, sink, q_seq, comp, comp_pt, idx_c, win, win_pt, idx_w, out, so
         cpt_stride = comp_pt.shape[-1]
         ic = _dev(idx_c, "idx_c", _int32, here)
         kc = idx_c.shape[-1]
+        if idx_c.numel() < T * kc:
+            raise ValueError(f"idx_c must have a row for each of the {T} queries")
     if idx_w is not None:
         iw = _dev(idx_w, "idx_w", _int32, here)
         n_w = iw_stride = idx_w.shape[-1]
+        if idx_w.numel() < T * n_w:
+            raise ValueError(f"idx_w must have a row for each of the {T} queries")
     elif win_pos is not None and kw:
         # window indices computed in the kernel from the positions
         wpos = _dev(win_pos, "win_pos", _int32, here)
         n_w, ring = int(kw), int(win_ring)
+        if win_pos.numel() < T:
+            raise ValueError(f"win_pos must have an entry for each of the {T} queries")
     if idx_w is not None or wpos is not None:
         wd = ctypes.pointer(_pool(win, "win", here))
         wpt = _dev(win_pt, "win_pt", _int32, here)
@@ -721,9 +731,11 @@ def _attn_args(q, sink, q_seq, comp, comp_pt, idx_c, win, win_pt, idx_w, out, so
             raise ValueError("rope_cs must be [rows, 32, 2]")
         rcs = _dev(rope_cs, "rope_cs", _f32, here)
         rpos = _dev(rope_pos, "rope_pos", _int32, here)
+        if rope_pos.numel() < T:
+            raise ValueError(f"rope_pos must have an entry for each of the {T} queries")
         rope_rows = rope_cs.shape[0]
     # in the order of the fields: one construction costs a third of as many assignments
-    return AttnArgs(qp, q.shape[0], q.shape[1], float(softmax_scale), int(flags), _dev(sink, "attn_sink", _f32, here),
+    return AttnArgs(qp, T, H, float(softmax_scale), int(flags), _dev(sink, "attn_sink", _f32, here),
                     _dev(q_seq, "q_seq", _int32, here), cd, cpt, cpt_stride, kc, ic, kc, n_w, wd, wpt, wpt_stride, iw_stride,
                     iw, _dev_or_pinned(out, "out", _bf16, here),
                     _dev_or_pinned(lse, "lse", _f32, here) if lse is not None else None,
