@@ -287,12 +287,6 @@ DSV4SA_API int dsv4sa_attn_plan(int32_t mode, int32_t T, int32_t H, int32_t kc, 
   return dsv4sa::attn_plan(mode, T, H, kc, kw, nsplit, rows_per_split, launches);
 }
 
-// Whether an attention call reads FP4 pools: both of its pools are.
-static bool attn_fp4(const dsv4sa_attn_args* a) {
-  const dsv4sa_pool_desc* d = a->kc > 0 ? a->comp : (a->kw > 0 ? a->win : nullptr);
-  return d && d->kind == DSV4SA_POOL_KV_FP4;
-}
-
 static int attn_validate(int32_t mode, const dsv4sa_attn_args* a) {
   if (!a) return DSV4SA_ERR_INVALID_ARG;
   if (a->T < 0 || a->kc < 0 || a->kw < 0) return DSV4SA_ERR_INVALID_ARG;
@@ -301,7 +295,7 @@ static int attn_validate(int32_t mode, const dsv4sa_attn_args* a) {
   if (a->T == 0) return DSV4SA_OK;
   if (!a->q || !words(a->attn_sink) || !words(a->q_seq) || !a->out || !aligned(a->lse, 4)) return DSV4SA_ERR_INVALID_ARG;
   if (!aligned(a->q, 16) || !aligned(a->out, 16)) return DSV4SA_ERR_INVALID_ARG;
-  const bool fp4 = attn_fp4(a);
+  const bool fp4 = dsv4sa::attn_over_fp4(a);
   const int32_t kind = fp4 ? DSV4SA_POOL_KV_FP4 : DSV4SA_POOL_KV;
   if (a->kc > 0 && a->kw > 0 && a->comp && a->win && a->comp->kind != a->win->kind &&
       (a->comp->kind == DSV4SA_POOL_KV || fp4) && (a->win->kind == DSV4SA_POOL_KV || a->win->kind == DSV4SA_POOL_KV_FP4))

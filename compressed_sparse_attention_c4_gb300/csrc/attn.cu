@@ -825,18 +825,12 @@ static int fill_params(int32_t mode, const dsv4sa_attn_args* a, AttnParams& p, i
   return DSV4SA_OK;
 }
 
-// A call over FP4 pools (both are, the front end has checked).
-static bool fp4_pools(const dsv4sa_attn_args* a) {
-  const dsv4sa_pool_desc* d = a->kc > 0 ? a->comp : (a->kw > 0 ? a->win : nullptr);
-  return d && d->kind == DSV4SA_POOL_KV_FP4;
-}
-
 int launch_sparse_attn(int32_t mode, const dsv4sa_attn_args* a, cudaStream_t stream) {
   AttnParams p{};
   int hn = 0, groups = 0;
   const int rc = fill_params(mode, a, p, hn, groups);
   if (rc != DSV4SA_OK || a->T == 0) return rc;
-  if (fp4_pools(a)) return attn::launch_fp4(mode, p, stream);
+  if (attn_over_fp4(a)) return attn::launch_fp4(mode, p, stream);
   if (mode == DSV4SA_ATTN_DECODE && p.merge == kMergeCluster) return attn::launch_decode_cluster(p, hn, groups, stream);
   switch (hn) {
     case 16: return launch_hn<16>(p, groups, stream);
@@ -856,7 +850,7 @@ int launch_topk_sparse_attn(const dsv4sa_attn_args* a, const float* logits, int6
   int hn = 0, groups = 0;
   const int rc = fill_params(DSV4SA_ATTN_DECODE, a, p, hn, groups);
   if (rc != DSV4SA_OK || a->T == 0) return rc;
-  const bool fp4 = fp4_pools(a);
+  const bool fp4 = attn_over_fp4(a);
   const bool fuse = !fp4 && p.merge == kMergeCluster && k <= a->kc && n_max <= attn::kFusedMaxRow &&
                     p.kc_split <= attn::kFusedMaxSplitRows && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
                     logits_stride % 4 == 0;

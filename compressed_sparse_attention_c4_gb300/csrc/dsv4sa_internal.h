@@ -54,6 +54,13 @@ int attn_plan(int32_t mode, int32_t T, int32_t H, int32_t kc, int32_t kw, int32_
 // so repeated calls (and calls under stream capture) make no attribute call.
 bool smem_attr_once(int device, int slot, const void* kernel, int bytes);
 
+// Whether an attention call reads FP4 pools: its first list's pool decides, and the front end
+// refuses a second pool of another kind.
+inline bool attn_over_fp4(const dsv4sa_attn_args* a) {
+  const dsv4sa_pool_desc* d = a->kc > 0 ? a->comp : (a->kw > 0 ? a->win : nullptr);
+  return d && d->kind == DSV4SA_POOL_KV_FP4;
+}
+
 uint32_t read_error_word_indexer(cudaStream_t stream, bool clear);
 uint32_t read_error_word_topk(cudaStream_t stream, bool clear);
 uint32_t read_error_word_attn(cudaStream_t stream, bool clear);
