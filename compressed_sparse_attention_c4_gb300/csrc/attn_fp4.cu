@@ -36,7 +36,7 @@
 // K = 16 reads 6 KB and takes 48 cycles, the 128 bytes a clock of shared memory
 // (measured), so while MMAs run other accesses hardly proceed, and the phases of a
 // chunk (about 3000 cycles of MMAs, 1000 of stores, the widening's 7168 words of eight codes)
-// follow one another: 4096 queries of 640 rows take 578 us, 594 TFLOP/s.  The tile is
+// follow one another: 4096 queries of 640 rows take 582 us, 590 TFLOP/s.  The tile is
 // handed over in two halves of its dims: as a whole that call took 687 us, by quarters
 // 629, by halves 617 then (a wait drains the tensor pipe).  Two tiles of 64 rows in turn, a
 // group of gather warps for each, took 726 against 610: each step from one kind of warp to
@@ -71,8 +71,10 @@ constexpr int kLastChunk = 256;          // meta: rows of the chunk (<= 128), an
 // Registers per thread (setmaxnreg): the launch gives 896 x 72 = 64512, the three
 // kinds of warpgroup then hold 256 x 96 + 512 x 64 + 128 x 56 = 64512, or, for 64 heads,
 // whose softmax threads have 32 scores and sums each, 256 x 120 + 512 x 56 + 128 x 40 (4096
-// queries of 64 heads 580 us, with 112, 56 and 56 584, with the first shares 597; 128 of 8
-// heads 31.2 us, with 112, 56 and 56 33.7).
+// queries of 64 heads, in a graph: 582 us, with 112, 56 and 56 582, with the first shares 599;
+// 1024 with a window of 60 rows 153.3, 154.4, 158.8).  With 112, 56 and 56 the smaller items
+// take as long (128 ragged queries of 8 heads 31.6 us and 31.5).  The 64-head kernel spills a
+// little by the compiler's count, 44 bytes stored and 40 loaded.
 template <int HN>
 struct Regs4 {
   static constexpr int kCompute = HN == 64 ? 120 : 96, kGather = HN == 64 ? 56 : 64, kMma = HN == 64 ? 40 : 56;
@@ -87,7 +89,7 @@ template <int HN>
 struct Smem4 {
   // Halves of tiles.  (With 16 heads a third one fits, so that the next chunk is widened
   // while this one is scored: 128 queries of 8 heads, up to 1152 rows, 31.2 us for 32.1 in
-  // a graph of such calls, but 37.2 for 33.3 launched one by one.)
+  // a graph of such calls then, but 37.2 for 33.3 launched one by one.)
   static constexpr int kSlots = 2;
   static constexpr int kStage = HN == 16 ? 8 : 16;       // heads of an output step
   static constexpr int kKv = 0;
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(kThreads4, 1) sparse_attn_fp4_kernel(const Att
             // 32 values: units 4 (piece & 1) + x of column block 2 b + (piece >> 1).  The
             // upper two pieces take x in the order 2, 3, 0, 1, so that the eight lanes of
             // two rows hit eight different bank groups.  (Eight lanes with eight rows of the
-            // same piece would, too, but load eight half-used sectors: 644 us for 578.)
+            // same piece would, too, but load eight half-used sectors: 644 us for 578 then.)
             const BlockScale bs = block_scale((sb >> (8 * b)) & 0xFFu);
             uint8_t* blk = half + (2 * (b & 1) + (piece >> 1)) * kKvBlock;
             const uint32_t c4[4] = {code[b].x, code[b].y, code[b].z, code[b].w};

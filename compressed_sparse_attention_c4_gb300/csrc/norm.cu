@@ -15,11 +15,11 @@
 // current row is reduced, so reads stay in flight.  Rows of up to 512 are bound by
 // their instructions as much as by HBM: two units a thread instead of one halve the
 // shuffles and addresses a value, packed fp32 the arithmetic, and 64 registers leave
-// 32 warps a multiprocessor (262144 rows of 128: 41 us before these, 20.4 with them,
-// 18.3 with 32-bit rows and the hardware's reciprocals, 15.2 at the measured copy bandwidth;
-// several rows a thread at once took 23 to 31).  Long
-// rows are bound by HBM: 8191 rows of 7168 with residual, sum and BF16 output 80.9 us,
-// 78.3 at the copy's bandwidth.
+// 32 warps a multiprocessor (262144 rows of 128: 41 us before these, 20.4 with them, 18.3
+// with 32-bit rows and the hardware's reciprocals, 17.8 with rare means apart, 15.2 at the
+// measured copy bandwidth; several rows a thread at once took 23 to 31).  With a residual these
+// kernels spill 16 bytes.  Long rows are bound by HBM: 8191 rows of 7168 with residual, sum and
+// BF16 output 80.5 us, 78.3 at the copy's bandwidth.
 #include <atomic>
 
 #include "common.cuh"

@@ -7,9 +7,12 @@
 // the device, so a beam step or a clean-up costs the host no round trip.
 //
 // Everything here moves bytes: the bound is HBM for whole pages (compacting 29490 pages of
-// 27904 bytes takes 244 us, the measured copy bandwidth) and latency for a few table
-// rows (four forks of one sequence, released before, 7.8 us in two kernels; 256 forks of
-// 64 sequences 13.6, their bytes 2).  Counts are 32-bit integers changed by atomic additions,
+// 27904 bytes takes 244 us, the measured copy bandwidth; copying 16000 of them by a list
+// 139, 6.4 TB/s) and latency for a few table rows (four forks of one sequence, released
+// before, 8.0 us in two kernels; 256 forks of 64 sequences 13.6, their bytes 2).  Two plans
+// are one CTA's walk over the use counts and grow with the pool: the search for free pages
+// takes 155 us for each million pages in use below the first free one, the plan of a compaction
+// in place 1.0 ms for each million pages.  Counts are 32-bit integers changed by atomic additions,
 // whose order does not change the result; page ids are handed out by scans in
 // id order, so a call gives the same ids every time.
 #include "common.cuh"
@@ -41,8 +44,7 @@ struct CacheParams {
 };
 
 // Copy `units` 16-byte units, up to eight loads in flight per thread (a page is five
-// to ten units a thread, so a loop of whole batches alone would run one at a time:
-// a compaction that took 370 us so took 294 with batches of eight).
+// to ten units a thread, so a loop of whole batches alone would run one at a time).
 __device__ __forceinline__ void copy_units(uint4* dst, const uint4* src, int units, int tid, int threads) {
   for (int u0 = tid; u0 < units; u0 += 8 * threads) {
     uint4 v[8];
@@ -56,7 +58,8 @@ __device__ __forceinline__ void copy_units(uint4* dst, const uint4* src, int uni
 }
 
 // Page `to` of every pool of d = page `from` of s's, by a CTA: one list of 16-byte
-// units over the pools, eight in flight a thread.
+// units over the pools, eight in flight a thread (a compaction that took 370 us with one
+// in flight took 294 so, before the grid of launch_cache_compact).
 __device__ __forceinline__ void copy_page(const CacheParams& d, int64_t to, const CacheParams& s, int64_t from, int tid) {
   int total = 0;
   for (int k = 0; k < s.n_pools; ++k) total += static_cast<int>(s.pool[k].stride / 16);

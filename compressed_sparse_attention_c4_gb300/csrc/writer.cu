@@ -267,9 +267,11 @@ __global__ void __launch_bounds__(kThreads) fp4_key_write_kernel(const WriterPar
 // exponent as one byte (the last two bytes of the scale row are padding, never
 // written).  A block that holds an infinity or a NaN gets the exponent byte 255
 // (E8M0 NaN) and codes 0, so it reads back as NaN.  kRowsW rows per warp are in
-// flight: the row loads are independent of the entry -> page look-ups (65529 rows 14.8 us,
-// 13.5 being the bytes at the measured copy bandwidth; 15.4 with one row, 14.6 with four,
-// but 32 rows take 1.6, 2.1 and 2.5 us).  The integer pipe is nearly as busy (73%).
+// flight: the row loads are independent of the entry -> page look-ups.  65529 rows take
+// 15.0 us in a graph of such calls, 13.5 being the bytes at the measured copy bandwidth, and
+// 32 rows 2.3 (with the grid of launch_rows below, one row a warp takes 14.6 and 1.9, four 15.1
+// and 2.9; two were the best of 65529 with eight CTAs a multiprocessor).  The integer pipe is
+// nearly as busy (68%).
 constexpr int kRowsW = 2;
 
 // Eight values -> eight codes, nearest, ties to even, saturating (as e2m1_code counts out).
@@ -370,9 +372,9 @@ __global__ void __launch_bounds__(kThreads) kv_fp4_write_kernel(const WriterPara
 // bits; past its range an infinity, as a product of the two rounds to).  A warp per
 // row, lane c writing the 16-byte units c and 32 + c of it as in the writer; kRowsR
 // rows per warp in flight.  One: a row is three dependent loads (entry, page id, row), but
-// many warps hide them as well as many rows a warp do (65529 FP4 rows, each warp once: 16.8 us with 1 row,
-// 17.5 with 2, 16.9 with 4, 20.1 with 8) and few rows are read sooner (32 rows 1.7 us, 2.1,
-// 2.7, 3.5).
+// many warps hide them better than many rows a warp do (65529 FP4 rows, in L2 from the
+// call before: 15.9 us with one row, 17.3 with two, 17.1 with four), and few rows are read
+// sooner (32 rows 1.9 us, 2.3, 2.9).  65529 rows of an FP8 pool take 16.3 us.
 constexpr int kRowsR = 1;
 
 struct ReaderParams {
@@ -468,8 +470,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReaderParams
 
 // CTAs of `rows_per_block` rows over n rows, at most 20 a multiprocessor (six run at once):
 // enough that none is left with more to do, few enough that starting them does not show
-// (65529 FP4 rows written and read: 30.4 us; 64 a multiprocessor, one batch each, 31.8,
-// 12 31.4, 8 32.1).
+// (65529 FP4 rows written and then read, in a graph: 32.4 us; 64 a multiprocessor, one batch
+// each, 33.9, 12 33.3, 8 34.7).
 template <class P>
 cudaError_t launch_rows(void (*kernel)(P), const P& p, int64_t n, int64_t rows_per_block, cudaStream_t stream) {
   int dev = 0, sms = 0;
