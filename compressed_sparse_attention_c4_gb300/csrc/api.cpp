@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include <cuda_runtime_api.h>
@@ -78,7 +79,7 @@ uint64_t row_span(int64_t n, int64_t stride, int32_t dim) {
 namespace dsv4sa {
 
 bool smem_attr_once(int device, int slot, const void* kernel, int bytes) {
-  constexpr int kDevices = 64, kSlots = 16;
+  constexpr int kDevices = 64, kSlots = 24;
   static std::atomic<int> done[kDevices][kSlots];
   static std::mutex mu;
   if (device < 0 || device >= kDevices || slot < 0 || slot >= kSlots) return false;
@@ -469,6 +470,115 @@ DSV4SA_API int dsv4sa_rmsnorm_quant(const void* x, int64_t x_stride, const void*
                                       y, codes, scale, stream);
 }
 
+DSV4SA_API int dsv4sa_rope_table(float* cs, int64_t rows, int32_t pairs, int64_t first, double base, double factor,
+                                 int64_t original_len, double beta_fast, double beta_slow, cudaStream_t stream) {
+  if (rows < 0 || first < 0 || first > INT64_MAX - rows || pairs < 1 || original_len < 0) return DSV4SA_ERR_INVALID_ARG;
+  if (pairs > DSV4SA_MAX_ROPE_PAIRS) return DSV4SA_ERR_UNSUPPORTED;
+  if (!(base > 1.0 && base < 1e30) || !(factor >= 1.0 && factor < 1e30)) return DSV4SA_ERR_INVALID_ARG;
+  if (original_len > 0 && !(beta_slow > 0.0 && beta_fast >= beta_slow && beta_fast < 1e30)) return DSV4SA_ERR_INVALID_ARG;
+  if (rows == 0) return DSV4SA_OK;
+  if (!cs || !aligned(cs, 8)) return DSV4SA_ERR_INVALID_ARG;
+  return dsv4sa::launch_rope_table(cs, rows, pairs, first, base, factor, original_len, beta_fast, beta_slow, stream);
+}
+
+DSV4SA_API int dsv4sa_rope(const dsv4sa_rope_args* a, cudaStream_t stream) {
+  if (!a || a->T < 0 || a->H < 1 || a->dim < 8 || a->dim % 8 != 0) return DSV4SA_ERR_INVALID_ARG;
+  if (a->rope_dim < 16 || a->rope_dim % 16 != 0 || a->rope_off < 0 || a->rope_off % 8 != 0 ||
+      static_cast<int64_t>(a->rope_off) + a->rope_dim > a->dim)
+    return DSV4SA_ERR_INVALID_ARG;
+  if (a->layout != DSV4SA_ROPE_PAIRS && a->layout != DSV4SA_ROPE_HALVES) return DSV4SA_ERR_INVALID_ARG;
+  if ((a->inverse != 0 && a->inverse != 1) || (a->norm != 0 && a->norm != 1) || (a->norm && !(a->eps >= 0.f))) return DSV4SA_ERR_INVALID_ARG;
+  if (a->dim > 1024 || a->rope_dim > 2 * DSV4SA_MAX_ROPE_PAIRS || static_cast<int64_t>(a->T) * a->H >= (int64_t{1} << 30))
+    return DSV4SA_ERR_UNSUPPORTED;
+  const int64_t T = a->T, H = a->H, dim = a->dim, most = int64_t{1} << 40;
+  // a stride that only one row would use says nothing
+  const int64_t xt = T > 1 ? a->x_tok_stride : 0, xh = H > 1 ? a->x_head_stride : 0;
+  const int64_t ot = T > 1 ? a->out_tok_stride : 0, oh = H > 1 ? a->out_head_stride : 0;
+  for (const int64_t s : {xt, xh, ot, oh})
+    if (s < 0 || s % 8 != 0 || s > most) return DSV4SA_ERR_INVALID_ARG;
+  // the rows of out lie apart: heads within a token, or tokens within a head
+  if (!((H == 1 || oh >= dim) && (T == 1 || ot >= (H - 1) * oh + dim)) && !((T == 1 || ot >= dim) && (H == 1 || oh >= (T - 1) * ot + dim)))
+    if (T > 0) return DSV4SA_ERR_INVALID_ARG;
+  if (T == 0) return DSV4SA_OK;
+  if (!a->x || !a->out || !aligned(a->x, 16) || !aligned(a->out, 16)) return DSV4SA_ERR_INVALID_ARG;
+  if (!words(a->pos) || !a->rope_cs || !aligned(a->rope_cs, 16) || a->rope_rows < 1 || !aligned(a->norm_w, 16)) return DSV4SA_ERR_INVALID_ARG;
+  const uint64_t x_bytes = static_cast<uint64_t>((T - 1) * xt + (H - 1) * xh + dim) * 2;
+  const uint64_t out_bytes = static_cast<uint64_t>((T - 1) * ot + (H - 1) * oh + dim) * 2;
+  const bool in_place = a->x == a->out && xt == ot && xh == oh;
+  if (!in_place && overlap(a->x, x_bytes, a->out, out_bytes)) return DSV4SA_ERR_INVALID_ARG;
+  if (overlap(a->out, out_bytes, a->rope_cs, static_cast<uint64_t>(a->rope_rows) * a->rope_dim * 4) ||
+      overlap(a->out, out_bytes, a->pos, static_cast<uint64_t>(T) * 4) ||
+      (a->norm && a->norm_w && overlap(a->out, out_bytes, a->norm_w, static_cast<uint64_t>(dim) * 4)))
+    return DSV4SA_ERR_INVALID_ARG;
+  dsv4sa_rope_args b = *a;
+  b.x_tok_stride = xt, b.x_head_stride = xh, b.out_tok_stride = ot, b.out_head_stride = oh;
+  return dsv4sa::launch_rope(&b, stream);
+}
+
+DSV4SA_API int dsv4sa_cache_append(const dsv4sa_append_args* a, cudaStream_t stream) {
+  if (!a || a->n < 0 || a->n_src < 0 || a->pt_stride < 1 || a->ring < 0) return DSV4SA_ERR_INVALID_ARG;
+  if ((a->norm != 0 && a->norm != 1) || (a->norm && !(a->eps >= 0.f))) return DSV4SA_ERR_INVALID_ARG;
+  if (!pool_ok(a->pool, DSV4SA_POOL_KV) && !pool_ok(a->pool, DSV4SA_POOL_KV_FP4)) return DSV4SA_ERR_INVALID_ARG;
+  if (a->row_stride < DSV4SA_HEAD_DIM || a->row_stride % 8 != 0) return DSV4SA_ERR_INVALID_ARG;
+  if (a->n == 0) return DSV4SA_OK;
+  if (a->n_src < 1 || (!a->src_row && a->n_src < a->n)) return DSV4SA_ERR_INVALID_ARG;
+  if (!words(a->page_table) || !words(a->row_seq) || !a->rows || !aligned(a->rows, 16)) return DSV4SA_ERR_INVALID_ARG;
+  if (!aligned(a->row_pos, 4) || !aligned(a->row_entry, 4) || !aligned(a->src_row, 4) || !aligned(a->norm_w, 16)) return DSV4SA_ERR_INVALID_ARG;
+  if (!a->row_pos && (!a->row_entry || a->rope_cs)) return DSV4SA_ERR_INVALID_ARG;   // no slot, or no angle
+  if (a->rope_cs && (!aligned(a->rope_cs, 16) || a->rope_rows < 1)) return DSV4SA_ERR_INVALID_ARG;
+  if (overlap(a->rows, row_span(a->n_src, a->row_stride, DSV4SA_HEAD_DIM), a->pool->base,
+              dsv4sa_pool_bytes(a->pool->kind, a->pool->num_pages)))
+    return DSV4SA_ERR_INVALID_ARG;
+  return dsv4sa::launch_cache_append(a, stream);
+}
+
+DSV4SA_API size_t dsv4sa_tree_attn_workspace_size(int32_t n_seqs, int32_t max_nodes, int32_t H, int32_t n_max, int32_t window) {
+  if (n_seqs < 1 || max_nodes < 1 || max_nodes > DSV4SA_MAX_TREE_NODES || H < 1 || H > DSV4SA_MAX_HEADS || n_max < 0 || window < 0) return 0;
+  return dsv4sa::tree_attn_workspace(n_seqs, max_nodes, H, n_max, window);
+}
+
+DSV4SA_API int dsv4sa_tree_attn(const dsv4sa_tree_args* a, cudaStream_t stream) {
+  if (!a || a->T < 0 || a->n_seqs < 0 || a->max_nodes < 0 || a->n_max < 0 || a->window < 0 || a->win_ring < 0 || a->draft_entry < -1)
+    return DSV4SA_ERR_INVALID_ARG;
+  if (a->H < 1 || a->H > DSV4SA_MAX_HEADS || a->max_nodes > DSV4SA_MAX_TREE_NODES) return DSV4SA_ERR_UNSUPPORTED;
+  if (a->n_max > (1 << 29) || a->window > DSV4SA_MAX_TREE_WINDOW || a->draft_entry > (1 << 30)) return DSV4SA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(a->T) * a->H >= (int64_t{1} << 31) ||
+      static_cast<int64_t>(a->n_seqs) * ((static_cast<int64_t>(a->max_nodes) * a->H + 63) / 64) >= (int64_t{1} << 31))
+    return DSV4SA_ERR_UNSUPPORTED;
+  if (a->T == 0 || a->n_seqs == 0 || a->max_nodes == 0) return DSV4SA_OK;
+  if (!a->q || !a->out || !aligned(a->q, 16) || !aligned(a->out, 16) || !words(a->attn_sink) || !aligned(a->lse, 4)) return DSV4SA_ERR_INVALID_ARG;
+  if (!words(a->node_start) || !aligned(a->seq_row, 4) || !words(a->ctx) || !words(a->pos) || !aligned(a->anc, 8) || !words(a->n_vis))
+    return DSV4SA_ERR_INVALID_ARG;
+  const bool comp = a->n_max > 0, win = a->window > 0 || a->draft_entry >= 0;
+  for (const dsv4sa_pool_desc* d : {comp ? a->comp : nullptr, win ? a->win : nullptr})
+    if (d && !pool_ok(d, DSV4SA_POOL_KV) && !pool_ok(d, DSV4SA_POOL_KV_FP4)) return DSV4SA_ERR_INVALID_ARG;
+  if (comp && (!a->comp || !words(a->comp_pt) || a->comp_pt_stride < 1 ||
+               a->n_max > static_cast<int64_t>(a->comp_pt_stride) * DSV4SA_PAGE_SIZE))
+    return DSV4SA_ERR_INVALID_ARG;
+  if (win && (!a->win || !words(a->win_pt) || a->win_pt_stride < 1 ||
+              a->win_ring > static_cast<int64_t>(a->win_pt_stride) * DSV4SA_PAGE_SIZE))
+    return DSV4SA_ERR_INVALID_ARG;
+  if (comp && win && a->comp->kind != a->win->kind) return DSV4SA_ERR_UNSUPPORTED;   // one FP8 and one FP4 pool
+  if (a->rope_cs && (!words(a->rope_pos) || a->rope_rows < 1 || !aligned(a->rope_cs, 16))) return DSV4SA_ERR_INVALID_ARG;
+  const size_t need = dsv4sa::tree_attn_workspace(a->n_seqs, a->max_nodes, a->H, a->n_max, a->window);
+  if (!a->ws || a->ws_bytes < need || !aligned(a->ws, 16)) return DSV4SA_ERR_WORKSPACE;
+  const uint64_t rows = static_cast<uint64_t>(a->T) * a->H;
+  if (overlap(a->out, rows * 1024, a->q, rows * 1024)) return DSV4SA_ERR_INVALID_ARG;
+  return dsv4sa::launch_tree_attn(a, stream);
+}
+
+DSV4SA_API int dsv4sa_tree_window_indices(const int32_t* node_start, const int32_t* ctx, const int32_t* pos, const uint64_t* anc,
+                                          int32_t n_seqs, int32_t T, int32_t max_nodes, int32_t window, int32_t ring,
+                                          int32_t draft_entry, int32_t* idx_w, int64_t idx_stride, cudaStream_t stream) {
+  if (n_seqs < 0 || T < 0 || max_nodes < 0 || window < 0 || ring < 0 || draft_entry < -1) return DSV4SA_ERR_INVALID_ARG;
+  if (max_nodes > DSV4SA_MAX_TREE_NODES || window > DSV4SA_MAX_TREE_WINDOW || draft_entry > (1 << 30)) return DSV4SA_ERR_UNSUPPORTED;
+  if (idx_stride < static_cast<int64_t>(window) + max_nodes) return DSV4SA_ERR_INVALID_ARG;
+  if (n_seqs == 0 || T == 0 || max_nodes == 0) return DSV4SA_OK;
+  if (!words(node_start) || !words(ctx) || !words(pos) || !aligned(anc, 8) || !words(idx_w)) return DSV4SA_ERR_INVALID_ARG;
+  return dsv4sa::launch_tree_window_indices(node_start, ctx, pos, anc, n_seqs, T, max_nodes, window, ring, draft_entry, idx_w,
+                                            idx_stride, stream);
+}
+
 DSV4SA_API int dsv4sa_compress_windows(const void* kv, const void* score, int64_t tok_stride, int64_t n_tok,
                                        const int32_t* first_tok, const int32_t* prev_tok, const int32_t* position,
                                        int32_t n, int32_t ratio, int32_t overlap, const float* ape,
@@ -530,7 +640,8 @@ DSV4SA_API int dsv4sa_check_errors(cudaStream_t stream, uint32_t* bits_out) {
                         dsv4sa::read_error_word_attn(stream, true) | dsv4sa::read_error_word_attn_decode(stream, true) |
                         dsv4sa::read_error_word_writer(stream, true) |
                         dsv4sa::read_error_word_compress(stream, true) | dsv4sa::read_error_word_pages(stream, true) |
-                        dsv4sa::read_error_word_attn_fp4(stream, true);
+                        dsv4sa::read_error_word_attn_fp4(stream, true) | dsv4sa::read_error_word_rope(stream, true) |
+                        dsv4sa::read_error_word_append(stream, true) | dsv4sa::read_error_word_attn_tree(stream, true);
   if (cudaGetLastError() != cudaSuccess) return DSV4SA_ERR_CUDA;
   if (bits_out) *bits_out = bits;
   if (bits & 2u) return DSV4SA_ERR_DEVICE_TIMEOUT;

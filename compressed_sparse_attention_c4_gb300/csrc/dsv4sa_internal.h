@@ -69,6 +69,9 @@ uint32_t read_error_word_writer(cudaStream_t stream, bool clear);
 uint32_t read_error_word_compress(cudaStream_t stream, bool clear);
 uint32_t read_error_word_attn_fp4(cudaStream_t stream, bool clear);
 uint32_t read_error_word_pages(cudaStream_t stream, bool clear);
+uint32_t read_error_word_rope(cudaStream_t stream, bool clear);
+uint32_t read_error_word_append(cudaStream_t stream, bool clear);
+uint32_t read_error_word_attn_tree(cudaStream_t stream, bool clear);
 int launch_selftest_wait_timeout(int32_t* result, cudaStream_t stream);
 int launch_compress_windows(const void* kv, const void* score, int64_t tok_stride, int64_t n_tok,
                             const int32_t* first_tok,
@@ -92,6 +95,17 @@ int launch_cache_fork(const dsv4sa_cache_desc* c, const int32_t* src, const int3
                       int32_t* new_page, cudaStream_t stream);
 int launch_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* dst, int32_t* new_id, int32_t* n_used,
                          cudaStream_t stream);
+
+int launch_rope_table(float* cs, int64_t rows, int32_t pairs, int64_t first, double base, double factor,
+                      int64_t original_len, double beta_fast, double beta_slow, cudaStream_t stream);
+int launch_rope(const dsv4sa_rope_args* a, cudaStream_t stream);
+int launch_cache_append(const dsv4sa_append_args* a, cudaStream_t stream);
+
+size_t tree_attn_workspace(int32_t n_seqs, int32_t max_nodes, int32_t H, int32_t n_max, int32_t window);
+int launch_tree_attn(const dsv4sa_tree_args* a, cudaStream_t stream);
+int launch_tree_window_indices(const int32_t* node_start, const int32_t* ctx, const int32_t* pos, const uint64_t* anc, int32_t n_seqs,
+                               int32_t T, int32_t max_nodes, int32_t window, int32_t ring, int32_t draft_entry, int32_t* idx_w,
+                               int64_t idx_stride, cudaStream_t stream);
 
 int launch_rmsnorm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                          const float* norm_w, float eps, int32_t n, int32_t dim, int32_t group, void* residual_out,

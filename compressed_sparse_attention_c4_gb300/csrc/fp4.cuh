@@ -69,4 +69,18 @@ __device__ __forceinline__ uint4 scale_up(uint4 v, uint32_t more) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight values -> eight codes, nearest, ties to even, saturating (0.25 -> 0, 0.75 -> 1, ...).
+__device__ __forceinline__ uint32_t e2m1x8(const float2* y) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(y[0].x), "f"(y[0].y), "f"(y[1].x), "f"(y[1].y), "f"(y[2].x), "f"(y[2].y), "f"(y[3].x), "f"(y[3].y));
+  return r;
+}
+
 }  // namespace dsv4sa

@@ -274,20 +274,6 @@ __global__ void __launch_bounds__(kThreads) fp4_key_write_kernel(const WriterPar
 // nearly as busy (68%).
 constexpr int kRowsW = 2;
 
-// Eight values -> eight codes, nearest, ties to even, saturating (as e2m1_code counts out).
-__device__ __forceinline__ uint32_t e2m1x8(const float2* y) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r)
-      : "f"(y[0].x), "f"(y[0].y), "f"(y[1].x), "f"(y[1].y), "f"(y[2].x), "f"(y[2].y), "f"(y[3].x), "f"(y[3].y));
-  return r;
-}
-
 // The codes and the exponent byte of a unit whose block is lanes c, c ^ 1, c ^ 2, c ^ 3.
 // The block's absmax is a maximum of BF16 pairs (NaN wins).
 __device__ __forceinline__ uint32_t quantise_unit(const uint4 v, uint32_t& exponent) {

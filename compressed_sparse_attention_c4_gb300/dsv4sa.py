@@ -32,6 +32,8 @@ POOL_KV_FP4 = 3
 MAX_POOLS = 4
 ATTN_DECODE = 0
 ATTN_PREFILL = 1
+ROPE_PAIRS = 0     # pairs (2i, 2i + 1)
+ROPE_HALVES = 1    # pairs (i, i + half)
 PAGE = 64
 HEAD_DIM = 512
 
@@ -79,6 +81,37 @@ class CacheDesc(ctypes.Structure):
                 ("use", ctypes.c_void_p)]
 
 
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_tok_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_tok_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("dim", ctypes.c_int32), ("rope_off", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("rope_rows", ctypes.c_int32), ("rope_cs", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("norm_w", ctypes.c_void_p)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("pool", ctypes.POINTER(PoolDesc)), ("page_table", ctypes.c_void_p), ("pt_stride", ctypes.c_int32),
+                ("ring", ctypes.c_int32), ("row_seq", ctypes.c_void_p), ("row_pos", ctypes.c_void_p),
+                ("row_entry", ctypes.c_void_p), ("src_row", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("row_stride", ctypes.c_int64), ("n_src", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("rope_cs", ctypes.c_void_p), ("rope_rows", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("norm_w", ctypes.c_void_p), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class TreeArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("n_seqs", ctypes.c_int32), ("attn_sink", ctypes.c_void_p), ("node_start", ctypes.c_void_p),
+                ("seq_row", ctypes.c_void_p), ("ctx", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("anc", ctypes.c_void_p),
+                ("n_vis", ctypes.c_void_p), ("n_max", ctypes.c_int32), ("max_nodes", ctypes.c_int32),
+                ("comp", ctypes.POINTER(PoolDesc)), ("comp_pt", ctypes.c_void_p), ("win", ctypes.POINTER(PoolDesc)),
+                ("win_pt", ctypes.c_void_p), ("comp_pt_stride", ctypes.c_int32), ("win_pt_stride", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("win_ring", ctypes.c_int32), ("draft_entry", ctypes.c_int32),
+                ("rope_rows", ctypes.c_int32), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("rope_cs", ctypes.c_void_p), ("rope_pos", ctypes.c_void_p), ("ws", ctypes.c_void_p),
+                ("ws_bytes", ctypes.c_size_t)]
+
+
 class StepDesc(ctypes.Structure):
     _fields_ = [("host_in", ctypes.c_void_p), ("dev_in", ctypes.c_void_p), ("in_bytes", ctypes.c_size_t),
                 ("in_split", ctypes.c_size_t), ("kpool", ctypes.POINTER(PoolDesc)), ("page_table", ctypes.c_void_p),
@@ -120,6 +153,13 @@ _SIGS = {
     "dsv4sa_cache_compact": ([ctypes.POINTER(CacheDesc), ctypes.POINTER(CacheDesc), _P, _P, _P], ctypes.c_int),
     "dsv4sa_rmsnorm_quant": ([_P, _I64, _P, _I64, _P, ctypes.c_float, _I32, _I32, _I32, _P, _P, _P, _P, _P],
                              ctypes.c_int),
+    "dsv4sa_rope_table": ([_P, _I64, _I32, _I64, ctypes.c_double, ctypes.c_double, _I64, ctypes.c_double, ctypes.c_double,
+                           _P], ctypes.c_int),
+    "dsv4sa_rope": ([ctypes.POINTER(RopeArgs), _P], ctypes.c_int),
+    "dsv4sa_cache_append": ([ctypes.POINTER(AppendArgs), _P], ctypes.c_int),
+    "dsv4sa_tree_attn_workspace_size": ([_I32, _I32, _I32, _I32, _I32], _SZ),
+    "dsv4sa_tree_attn": ([ctypes.POINTER(TreeArgs), _P], ctypes.c_int),
+    "dsv4sa_tree_window_indices": ([_P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P], ctypes.c_int),
     "dsv4sa_compress_indices": ([_P, _I32, _I32, _P, _I32, _P], ctypes.c_int),
     "dsv4sa_selftest_wait_timeout": ([_P, _P], ctypes.c_int),
     "dsv4sa_copy_async": ([_P, _P, _SZ, _P], ctypes.c_int),
@@ -167,6 +207,7 @@ def _check(fn, status):
 
 # a small call is bound by the host: names of this module instead of attributes of torch
 _Tensor, _int32, _bf16, _f32, _u8 = torch.Tensor, torch.int32, torch.bfloat16, torch.float32, torch.uint8
+_int64 = torch.int64
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -601,6 +642,106 @@ def dsv4sa_rmsnorm_quant(x, norm_w, codes=None, scale=None, group: int = 128, re
         raise DSV4SAError("dsv4sa_rmsnorm_quant", st)
 
 
+# ---------------------------------------------------------------- rotary positions
+
+def dsv4sa_rope_table(cs, base: float = 10000.0, first: int = 0, factor: float = 1.0, original_len: int = 0,
+                      beta_fast: float = 32.0, beta_slow: float = 1.0, stream=None):
+    """The rotation table cs fp32 [rows, pairs, 2]: (cos, sin) of positions first, first + 1, ...
+    (first plus a table of 32 pairs is what the attention, the compressor and cache_append
+    take as rope_cs); factor > 1 scales the context, by YaRN with original_len > 0."""
+    if cs.dim() != 3 or cs.shape[2] != 2:
+        raise ValueError("cs must be [rows, pairs, 2]")
+    here = _here()
+    _check("dsv4sa_rope_table", lib().dsv4sa_rope_table(
+        _dev(cs, "cs", _f32, here), cs.shape[0], cs.shape[1], first, base, factor, original_len, beta_fast, beta_slow,
+        _stream(stream, here)))
+
+
+def _heads(t: torch.Tensor, name: str, shape, here):
+    """A BF16 tensor [T, H, dim] on the current CUDA device, tokens and heads strided -> (pointer, strides)."""
+    if t.get_device() != here:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        _refuse_device(name, t.get_device())
+    if t.dtype is not _bf16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    tok, head, col = t.stride()
+    if col != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must have consecutive values in a head")
+    return t.data_ptr(), tok, head
+
+
+def _table_of(rope_cs, pairs, here):
+    if rope_cs.dim() != 3 or rope_cs.shape[2] != 2 or (pairs and rope_cs.shape[1] != pairs):
+        raise ValueError(f"rope_cs must be [rows, {pairs or 'pairs'}, 2]")
+    return _dev(rope_cs, "rope_cs", _f32, here)
+
+
+def dsv4sa_rope(x, rope_cs, pos, out=None, rope_off=None, layout: int = ROPE_PAIRS, inverse: bool = False, eps=None,
+                norm_w=None, stream=None):
+    """Heads x bf16 [T, H, dim] (tokens and heads may be strided) with dims rope_off .. rope_off +
+    2 pairs (the last ones by default) rotated by rows pos int32 [T] of rope_cs [rows, pairs, 2],
+    into out, or in place.  With eps each head is divided by its root mean square first, and
+    multiplied by norm_w fp32 [dim] if given (see dsv4sa.h)."""
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError("x must be [T, H, dim]")
+    T, H, dim = shape
+    here = _here()
+    xp, xt, xh = _heads(x, "x", shape, here)
+    op, ot, oh = (xp, xt, xh) if out is None else _heads(out, "out", shape, here)
+    cs = _table_of(rope_cs, None, here)
+    rope_dim = 2 * rope_cs.shape[1]
+    if pos.numel() < T:
+        raise ValueError(f"pos must have an entry for each of the {T} tokens")
+    wp = None
+    if norm_w is not None:
+        if eps is None or norm_w.shape != (dim,):
+            raise ValueError("norm_w must be [dim], with eps")
+        wp = _dev(norm_w, "norm_w", _f32, here)
+    a = RopeArgs(xp, xt, xh, op, ot, oh, T, H, dim, dim - rope_dim if rope_off is None else rope_off, rope_dim, layout,
+                 1 if inverse else 0, rope_cs.shape[0], cs, _dev(pos, "pos", _int32, here), 0 if eps is None else 1, eps or 0.0, wp)
+    st = lib().dsv4sa_rope(ctypes.byref(a), _stream(stream, here))
+    if st:
+        raise DSV4SAError("dsv4sa_rope", st)
+
+
+def dsv4sa_cache_append(pool: PoolDesc, page_table, row_seq, row_pos, rows, rope_cs=None, row_entry=None, ring: int = 0,
+                        src_row=None, norm_w=None, eps=None, stream=None):
+    """New rows bf16 [n_src, 512] (rows may be strided) of the KV projection into a KV or KV_FP4 pool:
+    normed where eps is given (times norm_w fp32 [512] if given), the last 64 dims rotated by row
+    row_pos[r] of rope_cs [rows, 32, 2] where it is given, quantised.  Row r is rows[src_row[r]] or
+    rows[r]; it goes to entry row_entry[r], or by its position (modulo ring > 0), of page-table row
+    row_seq[r] (-1: skipped).  row_seq's length is the number of rows (all lists int32)."""
+    n = row_seq.shape[0]
+    shape = rows.shape
+    if len(shape) != 2 or shape[1] != HEAD_DIM:
+        raise ValueError("rows must be [n, 512]")
+    if src_row is None and shape[0] < n:
+        raise ValueError(f"rows must have one row for each of the {n} entries of row_seq")
+    here = _here()
+    rp, rs = _bf16_rows(rows, "rows", shape, here)
+    lists = []
+    for t, name in ((row_pos, "row_pos"), (row_entry, "row_entry"), (src_row, "src_row")):
+        if t is not None and t.numel() < n:
+            raise ValueError(f"{name} must have an entry for each of the {n} rows")
+        lists.append(None if t is None else _dev(t, name, _int32, here))
+    cs = None if rope_cs is None else _table_of(rope_cs, 32, here)
+    wp = None
+    if norm_w is not None:
+        if eps is None or norm_w.shape != (HEAD_DIM,):
+            raise ValueError("norm_w must be [512], with eps")
+        wp = _dev(norm_w, "norm_w", _f32, here)
+    a = AppendArgs(ctypes.pointer(_pool(pool, "pool", here)), _dev(page_table, "page_table", _int32, here), page_table.shape[-1],
+                   ring, _dev(row_seq, "row_seq", _int32, here), lists[0], lists[1], lists[2], rp, rs, shape[0], n, cs,
+                   0 if rope_cs is None else rope_cs.shape[0], 0 if eps is None else 1, wp, eps or 0.0, 0)
+    st = lib().dsv4sa_cache_append(ctypes.byref(a), _stream(stream, here))
+    if st:
+        raise DSV4SAError("dsv4sa_cache_append", st)
+
+
 def dsv4sa_compress_windows(kv, score, first_tok, prev_tok, position, ratio: int, overlap: bool, ape, norm_w,
                             rope_cs, out, eps: float = 1e-6, stream=None):
     """Pool windows of projected tokens into compressed entries (see dsv4sa.h).
@@ -774,6 +915,83 @@ def dsv4sa_sparse_attn_prefill(q, sink, q_seq, comp, comp_pt, idx_c, win, win_pt
     a = _attn_args(q, sink, q_seq, comp, comp_pt, idx_c, win, win_pt, idx_w, out, softmax_scale, lse, ws,
                    win_pos, kw, win_ring, flags, rope_cs, rope_pos)
     _check("dsv4sa_sparse_attn_prefill", lib().dsv4sa_sparse_attn_prefill(ctypes.byref(a), _stream(stream)))
+
+
+# ---------------------------------------------------------------- drafted tokens
+
+def _nodes(node_start, ctx, pos, anc, T, here):
+    """Addresses of a batch of trees' lists: first nodes [B + 1], committed tokens [B], positions and ancestors [T]."""
+    if ctx.numel() < node_start.numel() - 1:
+        raise ValueError("ctx must have an entry for each sequence")
+    if pos.numel() < T or (anc is not None and anc.numel() < T):
+        raise ValueError(f"pos and anc must have an entry for each of the {T} nodes")
+    return (_dev(node_start, "node_start", _int32, here), _dev(ctx, "ctx", _int32, here), _dev(pos, "pos", _int32, here),
+            None if anc is None else _dev(anc, "anc", _int64, here))
+
+
+def dsv4sa_tree_attn_workspace_size(n_seqs: int, max_nodes: int, H: int, n_max: int, window: int) -> int:
+    return int(lib().dsv4sa_tree_attn_workspace_size(n_seqs, max_nodes, H, n_max, window))
+
+
+def dsv4sa_tree_attn(q, sink, node_start, ctx, pos, comp, comp_pt, n_vis, n_max: int, win, win_pt, window: int, out,
+                     softmax_scale, max_nodes: int, seq_row=None, anc=None, win_ring: int = 0, draft_entry: int = -1, lse=None,
+                     ws=None, stream=None, rope_cs=None, rope_pos=None):
+    """Attention of drafted tokens: q bf16 [T, H, 512], sequence b's being rows node_start[b] ..
+    node_start[b + 1] - 1 (int32 [B + 1]), over compressed entries below n_vis [T], the window of
+    committed tokens (positions below ctx [B]) and the drafted rows that the bits of anc (int64 [T];
+    None: a chain) name, at draft_entry + j of the window pool (see dsv4sa.h).  comp with n_max 0,
+    and win with window 0 and no draft_entry, may be None.  rope_cs, rope_pos: as in the sparse attention."""
+    T, H, dim = q.shape
+    if dim != HEAD_DIM:
+        raise ValueError("q must be [T, H, 512]")
+    if out.shape != q.shape or sink.numel() < H or n_vis.numel() < T or (lse is not None and lse.numel() < T * H):
+        raise ValueError(f"out, attn_sink, n_vis or lse does not fit {T} queries of {H} heads")
+    here = _here()
+    B = node_start.numel() - 1
+    ns, cx, ps, an = _nodes(node_start, ctx, pos, anc, T, here)
+    rows = None
+    if seq_row is not None:
+        if seq_row.numel() < B:
+            raise ValueError("seq_row must have an entry for each sequence")
+        rows = _dev(seq_row, "seq_row", _int32, here)
+    cd = cpt = wd = wpt = rcs = rpos = None
+    cpt_stride = wpt_stride = rope_rows = 0
+    if comp is not None:
+        cd = ctypes.pointer(_pool(comp, "comp", here))
+        cpt = _dev(comp_pt, "comp_pt", _int32, here)
+        cpt_stride = comp_pt.shape[-1]
+    if win is not None:
+        wd = ctypes.pointer(_pool(win, "win", here))
+        wpt = _dev(win_pt, "win_pt", _int32, here)
+        wpt_stride = win_pt.shape[-1]
+    if rope_cs is not None:
+        rcs = _table_of(rope_cs, 32, here)
+        rpos = _dev(rope_pos, "rope_pos", _int32, here)
+        if rope_pos.numel() < T:
+            raise ValueError(f"rope_pos must have an entry for each of the {T} queries")
+        rope_rows = rope_cs.shape[0]
+    a = TreeArgs(_dev(q, "q", _bf16, here), T, H, float(softmax_scale), B, _dev(sink, "attn_sink", _f32, here), ns, rows, cx, ps, an,
+                 _dev(n_vis, "n_vis", _int32, here), n_max, max_nodes, cd, cpt, wd, wpt, cpt_stride, wpt_stride, window, win_ring,
+                 draft_entry, rope_rows, _dev(out, "out", _bf16, here), _dev(lse, "lse", _f32, here) if lse is not None else None,
+                 rcs, rpos, _dev(ws, "ws", _u8, here) if ws is not None else None, ws.numel() if ws is not None else 0)
+    st = lib().dsv4sa_tree_attn(ctypes.byref(a), _stream(stream, here))
+    if st:
+        raise DSV4SAError("dsv4sa_tree_attn", st)
+
+
+def dsv4sa_tree_window_indices(node_start, ctx, pos, window: int, ring: int, draft_entry: int, max_nodes: int, idx_w, anc=None,
+                               stream=None):
+    """The window list of each drafted token for the sparse attention: idx_w int32 [T, window +
+    max_nodes] (committed positions, then drafted rows; -1: none), as dsv4sa_tree_attn sees them."""
+    if idx_w.dim() != 2:
+        raise ValueError("idx_w must be [T, window + max_nodes]")
+    T = idx_w.shape[0]
+    here = _here()
+    ns, cx, ps, an = _nodes(node_start, ctx, pos, anc, T, here)
+    st = lib().dsv4sa_tree_window_indices(ns, cx, ps, an, node_start.numel() - 1, T, max_nodes, window, ring, draft_entry,
+                                          _dev(idx_w, "idx_w", _int32, here), idx_w.shape[1], _stream(stream, here))
+    if st:
+        raise DSV4SAError("dsv4sa_tree_window_indices", st)
 
 
 def dsv4sa_check_errors(stream=None) -> tuple[int, int]:

@@ -63,6 +63,9 @@ extern "C" {
 #define DSV4SA_MAX_TOPK    2048
 #define DSV4SA_MAX_POOLS   4    /* pools of one cache (dsv4sa_cache_desc)           */
 #define DSV4SA_MAX_NORM_DIM 16384
+#define DSV4SA_MAX_ROPE_PAIRS 256
+#define DSV4SA_MAX_TREE_NODES 64 /* drafted tokens of a sequence                        */
+#define DSV4SA_MAX_TREE_WINDOW 65536
 
 typedef enum {
   DSV4SA_OK = 0,
@@ -588,6 +591,171 @@ DSV4SA_API int dsv4sa_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_c
 DSV4SA_API int dsv4sa_rmsnorm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                                     const float* norm_w, float eps, int32_t n, int32_t dim, int32_t group,
                                     void* residual_out, void* y, uint8_t* codes, float* scale, cudaStream_t stream);
+
+/*
+ * Rotary positions: the table ([V4] §2.6 precompute_freqs_cis).  Row r, pair i of
+ * cs is (cos, sin) of (first + r) * w_i, with w_i = base^(-i / pairs) and, where
+ * the context is scaled (factor > 1):
+ *   original_len = 0   w_i / factor (interpolated positions)
+ *   original_len > 0   YaRN: w_i / factor * (1 - keep_i) + w_i * keep_i, keep_i =
+ *                      1 - clamp((i - lo) / (hi - lo), 0, 1), lo = max(floor(at(beta_fast)), 0),
+ *                      hi = min(ceil(at(beta_slow)), 2 pairs - 1), at(beta) = 2 pairs *
+ *                      ln(original_len / (2 pi beta)) / (2 ln base)
+ * What the attention, the compressor, dsv4sa_rope and dsv4sa_cache_append take as
+ * rope_cs (those of 512 dims with pairs = 32).  Frequencies are fp64; an angle is
+ * reduced to a part of a turn without rounding (64 bits), then rounded to fp32
+ * once, so far positions are as exact as near ones.
+ *   cs      device fp32 [rows][pairs][2], 8-byte aligned
+ *   pairs   1..DSV4SA_MAX_ROPE_PAIRS;  base > 1;  factor >= 1;  first >= 0
+ */
+DSV4SA_API int dsv4sa_rope_table(float* cs, int64_t rows, int32_t pairs, int64_t first, double base, double factor,
+                                 int64_t original_len, double beta_fast, double beta_slow, cudaStream_t stream);
+
+/*
+ * Rotary positions: heads rotated ([V4] §2.6 apply_rotary_emb, §2.11: queries are
+ * normed per head, then the last 64 dims rotated).  For token t and head h:
+ *   y = x[t, h],  or with norm: y = x / sqrt(mean(x^2) + eps) (* norm_w), in fp32
+ *   out[t, h] = y with dims [rope_off, rope_off + rope_dim) rotated by row pos[t]
+ *               of rope_cs, rounded to BF16 once:
+ *   pair i is (a, b) = dims (2i, 2i + 1) of that part (DSV4SA_ROPE_PAIRS) or dims
+ *   (i, i + rope_dim / 2) (DSV4SA_ROPE_HALVES);  (a, b) -> (a c - b s, b c + a s),
+ *   with inverse = 1 by the conjugate, which is also the gradient of the rotation.
+ * A position outside [0, rope_rows) sets DSV4SA_ERR_INDEX_OOB on the device; that
+ * token's heads are written unrotated.  Without norm the other dims are copied; in
+ * place they are not touched.  With norm: rows of infinities, NaN, squares that
+ * leave the fp32 range or only zeros with eps = 0 have no defined result.
+ */
+#define DSV4SA_ROPE_PAIRS 0
+#define DSV4SA_ROPE_HALVES 1
+typedef struct {
+  const void*  x;              /* bf16, 16-byte aligned; strides in values, multiples of 8 */
+  int64_t      x_tok_stride;
+  int64_t      x_head_stride;
+  void*        out;            /* bf16; x itself with x's strides (in place), or apart from it */
+  int64_t      out_tok_stride; /* rows of dim values that do not overlap */
+  int64_t      out_head_stride;
+  int32_t      T, H;           /* tokens, heads; T * H < 2^30 */
+  int32_t      dim;            /* of a head: a multiple of 8, <= 1024 */
+  int32_t      rope_off;       /* a multiple of 8 */
+  int32_t      rope_dim;       /* a multiple of 16, <= 2 * DSV4SA_MAX_ROPE_PAIRS */
+  int32_t      layout;         /* DSV4SA_ROPE_PAIRS, DSV4SA_ROPE_HALVES */
+  int32_t      inverse;        /* 0, 1 */
+  int32_t      rope_rows;
+  const float* rope_cs;        /* device fp32 [rope_rows][rope_dim / 2][2], 16-byte aligned */
+  const int32_t* pos;          /* device int32 [T] */
+  int32_t      norm;           /* 0, 1 */
+  float        eps;
+  const float* norm_w;         /* optional device fp32 [dim], 16-byte aligned */
+} dsv4sa_rope_args;
+DSV4SA_API int dsv4sa_rope(const dsv4sa_rope_args* args, cudaStream_t stream);
+
+/*
+ * New rows of the KV projection into a pool, normed and rotated on the way ([V4]
+ * §2.11: kv_norm, apply_rotary_emb, act_quant of the nope part; [SGL] 概念5).
+ * Row r, r < n, is x = rows[src_row ? src_row[r] : r] and becomes, in fp32:
+ *   y = x,  or with norm: x / sqrt(mean(x^2) + eps) (* norm_w)
+ *   dims 448..511 of y rotated as 32 pairs (448 + 2i, 449 + 2i) by row row_pos[r] of
+ *   rope_cs and rounded to BF16 (rope_cs null: not rotated)
+ *   dims 0..447 quantised as dsv4sa_cache_write does (without norm bit for bit so)
+ * It goes to entry row_entry[r] of the sequence of page-table row row_seq[r]; row_entry
+ * null: row_pos[r] % ring with ring > 0 (a ring of raw tokens), else row_pos[r].
+ * Rows with row_seq[r] = -1 are skipped (padding of a batch).  A row whose source, slot,
+ * page id or position (of rope_cs) is out of range is skipped and sets DSV4SA_ERR_INDEX_OOB
+ * on the device.  Rows that write the same slot in one call race.  Norms as in dsv4sa_rope.
+ */
+typedef struct {
+  const dsv4sa_pool_desc* pool;   /* KV or KV_FP4 */
+  const int32_t* page_table;      /* device int32 [rows][pt_stride] */
+  int32_t      pt_stride;
+  int32_t      ring;
+  const int32_t* row_seq;         /* device int32 [n] */
+  const int32_t* row_pos;         /* device int32 [n]; may be null with row_entry and without rope_cs */
+  const int32_t* row_entry;       /* device int32 [n], or null */
+  const int32_t* src_row;         /* device int32 [n], or null (then n_src >= n) */
+  const void*  rows;              /* device bf16 [n_src] rows of 512, 16-byte aligned, apart from the pool */
+  int64_t      row_stride;        /* values between rows, a multiple of 8 */
+  int32_t      n_src;
+  int32_t      n;
+  const float* rope_cs;           /* device fp32 [rope_rows][32][2], 16-byte aligned, or null */
+  int32_t      rope_rows;
+  int32_t      norm;              /* 0, 1 */
+  const float* norm_w;            /* optional device fp32 [512], 16-byte aligned */
+  float        eps;
+  int32_t      reserved;
+} dsv4sa_append_args;
+DSV4SA_API int dsv4sa_cache_append(const dsv4sa_append_args* args, cudaStream_t stream);
+
+/*
+ * Attention of drafted tokens over every entry they see ([V4] §2.8
+ * get_compress_topk_idxs, §2.11, §3.7 sparse_attn_kernel: layers without an indexer;
+ * one drafted token a sequence is plain decode of such a layer, to any length).
+ * Sequence b has the drafted tokens (nodes) t = node_start[b] .. node_start[b + 1] - 1,
+ * node j of it being t = node_start[b] + j.  Node t attends, as dsv4sa_sparse_attn_decode
+ * does, to
+ *   entries e < n_vis[t] of the compressed pool (clamped to [0, n_max]),
+ *   committed raw tokens p with pos[t] - window < p <= pos[t] and p < ctx[b]: entry p of
+ *     the window pool, p % win_ring with win_ring > 0,
+ *   drafted rows j of its sequence where bit j of anc[t] is set (its ancestors and itself;
+ *     bits at and above the sequence's nodes count nothing): entry draft_entry + j of the
+ *     window pool, where dsv4sa_cache_append put them.  anc null: a chain, bits 0..j;
+ *     draft_entry -1: no drafted rows.
+ * A node without any row gets zeros (lse: the sink).  q, out and lse rows outside every
+ * sequence are neither read nor written.  A sequence whose bounds do not lie within
+ * [0, T] or hold more than max_nodes nodes is left out, and a page id or entry out of range
+ * takes out its row; both set DSV4SA_ERR_INDEX_OOB on the device.  A row that holds an
+ * infinity or a NaN makes NaN of the nodes that see it, and of no other.
+ * The pools are two of kind KV or two of kind KV_FP4 (one of each: UNSUPPORTED).  Sums and
+ * partial results are fp32, P is rounded to BF16.  The lengths of the whole batch
+ * decide how the rows are split, so a node's bits may differ between batches; they are the
+ * same for the same batch on the same device.
+ */
+typedef struct {
+  const void*  q;               /* device bf16 [T][H][512], 16-byte aligned */
+  int32_t      T;
+  int32_t      H;               /* 1..128 */
+  float        softmax_scale;
+  int32_t      n_seqs;
+  const float* attn_sink;       /* device fp32 [H] */
+  const int32_t* node_start;    /* device int32 [n_seqs + 1] */
+  const int32_t* seq_row;       /* device int32 [n_seqs]: page-table row (of both tables); null: b */
+  const int32_t* ctx;           /* device int32 [n_seqs]: committed tokens */
+  const int32_t* pos;           /* device int32 [T] */
+  const uint64_t* anc;          /* device uint64 [T], or null */
+  const int32_t* n_vis;         /* device int32 [T] */
+  int32_t      n_max;           /* <= comp_pt_stride * 64; 0: no compressed entries */
+  int32_t      max_nodes;       /* nodes of a sequence at most, <= DSV4SA_MAX_TREE_NODES */
+  const dsv4sa_pool_desc* comp; /* may be null when n_max == 0 */
+  const int32_t* comp_pt;       /* device int32 [rows][comp_pt_stride] */
+  const dsv4sa_pool_desc* win;  /* may be null when window == 0 and draft_entry == -1 */
+  const int32_t* win_pt;        /* device int32 [rows][win_pt_stride] */
+  int32_t      comp_pt_stride;
+  int32_t      win_pt_stride;
+  int32_t      window;          /* 0..DSV4SA_MAX_TREE_WINDOW */
+  int32_t      win_ring;
+  int32_t      draft_entry;
+  int32_t      rope_rows;
+  void*        out;             /* device bf16 [T][H][512], apart from q */
+  float*       lse;             /* optional device fp32 [T][H] */
+  const float* rope_cs;         /* optional: inverse rotation of the output as in dsv4sa_attn_args, */
+  const int32_t* rope_pos;      /* by row rope_pos[t] */
+  void*        ws;              /* device workspace, 16-byte aligned; calls that share one are ordered by the caller */
+  size_t       ws_bytes;
+} dsv4sa_tree_args;
+/* Workspace bytes of a call with these arguments: an upper bound over devices, 42 MB at most. */
+DSV4SA_API size_t dsv4sa_tree_attn_workspace_size(int32_t n_seqs, int32_t max_nodes, int32_t H, int32_t n_max, int32_t window);
+DSV4SA_API int dsv4sa_tree_attn(const dsv4sa_tree_args* args, cudaStream_t stream);
+
+/*
+ * The same nodes' window as a list for dsv4sa_sparse_attn_* (layers whose indexer
+ * selects entries): idx_w[t][j], j < window, is the entry of committed position
+ * pos[t] - window + 1 + j, -1 outside [0, ctx[b]); idx_w[t][window + j], j < max_nodes,
+ * is draft_entry + j for the drafted rows node t sees, else -1.  Rows outside every
+ * sequence are left as they are.  Other arguments and errors as dsv4sa_tree_attn.
+ *   idx_w   device int32 [T][idx_stride], idx_stride >= window + max_nodes
+ */
+DSV4SA_API int dsv4sa_tree_window_indices(const int32_t* node_start, const int32_t* ctx, const int32_t* pos, const uint64_t* anc,
+                                          int32_t n_seqs, int32_t T, int32_t max_nodes, int32_t window, int32_t ring,
+                                          int32_t draft_entry, int32_t* idx_w, int64_t idx_stride, cudaStream_t stream);
 
 /*
  * The compressor's rotate path into an FP4 key pool ("DeepSeek-V4 全面解读"

@@ -876,3 +876,77 @@ def cache_compact_ids(use, in_place: bool) -> np.ndarray:
     holes = [i for i in range(used.size) if use[i] == 0]
     new_id[used[used >= used.size]] = holes
     return new_id
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def yarn_freqs(pairs: int, base: float, factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0,
+               beta_slow: float = 1.0) -> np.ndarray:
+    """Steps 1-2 of P1 §2.6 precompute_freqs_cis: base^(-i / pairs), and in a scaled
+    context divided by `factor` -- all of them (original_len 0), or those that turn
+    less than beta_slow times over original_len tokens, with a ramp (over the pair
+    numbers, between the floor and the ceiling of the two borders) to those that turn
+    more than beta_fast times."""
+    i = np.arange(pairs, dtype=np.float64)
+    w = float(base) ** (-i / pairs)
+    if factor == 1.0:
+        return w
+    if original_len == 0:
+        return w / factor
+    # pair i turns original_len * w_i / (2 pi) times; the border of beta turns, as a pair number
+    border = [pairs * np.log(original_len / (2 * np.pi * b)) / np.log(base) for b in (beta_fast, beta_slow)]
+    lo, hi = max(np.floor(border[0]), 0.0), min(np.ceil(border[1]), 2 * pairs - 1.0)
+    ramp = np.clip((i - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
+    return w * (1 - ramp) + w / factor * ramp
+
+
+def rotate_heads(x, table_rows, off: int, halves: bool, inverse: bool = False) -> np.ndarray:
+    """Dims [off, off + 2 n) of x [..., dim] as n complex pairs -- (2i, 2i + 1), or
+    (i, i + n) with `halves` -- times table_rows [..., n] (complex), or its conjugate
+    (P1 §2.6 apply_rotary_emb)."""
+    x = np.array(x, np.float64, copy=True)
+    n = table_rows.shape[-1]
+    a = np.arange(n) + off if halves else 2 * np.arange(n) + off
+    b = a + n if halves else a + 1
+    z = (x[..., a] + 1j * x[..., b]) * (np.conj(table_rows) if inverse else table_rows)
+    x[..., a], x[..., b] = z.real, z.imag
+    return x
+
+
+def append_row(x_bf16_bits, table_row, weight=None, eps=None) -> np.ndarray:
+    """A row of the KV projection as it enters the cache, before it is quantised: normed
+    where eps is given, its last 64 dims rotated where a table row is (P1 §2.11)."""
+    y = bf16_decode(x_bf16_bits)
+    if eps is not None:
+        y = rms_norm(y, 1.0 if weight is None else weight, eps)
+    return y if table_row is None else rotate_heads(y, np.asarray(table_row), NOPE, False)
+
+
+# ---------------------------------------------------------------- drafted tokens
+
+def tree_masks(parent) -> list:
+    """Bit j of mask i: node j is node i or one of its ancestors (parent -1: none)."""
+    out = []
+    for i, p in enumerate(parent):
+        out.append((out[p] if p >= 0 else 0) | 1 << i)
+    return out
+
+
+def tree_window(pos: int, ctx: int, window: int, ring: int, mask: int, nodes: int, draft_entry: int) -> tuple:
+    """Entries of the window pool that a drafted token sees: the slots of committed
+    positions pos - window + 1 .. pos below ctx (-1 where there is none), and those of the
+    drafted rows of its mask (P1 §2.8 get_window_topk_idxs with the drafted rows apart)."""
+    p = np.arange(pos - window + 1, pos + 1, dtype=np.int64)
+    win = np.where((p >= 0) & (p < ctx), p % ring if ring > 0 else p, -1)
+    j = np.arange(nodes)
+    seen = np.array([draft_entry >= 0 and bool(mask >> int(i) & 1) for i in j], bool)
+    return win, np.where(seen, draft_entry + j, -1)
+
+
+def attend_lse(q, rows, sink, softmax_scale) -> np.ndarray:
+    """ln(sum_j e^{a_hj} + e^{sink_h}) of sink_softmax_attention."""
+    a = np.concatenate([softmax_scale * (np.asarray(q, np.float64) @ np.asarray(rows, np.float64).reshape(-1, HEAD_DIM).T),
+                        np.asarray(sink, np.float64)[:, None]], axis=1)
+    m = a.max(axis=1)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        return np.where(np.isneginf(m), m, m + np.log(np.exp(a - np.where(np.isneginf(m), 0, m)[:, None]).sum(axis=1)))
