@@ -39,6 +39,7 @@ struct AppendParams {
   int32_t ring;
   int32_t n, n_src;
   int32_t rope_rows;
+  int32_t per;                // rows of a warp's batch
   float eps;
 };
 
@@ -79,117 +80,167 @@ __device__ __forceinline__ uint2 e4m3x8(const float2 (&y)[4], float scale, bool 
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
+// A warp takes `per` consecutive rows.  Lane l looks up row l's slot -- one chain of dependent
+// loads for all of them -- and the rows themselves come through shared memory, kStages of them
+// on the way at a time: each lane copies, and later reads, its own 16-byte units, so nothing
+// has to be waited for but the copy.
+constexpr int kStages = 4;
+constexpr int kMaxRows = 16;             // of a warp's batch
+constexpr int kStageBytes = 1024 + 256;  // the row, and its rotation
+
+__device__ __forceinline__ void copy16(uint8_t* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <bool kFp4, bool kNorm>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendParams p) {
   // default page layouts (see dsv4sa.h)
   constexpr int kNopeRow = kFp4 ? 224 : 448, kRopeOff = 64 * kNopeRow, kScaleOff = kRopeOff + 64 * 128;
+  __shared__ __align__(16) uint8_t ring[kThreads / 32][kStages][kStageBytes];
   griddep_launch();
   griddep_wait();
-  const int c = static_cast<int>(threadIdx.x & 31u);
+  const int c = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
   const bool rope_lane = c >= 24;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5; r < p.n; r += step) {   // warp-uniform
-    const int seq = __ldg(p.row_seq + r);
-    const int pos = p.row_pos ? __ldg(p.row_pos + r) : 0;
-    const int64_t src = p.src_row ? __ldg(p.src_row + r) : r;
-    const bool have = src >= 0 && src < p.n_src;
-    const uint4* from = p.rows + (have ? src : 0) * p.row_stride;
-    const uint4 v0 = __ldcs(from + c), v1 = __ldcs(from + 32 + c);
-    const int e = p.row_entry ? __ldg(p.row_entry + r) : (p.ring > 0 && pos >= 0 ? pos % p.ring : pos);
-    bool ok = have && seq >= 0 && e >= 0 && (e >> 6) < p.pt_stride && (!p.cs || (pos >= 0 && pos < p.rope_rows));
-    const int page = __ldg(p.page_table + static_cast<int64_t>(ok ? seq : 0) * p.pt_stride + (ok ? e >> 6 : 0));
-    float4 z0 = make_float4(1.f, 0.f, 1.f, 0.f), z1 = z0;
-    if (p.cs && rope_lane && ok) {
-      const float4* row = p.cs + static_cast<int64_t>(pos) * 16 + 2 * (c - 24);
-      z0 = __ldg(row);
-      z1 = __ldg(row + 1);
-    }
-    ok = ok && page >= 0 && page < p.num_pages;
-    if (!ok) {
-      if (c == 0 && seq != -1) raise_error(kErrIndex);   // -1: padding of the batch
-      continue;
-    }
-    float2 y0[4], y1[4];
-    unpack8(v0, y0);
-    unpack8(v1, y1);
-    if constexpr (kNorm) {
-      float2 s2 = make_float2(0.f, 0.f);
+  float4 w[4];
+  if constexpr (kNorm) {
+    const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s2 = fma2(y1[i], y1[i], fma2(y0[i], y0[i], s2));
-      float sq = s2.x + s2.y;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-      const float rstd = rsqrtf(fmaf(sq, 1.0f / 512.0f, p.eps));
-      const float2 rstd2 = make_float2(rstd, rstd);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y0[i] = mul2(y0[i], rstd2);
-        y1[i] = mul2(y1[i], rstd2);
+    for (int i = 0; i < 4; ++i) w[i] = p.w ? __ldg(p.w + (i >> 1) * 64 + 2 * c + (i & 1)) : one;
+  }
+  for (int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp) * p.per; r0 < p.n;
+       r0 += static_cast<int64_t>(gridDim.x) * (kThreads / 32) * p.per) {   // warp-uniform
+    const int rows = static_cast<int>(min(static_cast<int64_t>(p.per), p.n - r0));
+    // ---- row r0 + lane: its source, position, page (-1: not written) and slot
+    int l_src = 0, l_pos = 0, l_page = -1, l_slot = 0;
+    if (c < rows) {
+      const int64_t r = r0 + c;
+      const int seq = __ldg(p.row_seq + r);
+      l_pos = p.row_pos ? __ldg(p.row_pos + r) : 0;
+      l_src = p.src_row ? __ldg(p.src_row + r) : static_cast<int>(r);
+      const int e = p.row_entry ? __ldg(p.row_entry + r) : (p.ring > 0 && l_pos >= 0 ? l_pos % p.ring : l_pos);
+      const bool ok = l_src >= 0 && l_src < p.n_src && seq >= 0 && e >= 0 && (e >> 6) < p.pt_stride &&
+                      (!p.cs || (l_pos >= 0 && l_pos < p.rope_rows));
+      if (ok) l_page = __ldg(p.page_table + static_cast<int64_t>(seq) * p.pt_stride + (e >> 6));
+      if (l_page < 0 || l_page >= p.num_pages) {
+        l_page = -1;
+        if (seq != -1) raise_error(kErrIndex);             // -1: padding of the batch
       }
-      if (p.w) {
-        const float4 a = __ldg(p.w + 2 * c), b = __ldg(p.w + 2 * c + 1), d = __ldg(p.w + 64 + 2 * c), g = __ldg(p.w + 64 + 2 * c + 1);
-        y0[0] = mul2(y0[0], make_float2(a.x, a.y)), y0[1] = mul2(y0[1], make_float2(a.z, a.w));
-        y0[2] = mul2(y0[2], make_float2(b.x, b.y)), y0[3] = mul2(y0[3], make_float2(b.z, b.w));
-        y1[0] = mul2(y1[0], make_float2(d.x, d.y)), y1[1] = mul2(y1[1], make_float2(d.z, d.w));
-        y1[2] = mul2(y1[2], make_float2(g.x, g.y)), y1[3] = mul2(y1[3], make_float2(g.z, g.w));
-      }
+      l_slot = e & 63;
     }
-    uint32_t m0 = top_of(y0), m1 = top_of(y1);               // m1 of lanes 24-31 is not used
-    m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, 1)), m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
-    m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, 2)), m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, 2));
-    if constexpr (!kFp4) m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, 4)), m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, 4));
-    const int slot = e & 63;
-    uint8_t* pg = p.base + static_cast<int64_t>(page) * p.page_stride;
-    uint8_t* nope = pg + slot * kNopeRow;
-    if constexpr (kFp4) {
-      uint8_t* sc = pg + kScaleOff + slot * 16;
-      auto put = [&](const float2 (&y)[4], uint32_t mag, int u) {
-        const bool finite = mag < 0x7F800000u;
-        // e = ceil(log2(fp32(max(amax, 6 * 2^-126) * fp32(1/6)))), off the fields of that product (a normal number)
-        const uint32_t t = __float_as_uint(__fmul_rn(fmaxf(finite ? __uint_as_float(mag) : 0.f, kFp4AmaxFloor), kFp4MaxInv));
-        const uint32_t b = (t >> 23) + ((t & 0x7FFFFFu) != 0u ? 1u : 0u);   // the E8M0 byte
-        const float inv = __uint_as_float((254u - b) << 23);
-        float2 z[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = mul2(y[i], make_float2(inv, inv));
-        reinterpret_cast<uint32_t*>(nope)[u] = finite ? e2m1x8(z) : 0u;
-        if ((c & 3) == 0) sc[u >> 2] = static_cast<uint8_t>(finite ? b : 255u);
-      };
-      put(y0, m0, c);
-      if (!rope_lane) put(y1, m1, 32 + c);
-    } else {
-      float* sc = reinterpret_cast<float*>(pg + kScaleOff + slot * 32);
-      auto put = [&](const float2 (&y)[4], uint32_t mag, int u) {
-        const float scale = __fmul_rn(fmaxf(__uint_as_float(mag), kAmaxFloor), kFp8MaxInv);
-        reinterpret_cast<uint2*>(nope)[u] = e4m3x8(y, scale, mag < 0x7F800000u);
-        if ((c & 7) == 0) sc[u >> 3] = scale;
-      };
-      put(y0, m0, c);
-      if (!rope_lane) put(y1, m1, 32 + c);
-    }
-    if (rope_lane) {
-      const float2 cs[4] = {{z0.x, z0.y}, {z0.z, z0.w}, {z1.x, z1.y}, {z1.z, z1.w}};
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 y = y1[i];
-        if (p.cs) y1[i] = make_float2(fmaf(y.x, cs[i].x, -(y.y * cs[i].y)), fmaf(y.y, cs[i].x, y.x * cs[i].y));
-        const __nv_bfloat162 v = __floats2bfloat162_rn(y1[i].x, y1[i].y);
-        o[i] = *reinterpret_cast<const uint32_t*>(&v);
+    auto fetch = [&](int i) {            // row r0 + i; an empty group past the last one
+      const int src = __shfl_sync(0xffffffffu, l_src, i & 31), pos = __shfl_sync(0xffffffffu, l_pos, i & 31);
+      const int page = __shfl_sync(0xffffffffu, l_page, i & 31);
+      if (i < rows && page >= 0) {
+        uint8_t* at = ring[warp][i % kStages];
+        const uint4* from = p.rows + src * p.row_stride + c;
+        copy16(at + c * 16, from);
+        copy16(at + 512 + c * 16, from + 32);
+        if (p.cs && rope_lane) {
+          const float4* cs = p.cs + static_cast<int64_t>(pos) * 16 + 2 * (c - 24);
+          copy16(at + 1024 + (c - 24) * 32, cs);
+          copy16(at + 1040 + (c - 24) * 32, cs + 1);
+        }
       }
-      // neither normed nor rotated: the input's bits
-      reinterpret_cast<uint4*>(pg + kRopeOff + slot * 128)[c - 24] = kNorm || p.cs ? make_uint4(o[0], o[1], o[2], o[3]) : v1;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) fetch(i);
+#pragma unroll 1
+    for (int i = 0; i < rows; ++i) {
+      fetch(i + kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      const int page = __shfl_sync(0xffffffffu, l_page, i), slot = __shfl_sync(0xffffffffu, l_slot, i);
+      if (page < 0) continue;            // the same in the whole warp
+      const uint8_t* at = ring[warp][i % kStages];
+      const uint4 v0 = *reinterpret_cast<const uint4*>(at + c * 16), v1 = *reinterpret_cast<const uint4*>(at + 512 + c * 16);
+      float2 y0[4], y1[4];
+      unpack8(v0, y0);
+      unpack8(v1, y1);
+      if constexpr (kNorm) {
+        float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s2 = fma2(y1[i], y1[i], fma2(y0[i], y0[i], s2));
+        float sq = s2.x + s2.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        const float rstd = rsqrtf(fmaf(sq, 1.0f / 512.0f, p.eps));
+        const float2 rstd2 = make_float2(rstd, rstd);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y0[i] = mul2(y0[i], rstd2);
+          y1[i] = mul2(y1[i], rstd2);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {      // weights of 1 where there are none
+          y0[2 * i] = mul2(y0[2 * i], make_float2(w[i].x, w[i].y)), y0[2 * i + 1] = mul2(y0[2 * i + 1], make_float2(w[i].z, w[i].w));
+          y1[2 * i] = mul2(y1[2 * i], make_float2(w[2 + i].x, w[2 + i].y)), y1[2 * i + 1] = mul2(y1[2 * i + 1], make_float2(w[2 + i].z, w[2 + i].w));
+        }
+      }
+      uint32_t m0 = top_of(y0), m1 = top_of(y1);               // m1 of lanes 24-31 is not used
+      m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, 1)), m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
+      m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, 2)), m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, 2));
+      if constexpr (!kFp4) m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, 4)), m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, 4));
+      uint8_t* pg = p.base + static_cast<int64_t>(page) * p.page_stride;
+      uint8_t* nope = pg + slot * kNopeRow;
+      if constexpr (kFp4) {
+        uint8_t* sc = pg + kScaleOff + slot * 16;
+        auto put = [&](const float2 (&y)[4], uint32_t mag, int u) {
+          const bool finite = mag < 0x7F800000u;
+          // e = ceil(log2(fp32(max(amax, 6 * 2^-126) * fp32(1/6)))), off the fields of that product (a normal number)
+          const uint32_t t = __float_as_uint(__fmul_rn(fmaxf(finite ? __uint_as_float(mag) : 0.f, kFp4AmaxFloor), kFp4MaxInv));
+          const uint32_t b = (t >> 23) + ((t & 0x7FFFFFu) != 0u ? 1u : 0u);   // the E8M0 byte
+          const float inv = __uint_as_float((254u - b) << 23);
+          float2 z[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = mul2(y[i], make_float2(inv, inv));
+          reinterpret_cast<uint32_t*>(nope)[u] = finite ? e2m1x8(z) : 0u;
+          if ((c & 3) == 0) sc[u >> 2] = static_cast<uint8_t>(finite ? b : 255u);
+        };
+        put(y0, m0, c);
+        if (!rope_lane) put(y1, m1, 32 + c);
+      } else {
+        float* sc = reinterpret_cast<float*>(pg + kScaleOff + slot * 32);
+        auto put = [&](const float2 (&y)[4], uint32_t mag, int u) {
+          const float scale = __fmul_rn(fmaxf(__uint_as_float(mag), kAmaxFloor), kFp8MaxInv);
+          reinterpret_cast<uint2*>(nope)[u] = e4m3x8(y, scale, mag < 0x7F800000u);
+          if ((c & 7) == 0) sc[u >> 3] = scale;
+        };
+        put(y0, m0, c);
+        if (!rope_lane) put(y1, m1, 32 + c);
+      }
+      if (rope_lane) {
+        float4 z0, z1;
+        if (p.cs) {
+          z0 = *reinterpret_cast<const float4*>(at + 1024 + (c - 24) * 32);
+          z1 = *reinterpret_cast<const float4*>(at + 1040 + (c - 24) * 32);
+        }
+        const float2 cs[4] = {{z0.x, z0.y}, {z0.z, z0.w}, {z1.x, z1.y}, {z1.z, z1.w}};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = y1[i];
+          if (p.cs) y1[i] = make_float2(fmaf(y.x, cs[i].x, -(y.y * cs[i].y)), fmaf(y.y, cs[i].x, y.x * cs[i].y));
+          const __nv_bfloat162 v = __floats2bfloat162_rn(y1[i].x, y1[i].y);
+          o[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        // neither normed nor rotated: the input's bits
+        reinterpret_cast<uint4*>(pg + kRopeOff + slot * 128)[c - 24] = kNorm || p.cs ? make_uint4(o[0], o[1], o[2], o[3]) : v1;
+      }
     }
   }
 }
 
 template <bool kFp4, bool kNorm>
-cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
+cudaError_t launch_append(AppendParams& p, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cudaErrorUnknown;
-  const int64_t per = kThreads / 32, want = (static_cast<int64_t>(p.n) + per - 1) / per, cap = static_cast<int64_t>(sms) * 20;
-  return launch_pdl(cache_append_kernel<kFp4, kNorm>, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(kThreads), 0,
+  // batches that keep every multiprocessor's warps busy with one each, as far as there are rows
+  constexpr int64_t kWarps = kThreads / 32;
+  const int64_t n = p.n, want = (n + sms * 4 * kWarps - 1) / (sms * 4 * kWarps);
+  p.per = static_cast<int32_t>(want < 1 ? 1 : (want > kMaxRows ? kMaxRows : want));
+  const int64_t blocks = (n + p.per * kWarps - 1) / (p.per * kWarps), cap = static_cast<int64_t>(sms) * 16;
+  return launch_pdl(cache_append_kernel<kFp4, kNorm>, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(kThreads), 0,
                     stream, p);
 }
 

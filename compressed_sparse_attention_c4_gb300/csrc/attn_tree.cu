@@ -60,6 +60,9 @@ constexpr int kRegsCompute = 104, kRegsGather = 64, kRegsMma = 40;
 static_assert(kComputeThreads * kRegsCompute + kGatherThreads * kRegsGather + 128 * kRegsMma <= kThreadsT * 72,
               "the register shares fit in the launch's");
 constexpr uint32_t kBarCompute = 1;      // named barrier
+// Chunks that a CTA may have more than its share when items are left whole: cutting costs the
+// writing and joining of partial sums.
+constexpr int kWholeSlack = 2;
 
 struct TreeParams {
   const uint16_t* q;
@@ -230,10 +233,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
   // ---- this CTA's run of chunks: each thread counts a run of items, a scan over the threads
   {
     int64_t* part = reinterpret_cast<int64_t*>(kv);
+    int2* part_items = reinterpret_cast<int2*>(kv + 512);   // items, the longest one's chunks
     const int n_items = p.B * p.blocks, per = (n_items + kThreadsT - 1) / kThreadsT;
     const int i0 = min(static_cast<int64_t>(tid) * per, static_cast<int64_t>(n_items)), i1 = min(i0 + per, n_items);
-    auto walk = [&](int64_t until, int& item, int64_t at) {   // adds up items from i0 to the one that chunk `until` is in
+    // adds up items from i0 on, until the one that has chunk `until`, or is number `until_item` of this run
+    int seen = 0, longest = 0, size = 0;
+    auto walk = [&](int64_t until, int until_item, int& item, int64_t at) {
       int b_of = -1, s0 = 0, nodes = 0, ctx = 0;
+      seen = 0;
       for (item = i0; item < i1; ++item) {
         const int b = item / p.blocks, k = item - b * p.blocks;
         if (b != b_of) {
@@ -242,35 +249,57 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
           b_of = b;
         }
         if (k * kN >= nodes * p.H) continue;
-        const int c = chunks_of_item(p, s0, nodes, ctx, k);
-        if (at + c > until) return at;
-        at += c;
+        size = chunks_of_item(p, s0, nodes, ctx, k);
+        longest = max(longest, size);
+        if (at + size > until || seen == until_item) return at;
+        at += size;
+        ++seen;
       }
       return at;
     };
     int item;
-    const int64_t mine = walk(INT64_MAX, item, 0);
+    const int64_t mine = walk(INT64_MAX, -1, item, 0);
+    const int mine_items = seen;
     int64_t sum = mine;
+    int sum_items = mine_items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= static_cast<uint32_t>(o)) sum += up;
+      const int up_items = __shfl_up_sync(0xffffffffu, sum_items, o);
+      if (lane >= static_cast<uint32_t>(o)) sum += up, sum_items += up_items;
     }
-    if (lane == 31) part[warp] = sum;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) part[warp] = sum, part_items[warp] = make_int2(sum_items, longest);
     __syncthreads();
     int64_t before = sum - mine, total = 0;
+    int before_items = sum_items - mine_items, all_items = 0;
     for (int w = 0; w < kThreadsT / 32; ++w) {
-      before += w < static_cast<int>(warp) ? part[w] : 0;
+      const int2 q = part_items[w];
+      if (w < static_cast<int>(warp)) before += part[w], before_items += q.x;
       total += part[w];
+      all_items += q.x;
+      longest = max(longest, q.y);
     }
     // no more CTAs than chunks, so that every CTA between an item's first and last has a piece of it
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), g = blockIdx.x;
-    const int64_t w0 = g < ctas ? total * g / ctas : total, w1 = g < ctas ? total * (g + 1) / ctas : total;
-    if (w0 < w1 && before <= w0 && w0 < before + mine) {
-      first[1] = walk(w0, item, before);     // chunks before the item
-      first[0] = item;
+    if (all_items <= ctas && longest <= (total + ctas - 1) / ctas + kWholeSlack) {
+      // a CTA for each item, none is cut
+      if (before_items <= g && g < before_items + mine_items) {
+        const int64_t at = walk(INT64_MAX, static_cast<int>(g) - before_items, item, before);
+        first[0] = item;
+        first[1] = first[2] = at;
+        first[3] = at + size;
+      }
+    } else {
+      const int64_t w0 = g < ctas ? total * g / ctas : total, w1 = g < ctas ? total * (g + 1) / ctas : total;
+      if (w0 < w1 && before <= w0 && w0 < before + mine) {
+        first[1] = walk(w0, -1, item, before);     // chunks before the item
+        first[0] = item;
+        first[2] = w0;
+        first[3] = w1;
+      }
     }
-    if (tid == 0) first[2] = w0, first[3] = w1, first[4] = total;
+    if (tid == 0) first[4] = total;
     __syncthreads();
   }
   bool ok = true;                            // no wait of this thread has run out
@@ -470,7 +499,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
       int item = static_cast<int>(first[0]);
       int64_t base = first[1], at = first[2];    // chunks before the item; the next chunk of this CTA
       const int64_t w1 = first[3], total = first[4], ctas = min(static_cast<int64_t>(gridDim.x), total);
-      if (item < 0) at = w1;
+      if (item < 0) at = w1;                     // nothing for this CTA
       // Every one of the three warps walks the items (Q's place follows from the walk); the first writes them down.
 #pragma unroll 1
       for (int n_item = 0;; ++n_item) {
@@ -826,34 +855,50 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
   }
 }
 
-// Joins the pieces of cut items: unit = two columns, four warps a column, each every fourth
-// piece, lane l holding dims 4 l + 128 i.  The CTAs share out the units of all cut items.
+// Joins the pieces of cut items.  A column's pieces are added up by one warp (lane l holding dims
+// 4 l + 128 i) or, where there are many, by four: a unit is eight columns, or two.  The CTAs share
+// out the units of all cut items.
 constexpr int kMaxCtas = 160;
+constexpr int kFewPieces = 8;
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, int ctas) {
-  __shared__ int32_t cut[kMaxCtas];
+  __shared__ int32_t cut[kMaxCtas], units_to[kMaxCtas];   // CTA that cuts, units up to and with its item's
   __shared__ int32_t n_cut;
   __shared__ float4 acc[8][128];
   griddep_launch();
   griddep_wait();
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   if (tid < 32) {
-    int n = 0;
+    int n = 0, units = 0;
     for (int i = tid; i < (ctas + 31) / 32 * 32; i += 32) {
-      const bool has = i < ctas && p.ws_cut[i].y > 0;
-      const uint32_t bits = __ballot_sync(0xffffffffu, has);
-      if (has) cut[n + __popc(bits & ((1u << tid) - 1u))] = i;
+      const int4 rec = i < ctas ? p.ws_cut[i] : make_int4(0, 0, 0, 0);
+      const uint32_t bits = __ballot_sync(0xffffffffu, rec.y > 0);
+      int u = rec.y > 0 ? (rec.z - i < kFewPieces ? (rec.y + 7) / 8 : (rec.y + 1) / 2) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, u, o);
+        if (lane >= o) u += up;
+      }
+      if (rec.y > 0) {
+        const int at = n + __popc(bits & ((1u << tid) - 1u));
+        cut[at] = i;
+        units_to[at] = units + u;
+      }
       n += __popc(bits);
+      units += __shfl_sync(0xffffffffu, u, 31);
     }
     if (tid == 0) n_cut = n;
   }
   __syncthreads();
-  const int n_units = n_cut * (kN / 2);
+  const int n_units = n_cut > 0 ? units_to[n_cut - 1] : 0;
+  int which = 0;
   for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
-    const int g0 = cut[unit / (kN / 2)];
+    while (units_to[which] <= unit) ++which;
+    const int g0 = cut[which], in_item = unit - (which > 0 ? units_to[which - 1] : 0);
     const int4 rec = p.ws_cut[g0];
-    const int col = unit % (kN / 2) * 2 + (warp >> 2);
-    if (unit % (kN / 2) * 2 >= rec.y) continue;            // the same in the whole CTA
     const int last = rec.z, pieces = last - g0 + 1;
+    const bool few = pieces <= kFewPieces;
+    const int share = few ? 1 : 4;                         // warps of a column
+    const int col = few ? in_item * 8 + warp : in_item * 2 + (warp >> 2);
     const int64_t row = static_cast<int64_t>(rec.x) + col;
     const bool live = col < rec.y;
     const int head = static_cast<int>(row % p.H), node = static_cast<int>(row / p.H);
@@ -881,7 +926,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, int
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-    for (int i = warp & 3; i < pieces; i += 4) {
+    for (int i = few ? 0 : warp & 3; i < pieces; i += share) {
       const float2 ml = p.ws_ml[slot(i)];
       const float4* src = reinterpret_cast<const float4*>(p.ws_o + slot(i) * 512) + lane;
       float4 x[4];
@@ -895,33 +940,39 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, int
         v[j].z = fmaf(x[j].z, f, v[j].z), v[j].w = fmaf(x[j].w, f, v[j].w);
       }
     }
+    const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
+    // four dims from 4 q on of this column
+    auto put = [&](float4 s, int q) {
+      s.x *= inv, s.y *= inv, s.z *= inv, s.w *= inv;
+      if (p.rope_cs != nullptr && q >= 112) {
+        const int rr = __ldg(p.rope_pos + node);
+        if (rr >= 0 && rr < p.rope_rows) {                 // else flagged by the first kernel
+          const float4 cs = __ldg(p.rope_cs + static_cast<int64_t>(rr) * 16 + (q - 112));
+          const float2 a = rotate_back(s.x, s.y, cs.x, cs.y), b = rotate_back(s.z, s.w, cs.z, cs.w);
+          s = make_float4(a.x, a.y, b.x, b.y);
+        }
+      }
+      *reinterpret_cast<uint2*>(p.out + row * 512 + q * 4) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      if (p.lse && q == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    };
+    if (few) {
+      if (live)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put(v[j], lane + 32 * j);
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[warp][lane + 32 * j] = v[j];
     __syncthreads();
     // 128 threads a column: four dims each
-    {
-      const int c = tid >> 7, q = tid & 127;               // c = warp >> 2, this thread's column as above
-      float4 s = acc[c * 4][q];
+    const int q = tid & 127;                               // tid >> 7 = warp >> 2, this thread's column as above
+    float4 s = acc[warp & 4][q];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const float4 x = acc[c * 4 + w][q];
-        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-      }
-      const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
-      s.x *= inv, s.y *= inv, s.z *= inv, s.w *= inv;
-      if (live) {
-        if (p.rope_cs != nullptr && q >= 112) {
-          const int rr = __ldg(p.rope_pos + node);
-          if (rr >= 0 && rr < p.rope_rows) {               // else flagged by the first kernel
-            const float4 cs = __ldg(p.rope_cs + static_cast<int64_t>(rr) * 16 + (q - 112));
-            const float2 a = rotate_back(s.x, s.y, cs.x, cs.y), b = rotate_back(s.z, s.w, cs.z, cs.w);
-            s = make_float4(a.x, a.y, b.x, b.y);
-          }
-        }
-        *reinterpret_cast<uint2*>(p.out + row * 512 + q * 4) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-        if (p.lse && q == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-      }
+    for (int w = 1; w < 4; ++w) {
+      const float4 x = acc[(warp & 4) + w][q];
+      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
     }
+    if (live) put(s, q);
     __syncthreads();
   }
 }
@@ -1022,7 +1073,7 @@ int launch_tree_attn(const dsv4sa_tree_args* a, cudaStream_t stream) {
   if (launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreadsT), SmemT::kBytes + 1024, stream, p) != cudaSuccess)
     return DSV4SA_ERR_CUDA;
   if (ctas == 1) return DSV4SA_OK;       // nothing can be cut
-  return launch_pdl(tree_merge_kernel, dim3(static_cast<unsigned>(2 * sms)), dim3(256), 0, stream, p, ctas) == cudaSuccess ? DSV4SA_OK
+  return launch_pdl(tree_merge_kernel, dim3(static_cast<unsigned>(4 * sms)), dim3(256), 0, stream, p, ctas) == cudaSuccess ? DSV4SA_OK
                                                                                                                           : DSV4SA_ERR_CUDA;
 }
 

@@ -18,8 +18,10 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------- table
 // An angle is a phase: w_i / 2 pi as a 64-bit fraction of a turn, times the position, modulo
 // 2^64.  Whole turns drop out exactly, so a position of 2^40 costs no more precision than one of
-// 1: what is left of the angle has 64 bits below the point, and the fp32 sine and cosine take
-// their argument rounded once.  A thread keeps one pair and adds a constant phase from row to row.
+// 1.  The nearest quarter turn is taken off in whole numbers, too; what is left, at most an eighth of a
+// turn with 64 bits below the point, is rounded to fp32 and goes through the Taylor series of
+// sine and cosine (to x^9 and x^10: 2^-28 and 2^-32 at pi / 4).  A thread keeps one pair and
+// adds a constant phase from row to row.
 struct TableParams {
   float2* cs;
   int64_t first;
@@ -39,9 +41,18 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
   const uint64_t turn = p.turn[i], turn_step = turn * static_cast<uint64_t>(step);
   uint64_t phase = turn * static_cast<uint64_t>(p.first + r);
   for (; r < p.rows; r += step, phase += turn_step) {
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int64_t>(phase)) * 0x1p-63f, &s, &c);   // half turns in [-1, 1)
-    __stcs(p.cs + r * p.pairs + i, make_float2(c, s));
+    const uint64_t at = phase + (uint64_t{1} << 61);
+    const uint32_t quarter = static_cast<uint32_t>(at >> 62);
+    const int64_t rest = static_cast<int64_t>((at & ((uint64_t{1} << 62) - 1)) - (uint64_t{1} << 61));
+    // hi 2^32 + lo, each rounded on its own where it is long
+    const float part = fmaf(static_cast<float>(static_cast<int32_t>(rest >> 32)), 0x1p32f, static_cast<float>(static_cast<uint32_t>(rest)));
+    const float x = part * static_cast<float>(6.283185307179586476925 * 0x1p-64), xx = x * x;
+    const float s0 = fmaf(xx, fmaf(xx, fmaf(xx, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6);
+    const float c0 = fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f);
+    const float s = fmaf(x * xx, s0, x), c = fmaf(xx, c0, 1.f);
+    const uint32_t odd = quarter & 1u;
+    const uint32_t a = __float_as_uint(odd ? s : c) ^ ((quarter + 1u & 2u) << 30), b = __float_as_uint(odd ? c : s) ^ ((quarter & 2u) << 30);
+    __stcs(p.cs + r * p.pairs + i, make_float2(__uint_as_float(a), __uint_as_float(b)));
   }
 }
 
