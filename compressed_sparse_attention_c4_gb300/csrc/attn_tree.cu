@@ -60,6 +60,9 @@ constexpr int kRegsCompute = 104, kRegsGather = 64, kRegsMma = 40;
 static_assert(kComputeThreads * kRegsCompute + kGatherThreads * kRegsGather + 128 * kRegsMma <= kThreadsT * 72,
               "the register shares fit in the launch's");
 constexpr uint32_t kBarCompute = 1;      // named barrier
+// What is dealt out to the CTAs are an item's chunks and the step to the next item, which takes
+// about as long as a chunk.
+constexpr int kItemStep = 1;
 // Chunks that a CTA may have more than its share when items are left whole: cutting costs the
 // writing and joining of partial sums.
 constexpr int kWholeSlack = 2;
@@ -159,18 +162,37 @@ __device__ __forceinline__ int chunks_of(uint32_t rows) { return rows == 0 ? 1 :
 // A position as the masks use it: below 2^31 - 1, -1 for any that is negative.
 __device__ __forceinline__ int pos_of(int pos) { return min(max(pos, -1), 0x7FFFFFFE); }
 
-// Chunks of item (b, k), by one thread.
+// Chunks of item (b, k), by one thread: eight nodes' values are on the way at a time.
 __device__ __forceinline__ int chunks_of_item(const TreeParams& p, int s0, int nodes, int ctx, int k) {
   int nv = 0, lo = 0x7FFFFFFE, hi = -1;
   uint64_t anc = 0;
-  for (int n = k * kN / p.H; n < nodes && n * p.H < (k + 1) * kN; ++n) {
-    const int pos = pos_of(__ldg(p.pos + s0 + n));
-    nv = max(nv, min(__ldg(p.n_vis + s0 + n), p.n_max));
-    lo = min(lo, pos);
-    hi = max(hi, pos);
-    anc |= ancestors_of(p, s0, n, nodes);
+  const int last = min(nodes - 1, ((k + 1) * kN - 1) / p.H);
+  for (int n0 = k * kN / p.H; n0 <= last; n0 += 8) {
+    int v[8], pos[8];
+    uint64_t a[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = min(n0 + i, last);       // the last again, where there are fewer
+      v[i] = __ldg(p.n_vis + s0 + n);
+      pos[i] = __ldg(p.pos + s0 + n);
+      a[i] = ancestors_of(p, s0, n, nodes);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = pos_of(pos[i]);
+      nv = max(nv, min(v[i], p.n_max));
+      lo = min(lo, at);
+      hi = max(hi, at);
+      anc |= a[i];
+    }
   }
   return chunks_of(span_of(p, ctx, nv, lo, hi, anc).rows);
+}
+
+// a b / c, all below 2^63 c; without a 64-bit division where that is possible
+__device__ __forceinline__ int64_t scaled(int64_t a, int64_t b, int64_t c) {
+  const int64_t x = a * b;
+  return x >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(c)) : x / c;
 }
 
 template <bool kFp4>
@@ -198,6 +220,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
   uint64_t* bar_o = bar_full + 10;         // every PV of the item is complete
   uint64_t* bar_q = bar_full + 11;         // the item's Q is there
   uint64_t* bar_qfree = bar_full + 12;     // every S of the item is complete
+  uint64_t* bar_q0 = bar_full + 13;        // the first item's Q is there
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::kTmem);
 
   constexpr uint32_t kColS = 0, kColO = kN;
@@ -216,6 +239,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
     mbar_init(bar_o, 1);
     mbar_init(bar_q, kQThreads / 32);
     mbar_init(bar_qfree, 1);
+    mbar_init(bar_q0, kComputeThreads / 32);
     fence_mbar_init();
     first[0] = -1;
   }
@@ -230,7 +254,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  // ---- this CTA's run of chunks: each thread counts a run of items, a scan over the threads
+  // ---- this CTA's run of chunks (and steps): each thread counts a run of items, a scan over the threads
   {
     int64_t* part = reinterpret_cast<int64_t*>(kv);
     int2* part_items = reinterpret_cast<int2*>(kv + 512);   // items, the longest one's chunks
@@ -249,7 +273,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
           b_of = b;
         }
         if (k * kN >= nodes * p.H) continue;
-        size = chunks_of_item(p, s0, nodes, ctx, k);
+        size = chunks_of_item(p, s0, nodes, ctx, k) + kItemStep;
         longest = max(longest, size);
         if (at + size > until || seen == until_item) return at;
         at += size;
@@ -280,22 +304,26 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
       all_items += q.x;
       longest = max(longest, q.y);
     }
-    // no more CTAs than chunks, so that every CTA between an item's first and last has a piece of it
+    // no more CTAs than there is to deal out, so that every CTA between an item's first and last has a piece of it
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), g = blockIdx.x;
     if (all_items <= ctas && longest <= (total + ctas - 1) / ctas + kWholeSlack) {
       // a CTA for each item, none is cut
       if (before_items <= g && g < before_items + mine_items) {
-        const int64_t at = walk(INT64_MAX, static_cast<int>(g) - before_items, item, before);
+        item = i0;
+        const int64_t at = per > 1 ? walk(INT64_MAX, static_cast<int>(g) - before_items, item, before) : before;
         first[0] = item;
         first[1] = first[2] = at;
         first[3] = at + size;
       }
     } else {
-      const int64_t w0 = g < ctas ? total * g / ctas : total, w1 = g < ctas ? total * (g + 1) / ctas : total;
+      const int64_t w0 = g < ctas ? scaled(total, g, ctas) : total, w1 = g < ctas ? scaled(total, g + 1, ctas) : total;
       if (w0 < w1 && before <= w0 && w0 < before + mine) {
-        first[1] = walk(w0, -1, item, before);     // chunks before the item
-        first[0] = item;
-        first[2] = w0;
+        item = i0;
+        const int64_t at = per > 1 ? walk(w0, -1, item, before) : before;    // what lies before the item
+        const bool step = w0 - at >= size - kItemStep;      // only its last step: that is another CTA's
+        first[0] = step ? item + 1 : item;
+        first[1] = step ? at + size : at;
+        first[2] = step ? at + size : w0;
         first[3] = w1;
       }
     }
@@ -303,6 +331,19 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
     __syncthreads();
   }
   bool ok = true;                            // no wait of this thread has run out
+
+  // Q of an item: swizzled K-major tile; rows past the item's are zero.
+  auto load_q = [&](int row0, int cols, int from, int step) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q) + static_cast<int64_t>(row0) * 64;
+#pragma unroll 4
+    for (int u = from; u < kN * 64; u += step) {
+      const int h = u >> 6, v = u & 63;
+      cp_async16(qs + (v >> 3) * (kN * 128) + sw128_offset(h, v & 7), src + min(h, cols - 1) * 64 + v, h < cols ? 16u : 0u);
+    }
+    cp_async_wait();
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
 
   if (warp >= 8 && warp < kMmaWarp) {
     // =========================== gather warps ===========================
@@ -459,7 +500,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
         if (n == 0) break;
         if (lane == 0) mbar_arrive(bar_done + (n_item & 1));
         __syncwarp();
-        ok = warp_wait(bar_q, n_item & 1);
+        ok = n_item == 0 ? warp_wait(bar_q0, 0) : warp_wait(bar_q, (n_item - 1) & 1);
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
 #pragma unroll
@@ -497,7 +538,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
       // =========================== scheduler and Q ===========================
       const int qt = tid - kSchedWarp * 32;
       int item = static_cast<int>(first[0]);
-      int64_t base = first[1], at = first[2];    // chunks before the item; the next chunk of this CTA
+      int64_t base = first[1], at = first[2];    // what lies before the item; where this CTA goes on
       const int64_t w1 = first[3], total = first[4], ctas = min(static_cast<int64_t>(gridDim.x), total);
       if (item < 0) at = w1;                     // nothing for this CTA
       // Every one of the three warps walks the items (Q's place follows from the walk); the first writes them down.
@@ -529,6 +570,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
         const int row0 = more ? s0 * p.H + k * kN : 0;
         int chunks = 0;
         if (more) {
+          const int ctx = __ldg(p.ctx + b), seq = p.seq_row ? __ldg(p.seq_row + b) : b;
           int nv_max = 0, nv_min = 0x7FFFFFFF, lo = 0x7FFFFFFE, hi = -1, nvc[2], posc[2], nodec[2];
           uint64_t ancc[2], anc = 0;
 #pragma unroll
@@ -551,7 +593,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
           hi = __reduce_max_sync(0xffffffffu, hi);
           anc = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(anc >> 32))) << 32 |
                 __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(anc));
-          const Span sp = span_of(p, __ldg(p.ctx + b), nv_max, lo, hi, anc);
+          const Span sp = span_of(p, ctx, nv_max, lo, hi, anc);
           chunks = chunks_of(sp.rows);
           if (warp == kSchedWarp) {
             if (n_item >= 2 && ok) ok = warp_wait(bar_done + (n_item & 1), ((n_item >> 1) - 1) & 1);
@@ -586,8 +628,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
               it->win_rows = sp.win_rows;
               it->rows = sp.rows;
               it->win_lo = sp.win_lo;
-              it->seq = p.seq_row ? __ldg(p.seq_row + b) : b;
-              it->last_cta = static_cast<int>(((base + chunks) * ctas - 1) / total);
+              it->seq = seq;
+              const int64_t x = (base + chunks) * ctas - 1;   // the CTA that has the item's last chunk
+              it->last_cta = static_cast<int>(scaled(x, 1, total));
             }
           }
         } else if (warp == kSchedWarp) {
@@ -599,24 +642,16 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
           if (lane == 0) mbar_arrive(bar_item + (n_item & 1));
         }
         if (!more || !ok) break;
-        // ---- Q, when the S of the item before are complete.  Swizzled K-major tile; rows past the item's are zero.
-        const uint4* src = reinterpret_cast<const uint4*>(p.q) + static_cast<int64_t>(row0) * 64;
+        // ---- Q, when the S of the item before are complete (the first item's: by the softmax warps)
         if (n_item > 0) {
-          if (qt == 0) prefetch_l2(src, static_cast<uint32_t>(cols) * 1024u);
+          if (qt == 0) prefetch_l2(p.q + static_cast<int64_t>(row0) * 512, static_cast<uint32_t>(cols) * 1024u);
           ok = warp_wait(bar_qfree, (n_item - 1) & 1);
           if (!ok) break;
+          load_q(row0, cols, qt, kQThreads);
+          if (lane == 0) mbar_arrive(bar_q);
         }
-#pragma unroll 4
-        for (int u = qt; u < kN * 64; u += kQThreads) {
-          const int h = u >> 6, v = u & 63;
-          cp_async16(qs + (v >> 3) * (kN * 128) + sw128_offset(h, v & 7), src + min(h, cols - 1) * 64 + v, h < cols ? 16u : 0u);
-        }
-        cp_async_wait();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_q);
-        at = min(base + chunks, w1);
-        base += chunks;
+        base += chunks + kItemStep;
+        at = base;
         ++item;
       }
     }
@@ -631,6 +666,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
     if (tid < kN) m_used[tid] = -1e30f;
     if (tid == 0) p.ws_cut[blockIdx.x] = make_int4(0, 0, 0, 0);
     named_barrier_sync(kBarCompute, kComputeThreads);
+    if (warp_wait(bar_item, 0) && items[0].c0 < items[0].c1) {
+      load_q(items[0].row0, items[0].cols, tid, kComputeThreads);
+      if (lane == 0) mbar_arrive(bar_q0);
+    }
     int chunk = 0;
     bool alive = true;                                      // the same in all compute threads
 #pragma unroll 1
@@ -860,33 +899,39 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
 // out the units of all cut items.
 constexpr int kMaxCtas = 160;
 constexpr int kFewPieces = 8;
+static_assert(kMaxCtas <= 256, "a thread of the joining kernel looks at one CTA's record");
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, int ctas) {
   __shared__ int32_t cut[kMaxCtas], units_to[kMaxCtas];   // CTA that cuts, units up to and with its item's
   __shared__ int32_t n_cut;
+  __shared__ int2 sums[8];
   __shared__ float4 acc[8][128];
   griddep_launch();
   griddep_wait();
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  if (tid < 32) {
-    int n = 0, units = 0;
-    for (int i = tid; i < (ctas + 31) / 32 * 32; i += 32) {
-      const int4 rec = i < ctas ? p.ws_cut[i] : make_int4(0, 0, 0, 0);
-      const uint32_t bits = __ballot_sync(0xffffffffu, rec.y > 0);
-      int u = rec.y > 0 ? (rec.z - i < kFewPieces ? (rec.y + 7) / 8 : (rec.y + 1) / 2) : 0;
+  {
+    const int4 rec = tid < ctas ? p.ws_cut[tid] : make_int4(0, 0, 0, 0);
+    const bool has = rec.y > 0;
+    const uint32_t bits = __ballot_sync(0xffffffffu, has);
+    int u = has ? (rec.z - tid < kFewPieces ? (rec.y + 7) / 8 : (rec.y + 1) / 2) : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, u, o);
-        if (lane >= o) u += up;
-      }
-      if (rec.y > 0) {
-        const int at = n + __popc(bits & ((1u << tid) - 1u));
-        cut[at] = i;
-        units_to[at] = units + u;
-      }
-      n += __popc(bits);
-      units += __shfl_sync(0xffffffffu, u, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, u, o);
+      if (lane >= o) u += up;
     }
-    if (tid == 0) n_cut = n;
+    if (lane == 31) sums[warp] = make_int2(__popc(bits), u);
+    __syncthreads();
+    int n = 0, units = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) n += sums[i].x, units += sums[i].y;
+      all += sums[i].x;
+    }
+    if (has) {
+      const int at = n + __popc(bits & ((1u << lane) - 1u));
+      cut[at] = tid;
+      units_to[at] = units + u;
+    }
+    if (tid == 0) n_cut = all;
   }
   __syncthreads();
   const int n_units = n_cut > 0 ? units_to[n_cut - 1] : 0;
@@ -925,7 +970,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, int
     float4 v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
     for (int i = few ? 0 : warp & 3; i < pieces; i += share) {
       const float2 ml = p.ws_ml[slot(i)];
       const float4* src = reinterpret_cast<const float4*>(p.ws_o + slot(i) * 512) + lane;
