@@ -27,6 +27,18 @@
 //     dims x 4, N = 64, K = 128).
 //   softmax warps (8): thread = row, 32 of the item's columns.  P is BF16 against a max that is
 //     only moved (and O rescaled) when a score passes it by 2^8.
+// What bounds it: shared memory and the hand-overs from warp to warp.  A chunk takes about 6800
+// cycles (trees of 16 nodes, 64 heads, 8336 rows, traced): 2700 to widen its two halves, of which
+// the first half's 1270 nothing else can hide, 1200 for the second half of S, 1320 for the
+// softmax, 1090 until PV has read the first half; the matrix instructions read 384 KB of shared
+// memory (3070 cycles at 128 bytes a clock), the tile's stores are 128 KB more, and loads that pass
+// L1 meanwhile wait.  8 sequences x 16 nodes x 64 heads at 8192 entries: 227 us, 615 TFLOP/s, 0.32
+// of the matrix peak; 32 x 4 nodes at 512 entries 31.1 us; one token of 16 heads at 512 entries
+// 18.9 (scan of the lengths, the item's description, Q, a chunk, its sums, the joining kernel).
+// Sixteen warps that load, widen and do the softmax in turn (so that widening overlaps PV) took
+// 255 to 268 us for the first of these, 236 then with warps of one kind each: their loads wait for the shared memory
+// that the matrix instructions use.  Loads that leave L1 out took 311.  Dealing out an item's last step as a chunk, and the
+// first item's Q fetched by the softmax warps: mixed batch of 64 sequences 91 -> 79 us.
 // Only chunks that hold a row that some node does not see look at masks.  A row that holds an
 // infinity or a NaN shows in its scores, which then are no numbers for any column: it is taken
 // out of the tile (0 times it would be a NaN for nodes that do not see it), and the nodes that
@@ -894,7 +906,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
   }
 }
 
-// Joins the pieces of cut items.  A column's pieces are added up by one warp (lane l holding dims
+// Joins the pieces of cut items (bound by the partial sums, 2 KB a column and piece, which are in
+// L2, and for few items by its launch, 2 us).  Two columns a unit whatever the pieces, and every
+// item cut, took 68.7 us for 128 items of six chunks; 33.8 with eight columns a unit and items left whole.
+// A column's pieces are added up by one warp (lane l holding dims
 // 4 l + 128 i) or, where there are many, by four: a unit is eight columns, or two.  The CTAs share
 // out the units of all cut items.
 constexpr int kMaxCtas = 160;
