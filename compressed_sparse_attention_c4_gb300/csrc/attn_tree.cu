@@ -318,7 +318,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
     }
     // no more CTAs than there is to deal out, so that every CTA between an item's first and last has a piece of it
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), g = blockIdx.x;
-    if (all_items <= ctas && longest <= (total + ctas - 1) / ctas + kWholeSlack) {
+    if (total == 0) {
+      // no sequence has a node: nothing for any CTA
+    } else if (all_items <= ctas && longest <= (total + ctas - 1) / ctas + kWholeSlack) {
       // a CTA for each item, none is cut
       if (before_items <= g && g < before_items + mine_items) {
         item = i0;
