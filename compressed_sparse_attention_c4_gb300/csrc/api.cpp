@@ -558,6 +558,10 @@ DSV4SA_API int dsv4sa_tree_attn(const dsv4sa_tree_args* a, cudaStream_t stream) 
   if (win && (!a->win || !words(a->win_pt) || a->win_pt_stride < 1 ||
               a->win_ring > static_cast<int64_t>(a->win_pt_stride) * DSV4SA_PAGE_SIZE))
     return DSV4SA_ERR_INVALID_ARG;
+  // without seq_row sequence b has row b
+  if (a->comp_pt_rows < 0 || a->win_pt_rows < 0) return DSV4SA_ERR_INVALID_ARG;
+  if (!a->seq_row && ((comp && a->comp_pt_rows > 0 && a->comp_pt_rows < a->n_seqs) || (win && a->win_pt_rows > 0 && a->win_pt_rows < a->n_seqs)))
+    return DSV4SA_ERR_INVALID_ARG;
   if (comp && win && a->comp->kind != a->win->kind) return DSV4SA_ERR_UNSUPPORTED;   // one FP8 and one FP4 pool
   if (a->rope_cs && (!words(a->rope_pos) || a->rope_rows < 1 || !aligned(a->rope_cs, 16))) return DSV4SA_ERR_INVALID_ARG;
   const size_t need = dsv4sa::tree_attn_workspace(a->n_seqs, a->max_nodes, a->H, a->n_max, a->window);

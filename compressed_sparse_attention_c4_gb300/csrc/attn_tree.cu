@@ -101,6 +101,7 @@ struct TreeParams {
   int4* ws_cut;              // [CTAs]: (first row of q, columns, last CTA) of the item that CTA cuts first
   int64_t comp_page_stride, comp_num_pages, win_page_stride, win_num_pages;
   int32_t comp_pt_stride, win_pt_stride;
+  int32_t comp_pt_rows, win_pt_rows;    // of the tables; INT32_MAX where the caller did not say
   int32_t n_max, window, win_ring, draft_entry;
   int32_t B, T, H, max_nodes, blocks;   // blocks: items of a sequence at most
   int32_t rope_rows;
@@ -117,7 +118,7 @@ struct alignas(16) Item {
   int32_t nv_max, nv_min;    // entries that any, that every node sees
   uint32_t win_rows, rows;   // rows of the window; all rows
   int64_t win_lo;            // the window's first position
-  int32_t seq;               // row of the page tables
+  int32_t seq_comp, seq_win; // its row of each page table, -1: not a row of it
   int32_t last_cta;          // the CTA that has the item's last chunk
   int32_t nv[kN], lo[kN], hi[kN];   // by column: entries, first and last position of the window
   uint64_t anc[kN];
@@ -379,8 +380,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
       auto locate = [&](int ch) -> uint64_t {
         const uint32_t rr = static_cast<uint32_t>(ch) * kRows + row;
         if (rr >= rows) return 0;
-        const int seq = it->seq;
         if (rr < nv_max) {
+          const int seq = it->seq_comp;
           const int page = seq >= 0 ? __ldg(p.comp_pt + static_cast<int64_t>(seq) * p.comp_pt_stride + (rr >> 6)) : -1;
           if (page < 0 || page >= p.comp_num_pages) return 0;
           return reinterpret_cast<uint64_t>(p.comp_base + page * p.comp_page_stride) | (rr & 63u);
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
         } else {
           e = static_cast<uint32_t>(p.draft_entry) + (e - it->win_rows);
         }
+        const int seq = it->seq_win;
         const int page = seq >= 0 && static_cast<int>(e >> 6) < p.win_pt_stride
                              ? __ldg(p.win_pt + static_cast<int64_t>(seq) * p.win_pt_stride + (e >> 6)) : -1;
         if (page < 0 || page >= p.win_num_pages) return 0;
@@ -642,7 +644,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
               it->win_rows = sp.win_rows;
               it->rows = sp.rows;
               it->win_lo = sp.win_lo;
-              it->seq = seq;
+              it->seq_comp = seq < p.comp_pt_rows ? seq : -1;
+              it->seq_win = seq < p.win_pt_rows ? seq : -1;
               const int64_t x = (base + chunks) * ctas - 1;   // the CTA that has the item's last chunk
               it->last_cta = static_cast<int>(scaled(x, 1, total));
             }
@@ -1100,6 +1103,7 @@ int launch_tree_attn(const dsv4sa_tree_args* a, cudaStream_t stream) {
     p.comp_num_pages = a->comp->num_pages;
     p.comp_pt = a->comp_pt;
     p.comp_pt_stride = a->comp_pt_stride;
+    p.comp_pt_rows = a->comp_pt_rows > 0 ? a->comp_pt_rows : INT32_MAX;
   }
   if (a->window > 0 || a->draft_entry >= 0) {
     fp4 = a->win->kind == DSV4SA_POOL_KV_FP4;
@@ -1108,6 +1112,7 @@ int launch_tree_attn(const dsv4sa_tree_args* a, cudaStream_t stream) {
     p.win_num_pages = a->win->num_pages;
     p.win_pt = a->win_pt;
     p.win_pt_stride = a->win_pt_stride;
+    p.win_pt_rows = a->win_pt_rows > 0 ? a->win_pt_rows : INT32_MAX;
   }
   p.rope_cs = reinterpret_cast<const float4*>(a->rope_cs);
   p.rope_pos = a->rope_pos;

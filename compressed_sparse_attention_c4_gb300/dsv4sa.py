@@ -109,7 +109,7 @@ class TreeArgs(ctypes.Structure):
                 ("window", ctypes.c_int32), ("win_ring", ctypes.c_int32), ("draft_entry", ctypes.c_int32),
                 ("rope_rows", ctypes.c_int32), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
                 ("rope_cs", ctypes.c_void_p), ("rope_pos", ctypes.c_void_p), ("ws", ctypes.c_void_p),
-                ("ws_bytes", ctypes.c_size_t)]
+                ("ws_bytes", ctypes.c_size_t), ("comp_pt_rows", ctypes.c_int32), ("win_pt_rows", ctypes.c_int32)]
 
 
 class StepDesc(ctypes.Structure):
@@ -929,6 +929,14 @@ def _nodes(node_start, ctx, pos, anc, T, here):
             None if anc is None else _dev(anc, "anc", _int64, here))
 
 
+def _table_rows(pt, name, least):
+    """Rows of a page table, which has to have at least so many."""
+    rows = pt.numel() // pt.shape[-1] if pt.dim() and pt.shape[-1] else 0
+    if rows < least:
+        raise ValueError(f"{name} must have a row for each sequence ({least} at least)")
+    return rows
+
+
 def dsv4sa_tree_attn_workspace_size(n_seqs: int, max_nodes: int, H: int, n_max: int, window: int) -> int:
     return int(lib().dsv4sa_tree_attn_workspace_size(n_seqs, max_nodes, H, n_max, window))
 
@@ -939,7 +947,8 @@ def dsv4sa_tree_attn(q, sink, node_start, ctx, pos, comp, comp_pt, n_vis, n_max:
     """Attention of drafted tokens: q bf16 [T, H, 512], sequence b's being rows node_start[b] ..
     node_start[b + 1] - 1 (int32 [B + 1]), over compressed entries below n_vis [T], the window of
     committed tokens (positions below ctx [B]) and the drafted rows that the bits of anc (int64 [T];
-    None: a chain) name, at draft_entry + j of the window pool (see dsv4sa.h).  comp with n_max 0,
+    None: a chain) name, at draft_entry + j of the window pool (see dsv4sa.h).  Sequence b's pages are
+    row seq_row[b] (None: b) of comp_pt and win_pt.  comp with n_max 0,
     and win with window 0 and no draft_entry, may be None.  rope_cs, rope_pos: as in the sparse attention."""
     T, H, dim = q.shape
     if dim != HEAD_DIM:
@@ -955,15 +964,17 @@ def dsv4sa_tree_attn(q, sink, node_start, ctx, pos, comp, comp_pt, n_vis, n_max:
             raise ValueError("seq_row must have an entry for each sequence")
         rows = _dev(seq_row, "seq_row", _int32, here)
     cd = cpt = wd = wpt = rcs = rpos = None
-    cpt_stride = wpt_stride = rope_rows = 0
+    cpt_stride = wpt_stride = cpt_rows = wpt_rows = rope_rows = 0
     if comp is not None:
         cd = ctypes.pointer(_pool(comp, "comp", here))
         cpt = _dev(comp_pt, "comp_pt", _int32, here)
         cpt_stride = comp_pt.shape[-1]
+        cpt_rows = _table_rows(comp_pt, "comp_pt", 1 if seq_row is not None else B) if n_max > 0 else 0
     if win is not None:
         wd = ctypes.pointer(_pool(win, "win", here))
         wpt = _dev(win_pt, "win_pt", _int32, here)
         wpt_stride = win_pt.shape[-1]
+        wpt_rows = _table_rows(win_pt, "win_pt", 1 if seq_row is not None else B) if window > 0 or draft_entry >= 0 else 0
     if rope_cs is not None:
         rcs = _table_of(rope_cs, 32, here)
         rpos = _dev(rope_pos, "rope_pos", _int32, here)
@@ -973,7 +984,8 @@ def dsv4sa_tree_attn(q, sink, node_start, ctx, pos, comp, comp_pt, n_vis, n_max:
     a = TreeArgs(_dev(q, "q", _bf16, here), T, H, float(softmax_scale), B, _dev(sink, "attn_sink", _f32, here), ns, rows, cx, ps, an,
                  _dev(n_vis, "n_vis", _int32, here), n_max, max_nodes, cd, cpt, wd, wpt, cpt_stride, wpt_stride, window, win_ring,
                  draft_entry, rope_rows, _dev(out, "out", _bf16, here), _dev(lse, "lse", _f32, here) if lse is not None else None,
-                 rcs, rpos, _dev(ws, "ws", _u8, here) if ws is not None else None, ws.numel() if ws is not None else 0)
+                 rcs, rpos, _dev(ws, "ws", _u8, here) if ws is not None else None, ws.numel() if ws is not None else 0,
+                 cpt_rows, wpt_rows)
     st = lib().dsv4sa_tree_attn(ctypes.byref(a), _stream(stream, here))
     if st:
         raise DSV4SAError("dsv4sa_tree_attn", st)

@@ -701,8 +701,8 @@ DSV4SA_API int dsv4sa_cache_append(const dsv4sa_append_args* args, cudaStream_t 
  *     draft_entry -1: no drafted rows.
  * A node without any row gets zeros (lse: the sink).  q, out and lse rows outside every
  * sequence are neither read nor written.  A sequence whose bounds do not lie within
- * [0, T] or hold more than max_nodes nodes is left out, and a page id or entry out of range
- * takes out its row; both set DSV4SA_ERR_INDEX_OOB on the device.  A row that holds an
+ * [0, T] or hold more than max_nodes nodes is left out, and a page id, an entry or a row of
+ * the page table (seq_row) out of range takes out its rows; both set DSV4SA_ERR_INDEX_OOB on the device.  A row that holds an
  * infinity or a NaN makes NaN of the nodes that see it, and of no other.
  * The pools are two of kind KV or two of kind KV_FP4 (one of each: UNSUPPORTED).  Sums and
  * partial results are fp32, P is rounded to BF16.  The lengths of the whole batch
@@ -740,6 +740,8 @@ typedef struct {
   const int32_t* rope_pos;      /* by row rope_pos[t] */
   void*        ws;              /* device workspace, 16-byte aligned; calls that share one are ordered by the caller */
   size_t       ws_bytes;
+  int32_t      comp_pt_rows;    /* rows of comp_pt and of win_pt, which seq_row is held against (without it: */
+  int32_t      win_pt_rows;     /* n_seqs); 0: not told, and not checked */
 } dsv4sa_tree_args;
 /* Workspace bytes of a call with these arguments: an upper bound over devices, 42 MB at most. */
 DSV4SA_API size_t dsv4sa_tree_attn_workspace_size(int32_t n_seqs, int32_t max_nodes, int32_t H, int32_t n_max, int32_t window);
