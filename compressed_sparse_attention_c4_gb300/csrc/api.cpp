@@ -516,7 +516,7 @@ DSV4SA_API int dsv4sa_rope(const dsv4sa_rope_args* a, cudaStream_t stream) {
 }
 
 DSV4SA_API int dsv4sa_cache_append(const dsv4sa_append_args* a, cudaStream_t stream) {
-  if (!a || a->n < 0 || a->n_src < 0 || a->pt_stride < 1 || a->ring < 0) return DSV4SA_ERR_INVALID_ARG;
+  if (!a || a->n < 0 || a->n_src < 0 || a->pt_stride < 1 || a->pt_rows < 0 || a->ring < 0) return DSV4SA_ERR_INVALID_ARG;
   if ((a->norm != 0 && a->norm != 1) || (a->norm && !(a->eps >= 0.f))) return DSV4SA_ERR_INVALID_ARG;
   if (!pool_ok(a->pool, DSV4SA_POOL_KV) && !pool_ok(a->pool, DSV4SA_POOL_KV_FP4)) return DSV4SA_ERR_INVALID_ARG;
   if (a->row_stride < DSV4SA_HEAD_DIM || a->row_stride % 8 != 0) return DSV4SA_ERR_INVALID_ARG;

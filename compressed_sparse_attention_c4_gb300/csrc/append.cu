@@ -36,6 +36,7 @@ struct AppendParams {
   uint8_t* base;
   int64_t page_stride, num_pages;
   int32_t pt_stride;
+  int32_t pt_rows;            // INT32_MAX where the caller did not say
   int32_t ring;
   int32_t n, n_src;
   int32_t rope_rows;
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
       l_pos = p.row_pos ? __ldg(p.row_pos + r) : 0;
       l_src = p.src_row ? __ldg(p.src_row + r) : static_cast<int>(r);
       const int e = p.row_entry ? __ldg(p.row_entry + r) : (p.ring > 0 && l_pos >= 0 ? l_pos % p.ring : l_pos);
-      const bool ok = l_src >= 0 && l_src < p.n_src && seq >= 0 && e >= 0 && (e >> 6) < p.pt_stride &&
+      const bool ok = l_src >= 0 && l_src < p.n_src && seq >= 0 && seq < p.pt_rows && e >= 0 && (e >> 6) < p.pt_stride &&
                       (!p.cs || (l_pos >= 0 && l_pos < p.rope_rows));
       if (ok) l_page = __ldg(p.page_table + static_cast<int64_t>(seq) * p.pt_stride + (e >> 6));
       if (l_page < 0 || l_page >= p.num_pages) {
@@ -264,6 +265,7 @@ int launch_cache_append(const dsv4sa_append_args* a, cudaStream_t stream) {
   p.page_stride = a->pool->page_stride;
   p.num_pages = a->pool->num_pages;
   p.pt_stride = a->pt_stride;
+  p.pt_rows = a->pt_rows > 0 ? a->pt_rows : INT32_MAX;
   p.ring = a->ring;
   p.n = a->n;
   p.n_src = a->n_src;

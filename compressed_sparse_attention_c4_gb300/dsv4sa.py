@@ -96,7 +96,7 @@ class AppendArgs(ctypes.Structure):
                 ("row_entry", ctypes.c_void_p), ("src_row", ctypes.c_void_p), ("rows", ctypes.c_void_p),
                 ("row_stride", ctypes.c_int64), ("n_src", ctypes.c_int32), ("n", ctypes.c_int32),
                 ("rope_cs", ctypes.c_void_p), ("rope_rows", ctypes.c_int32), ("norm", ctypes.c_int32),
-                ("norm_w", ctypes.c_void_p), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+                ("norm_w", ctypes.c_void_p), ("eps", ctypes.c_float), ("pt_rows", ctypes.c_int32)]
 
 
 class TreeArgs(ctypes.Structure):
@@ -708,6 +708,14 @@ def dsv4sa_rope(x, rope_cs, pos, out=None, rope_off=None, layout: int = ROPE_PAI
         raise DSV4SAError("dsv4sa_rope", st)
 
 
+def _table_rows(pt, name, least):
+    """Rows of a page table, which has to have at least so many."""
+    rows = pt.numel() // pt.shape[-1] if pt.dim() and pt.shape[-1] else 0
+    if rows < least:
+        raise ValueError(f"{name} must have a row for each sequence ({least} at least)")
+    return rows
+
+
 def dsv4sa_cache_append(pool: PoolDesc, page_table, row_seq, row_pos, rows, rope_cs=None, row_entry=None, ring: int = 0,
                         src_row=None, norm_w=None, eps=None, stream=None):
     """New rows bf16 [n_src, 512] (rows may be strided) of the KV projection into a KV or KV_FP4 pool:
@@ -734,9 +742,10 @@ def dsv4sa_cache_append(pool: PoolDesc, page_table, row_seq, row_pos, rows, rope
         if eps is None or norm_w.shape != (HEAD_DIM,):
             raise ValueError("norm_w must be [512], with eps")
         wp = _dev(norm_w, "norm_w", _f32, here)
+    pt_rows = _table_rows(page_table, "page_table", 1 if n else 0)
     a = AppendArgs(ctypes.pointer(_pool(pool, "pool", here)), _dev(page_table, "page_table", _int32, here), page_table.shape[-1],
                    ring, _dev(row_seq, "row_seq", _int32, here), lists[0], lists[1], lists[2], rp, rs, shape[0], n, cs,
-                   0 if rope_cs is None else rope_cs.shape[0], 0 if eps is None else 1, wp, eps or 0.0, 0)
+                   0 if rope_cs is None else rope_cs.shape[0], 0 if eps is None else 1, wp, eps or 0.0, pt_rows)
     st = lib().dsv4sa_cache_append(ctypes.byref(a), _stream(stream, here))
     if st:
         raise DSV4SAError("dsv4sa_cache_append", st)
@@ -927,14 +936,6 @@ def _nodes(node_start, ctx, pos, anc, T, here):
         raise ValueError(f"pos and anc must have an entry for each of the {T} nodes")
     return (_dev(node_start, "node_start", _int32, here), _dev(ctx, "ctx", _int32, here), _dev(pos, "pos", _int32, here),
             None if anc is None else _dev(anc, "anc", _int64, here))
-
-
-def _table_rows(pt, name, least):
-    """Rows of a page table, which has to have at least so many."""
-    rows = pt.numel() // pt.shape[-1] if pt.dim() and pt.shape[-1] else 0
-    if rows < least:
-        raise ValueError(f"{name} must have a row for each sequence ({least} at least)")
-    return rows
 
 
 def dsv4sa_tree_attn_workspace_size(n_seqs: int, max_nodes: int, H: int, n_max: int, window: int) -> int:

@@ -659,9 +659,9 @@ DSV4SA_API int dsv4sa_rope(const dsv4sa_rope_args* args, cudaStream_t stream);
  *   dims 0..447 quantised as dsv4sa_cache_write does (without norm bit for bit so)
  * It goes to entry row_entry[r] of the sequence of page-table row row_seq[r]; row_entry
  * null: row_pos[r] % ring with ring > 0 (a ring of raw tokens), else row_pos[r].
- * Rows with row_seq[r] = -1 are skipped (padding of a batch).  A row whose source, slot,
- * page id or position (of rope_cs) is out of range is skipped and sets DSV4SA_ERR_INDEX_OOB
- * on the device.  Rows that write the same slot in one call race.  Norms as in dsv4sa_rope.
+ * Rows with row_seq[r] = -1 are skipped (padding of a batch).  A row whose source, row of the
+ * page table, slot, page id or position (of rope_cs) is out of range is skipped and sets
+ * DSV4SA_ERR_INDEX_OOB on the device.  Rows that write the same slot in one call race.  Norms as in dsv4sa_rope.
  */
 typedef struct {
   const dsv4sa_pool_desc* pool;   /* KV or KV_FP4 */
@@ -681,7 +681,7 @@ typedef struct {
   int32_t      norm;              /* 0, 1 */
   const float* norm_w;            /* optional device fp32 [512], 16-byte aligned */
   float        eps;
-  int32_t      reserved;
+  int32_t      pt_rows;           /* rows of page_table, which row_seq is held against; 0: not told, and not checked */
 } dsv4sa_append_args;
 DSV4SA_API int dsv4sa_cache_append(const dsv4sa_append_args* args, cudaStream_t stream);
 

@@ -7,8 +7,8 @@ import pytest
 
 from test_abi_cpu import HEADER
 from test_binding_devices_cpu import bf16, f32, i32, on
-from test_cache_norm_cpu import INVALID, pool, ptr
-from test_drafts_cpu import L, WORKSPACE, gpu0, tree_args  # noqa: F401
+from test_cache_norm_cpu import INVALID, OK, pool, ptr
+from test_drafts_cpu import L, WORKSPACE, append_args, gpu0, tree_args  # noqa: F401
 
 
 def tree_call(L, B, comp_rows, win_rows, seq_row=None, n_max=9, window=128, draft=128):
@@ -43,7 +43,23 @@ def test_tree_call_counts_table_rows(L):
         assert st(n_seqs=2, **bad) == INVALID, bad
 
 
-@pytest.mark.parametrize("struct,name,fields", [("TreeArgs", "dsv4sa_tree_args", ["seq_row", "ws_bytes", "comp_pt_rows", "win_pt_rows"])])
+def test_append_counts_table_rows(L, gpu0):
+    rows, seq = on((5, 512), bf16), on((5,), i32)
+    L.dsv4sa_cache_append(L.PoolDesc(), on((2, 4), i32), seq, seq, rows)
+    L.dsv4sa_cache_append(L.PoolDesc(), on((0, 4), i32), seq[:0], seq[:0], rows[:0])
+    with pytest.raises(ValueError, match="row"):
+        L.dsv4sa_cache_append(L.PoolDesc(), on((0, 4), i32), seq, seq, rows)
+    assert L.lib.reached == ["dsv4sa_cache_append"] * 2
+
+
+def test_append_call_refuses_negative_table_rows(L):
+    p = pool(L, L.POOL_KV, 1)
+    assert L.lib().dsv4sa_cache_append(ctypes.byref(append_args(L, p, n=0, pt_rows=3)), None) == OK
+    assert L.lib().dsv4sa_cache_append(ctypes.byref(append_args(L, p, pt_rows=-1)), None) == INVALID
+
+
+@pytest.mark.parametrize("struct,name,fields", [("TreeArgs", "dsv4sa_tree_args", ["seq_row", "ws_bytes", "comp_pt_rows", "win_pt_rows"]),
+                                                ("AppendArgs", "dsv4sa_append_args", ["row_entry", "norm_w", "eps", "pt_rows"])])
 def test_struct_is_the_headers(L, tmp_path, struct, name, fields):
     """The binding's structure has the header's size and offsets."""
     src, exe = tmp_path / "s.c", tmp_path / "s"
