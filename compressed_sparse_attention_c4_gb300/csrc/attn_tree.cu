@@ -116,13 +116,16 @@ struct alignas(16) Item {
   int32_t cols;
   int32_t col0;              // first row of its sequence's queries
   int32_t nv_max, nv_min;    // entries that any, that every node sees
-  uint32_t win_rows, rows;   // rows of the window; all rows
-  int64_t win_lo;            // the window's first position
+  uint32_t win_rows, rows;   // rows of the windows; all rows
+  int32_t runs;              // of consecutive positions that the windows' rows are
   int32_t seq_comp, seq_win; // its row of each page table, -1: not a row of it
   int32_t last_cta;          // the CTA that has the item's last chunk
   int32_t nv[kN], lo[kN], hi[kN];   // by column: entries, first and last position of the window
   uint64_t anc[kN];
+  uint64_t any;              // drafted rows that some node sees
   int32_t rope[kN];          // row of the rotation table, -1: none
+  uint32_t run_row[kN];      // a run's first row among the windows', and its first position less that
+  int32_t run_shift[kN];
 };
 
 struct SmemT {
@@ -158,18 +161,29 @@ __device__ __forceinline__ uint64_t ancestors_of(const TreeParams& p, int s0, in
   const uint64_t a = p.anc ? __ldg(p.anc + s0 + node) : (uint64_t(2) << node) - 1;
   return a & (nodes == 64 ? ~uint64_t(0) : (uint64_t(1) << nodes) - 1);
 }
-// Rows of an item: entries, window [lo, lo + n) and drafted rows.
-struct Span {
-  int64_t win_lo;
-  uint32_t win_rows, rows;
-};
-__device__ __forceinline__ Span span_of(const TreeParams& p, int ctx, int nv_max, int pos_min, int pos_max, uint64_t anc) {
-  Span s;
-  const int64_t lo = static_cast<int64_t>(pos_min) - p.window + 1, hi = min(ctx, pos_max + 1);
-  s.win_lo = lo > 0 ? lo : 0;
-  s.win_rows = p.window > 0 && hi > s.win_lo ? static_cast<uint32_t>(hi - s.win_lo) : 0u;
-  s.rows = static_cast<uint32_t>(nv_max) + s.win_rows + static_cast<uint32_t>(64 - __clzll(static_cast<long long>(anc)));
-  return s;
+// The committed rows that an item's nodes see are the union of their windows, usually one run of
+// consecutive positions; where nodes lie further apart than a window there are more runs.
+// lo and hi are the lowest and the highest position, of those that are not negative (hi < 0: there is none).
+// Of positions this close the windows leave no gap.
+__device__ __forceinline__ bool one_run(uint32_t lo, int hi, int window) { return hi - static_cast<int>(lo) <= window; }
+__device__ __forceinline__ int run_start(int pos, int window) { return max(pos - window + 1, 0); }
+// Rows of the windows of n nodes: exact for one run; else no fewer, for dealing out chunks.
+__device__ __forceinline__ uint32_t run_rows(uint32_t lo, int hi, int n, int window, int ctx) {
+  if (hi < 0 || window == 0) return 0;
+  const uint32_t range = static_cast<uint32_t>(max(min(hi + 1, max(ctx, 0)) - run_start(static_cast<int>(lo), window), 0));
+  return one_run(lo, hi, window) ? range : min(range, static_cast<uint32_t>(n) * static_cast<uint32_t>(window));
+}
+__device__ __forceinline__ uint32_t rows_of(int nv_max, uint32_t win_rows, uint64_t anc) {
+  return static_cast<uint32_t>(nv_max) + win_rows + static_cast<uint32_t>(64 - __clzll(static_cast<long long>(anc)));
+}
+// Position of row e of an item's windows.
+__device__ __forceinline__ uint32_t position_of(const Item* it, uint32_t e) {
+  int s = it->runs - 1;
+  if (s > 0) {
+#pragma unroll 1
+    while (e < it->run_row[s]) --s;
+  }
+  return e + static_cast<uint32_t>(it->run_shift[s]);
 }
 __device__ __forceinline__ int chunks_of(uint32_t rows) { return rows == 0 ? 1 : static_cast<int>((rows + kRows - 1) / kRows); }
 // A position as the masks use it: below 2^31 - 1, -1 for any that is negative.
@@ -177,10 +191,11 @@ __device__ __forceinline__ int pos_of(int pos) { return min(max(pos, -1), 0x7FFF
 
 // Chunks of item (b, k), by one thread: eight nodes' values are on the way at a time.
 __device__ __forceinline__ int chunks_of_item(const TreeParams& p, int s0, int nodes, int ctx, int k) {
-  int nv = 0, lo = 0x7FFFFFFE, hi = -1;
+  uint32_t lo = ~0u;         // a position of -1 is above all others
+  int nv = 0, hi = -1;
   uint64_t anc = 0;
-  const int last = min(nodes - 1, ((k + 1) * kN - 1) / p.H);
-  for (int n0 = k * kN / p.H; n0 <= last; n0 += 8) {
+  const int first = k * kN / p.H, last = min(nodes - 1, ((k + 1) * kN - 1) / p.H);
+  for (int n0 = first; n0 <= last; n0 += 8) {
     int v[8], pos[8];
     uint64_t a[8];
 #pragma unroll
@@ -194,12 +209,12 @@ __device__ __forceinline__ int chunks_of_item(const TreeParams& p, int s0, int n
     for (int i = 0; i < 8; ++i) {
       const int at = pos_of(pos[i]);
       nv = max(nv, min(v[i], p.n_max));
-      lo = min(lo, at);
+      lo = min(lo, static_cast<uint32_t>(at));
       hi = max(hi, at);
       anc |= a[i];
     }
   }
-  return chunks_of(span_of(p, ctx, nv, lo, hi, anc).rows);
+  return chunks_of(rows_of(nv, run_rows(lo, hi, last - first + 1, p.window, ctx), anc));
 }
 
 // a b / c, all below 2^63 c; without a 64-bit division where that is possible
@@ -319,28 +334,20 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
     }
     // no more CTAs than there is to deal out, so that every CTA between an item's first and last has a piece of it
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total), g = blockIdx.x;
-    if (total == 0) {
-      // no sequence has a node: nothing for any CTA
-    } else if (all_items <= ctas && longest <= (total + ctas - 1) / ctas + kWholeSlack) {
-      // a CTA for each item, none is cut
-      if (before_items <= g && g < before_items + mine_items) {
-        item = i0;
-        const int64_t at = per > 1 ? walk(INT64_MAX, static_cast<int>(g) - before_items, item, before) : before;
-        first[0] = item;
-        first[1] = first[2] = at;
-        first[3] = at + size;
-      }
-    } else {
-      const int64_t w0 = g < ctas ? scaled(total, g, ctas) : total, w1 = g < ctas ? scaled(total, g + 1, ctas) : total;
-      if (w0 < w1 && before <= w0 && w0 < before + mine) {
-        item = i0;
-        const int64_t at = per > 1 ? walk(w0, -1, item, before) : before;    // what lies before the item
-        const bool step = w0 - at >= size - kItemStep;      // only its last step: that is another CTA's
-        first[0] = step ? item + 1 : item;
-        first[1] = step ? at + size : at;
-        first[2] = step ? at + size : w0;
-        first[3] = w1;
-      }
+    // its item is this thread's where the thread counted it: number g of all items, left whole, or the one that has
+    // chunk w0 of all; none where no sequence has a node
+    const bool whole = total > 0 && all_items <= ctas && longest <= (total + ctas - 1) / ctas + kWholeSlack;
+    int64_t w0 = total, w1 = total;
+    if (!whole && g < ctas) w0 = scaled(total, g, ctas), w1 = scaled(total, g + 1, ctas);
+    if (whole ? before_items <= g && g < before_items + mine_items : w0 < w1 && before <= w0 && w0 < before + mine) {
+      item = i0;
+      const int64_t at = per > 1 ? walk(whole ? INT64_MAX : w0, whole ? static_cast<int>(g) - before_items : -1, item, before) : before;
+      if (whole) w0 = at, w1 = at + size;
+      const bool step = w0 - at >= size - kItemStep;        // only its last step: that is another CTA's
+      first[0] = step ? item + 1 : item;
+      first[1] = step ? at + size : at;
+      first[2] = step ? at + size : w0;
+      first[3] = w1;
     }
     if (tid == 0) first[4] = total;
     __syncthreads();
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
       int c = it->c0;
       if (c == c1) break;
       const uint32_t nv_max = static_cast<uint32_t>(it->nv_max), rows = it->rows;
-      // the row's page (1024-byte aligned) and its slot, 0: no row
+      // the row's page (1024-byte aligned) and its slot; 0: no row, or its page is out of range
       auto locate = [&](int ch) -> uint64_t {
         const uint32_t rr = static_cast<uint32_t>(ch) * kRows + row;
         if (rr >= rows) return 0;
@@ -388,7 +395,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
         }
         uint32_t e = rr - nv_max;
         if (e < it->win_rows) {
-          const uint32_t at = static_cast<uint32_t>(it->win_lo) + e;
+          const uint32_t at = position_of(it, e);
           e = p.win_ring > 0 ? at % static_cast<uint32_t>(p.win_ring) : at;
         } else {
           e = static_cast<uint32_t>(p.draft_entry) + (e - it->win_rows);
@@ -441,7 +448,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
           if (h == 0) {
             const uint32_t bits = __ballot_sync(0xffffffffu, bad);
             if (lane == 0) bad_rows[warp - 8] = bits;
-            if (bits != 0 && lane == 0) raise_error(kErrIndex);
+            if (bits != 0) {               // of a drafted row that no node sees it does not matter
+              const uint32_t draft = static_cast<uint32_t>(c) * kRows + row - nv_max - it->win_rows;
+              if (bad && (draft >= 64 || (it->any >> draft & 1) != 0)) raise_error(kErrIndex);
+            }
           }
           if constexpr (kFp4) {
 #pragma unroll
@@ -587,7 +597,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
         int chunks = 0;
         if (more) {
           const int ctx = __ldg(p.ctx + b), seq = p.seq_row ? __ldg(p.seq_row + b) : b;
-          int nv_max = 0, nv_min = 0x7FFFFFFF, lo = 0x7FFFFFFE, hi = -1, nvc[2], posc[2], nodec[2];
+          uint32_t lo = ~0u;
+          int nv_max = 0, nv_min = INT32_MAX, hi = -1, nvc[2], posc[2], nodec[2];
           uint64_t ancc[2], anc = 0;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -599,7 +610,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
             ancc[j] = ancestors_of(p, s0, node, nodes);
             nv_max = max(nv_max, nvc[j]);
             nv_min = min(nv_min, nvc[j]);
-            lo = min(lo, posc[j]);
+            lo = min(lo, static_cast<uint32_t>(posc[j]));
             hi = max(hi, posc[j]);
             anc |= ancc[j];
           }
@@ -609,8 +620,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
           hi = __reduce_max_sync(0xffffffffu, hi);
           anc = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(anc >> 32))) << 32 |
                 __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(anc));
-          const Span sp = span_of(p, ctx, nv_max, lo, hi, anc);
-          chunks = chunks_of(sp.rows);
+          uint32_t win_rows = run_rows(lo, hi, (k * kN + cols - 1) / p.H - k * kN / p.H + 1, p.window, ctx);
+          chunks = chunks_of(rows_of(nv_max, win_rows, anc));
           if (warp == kSchedWarp) {
             if (n_item >= 2 && ok) ok = warp_wait(bar_done + (n_item & 1), ((n_item >> 1) - 1) & 1);
             Item* it = items + (n_item & 1);
@@ -631,6 +642,32 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
               }
               it->rope[col] = r;
             }
+            int runs = 1;
+            if (lane == 0) it->run_shift[0] = run_start(static_cast<int>(lo), p.window);
+            if (win_rows > 0 && !one_run(lo, hi, p.window)) {
+              // the union, position by position: `end` is behind the last run
+              int end = 0;
+              runs = 0;
+              win_rows = 0;
+#pragma unroll 1
+              for (int x = -1;;) {
+                int next = INT32_MAX;              // the lowest position above x
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (posc[j] > x) next = min(next, posc[j]);
+                x = __reduce_min_sync(0xffffffffu, next);
+                if (x == INT32_MAX) break;
+                const int from = run_start(x, p.window), to = min(x + 1, ctx);
+                if (to <= max(from, end)) continue;
+                if (runs == 0 || from > end) {
+                  if (lane == 0) it->run_row[runs] = win_rows, it->run_shift[runs] = from - static_cast<int>(win_rows);
+                  ++runs;
+                  end = from;
+                }
+                win_rows += static_cast<uint32_t>(to - end);
+                end = to;
+              }
+            }
             if (lane == 0) {
               const int64_t end = min(base + chunks, w1);
               it->c0 = static_cast<int>(at - base);
@@ -641,9 +678,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
               it->col0 = k * kN;
               it->nv_max = nv_max;
               it->nv_min = nv_min;
-              it->win_rows = sp.win_rows;
-              it->rows = sp.rows;
-              it->win_lo = sp.win_lo;
+              it->win_rows = win_rows;
+              it->rows = rows_of(nv_max, win_rows, anc);
+              it->any = anc;
+              it->runs = runs;
               it->seq_comp = seq < p.comp_pt_rows ? seq : -1;
               it->seq_win = seq < p.win_pt_rows ? seq : -1;
               const int64_t x = (base + chunks) * ctas - 1;   // the CTA that has the item's last chunk
@@ -713,7 +751,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_attn_kernel(const TreeParam
 #pragma unroll 4
             for (int i = 0; i < kHW; ++i) seen |= (rr < static_cast<uint32_t>(it->nv[hb + i]) ? 1u : 0u) << i;
           } else if (rr < win_end) {
-            const int at = static_cast<int>(it->win_lo) + static_cast<int>(rr - nv_max);
+            const int at = static_cast<int>(position_of(it, rr - nv_max));
 #pragma unroll 4
             for (int i = 0; i < kHW; ++i) seen |= (at >= it->lo[hb + i] && at <= it->hi[hb + i] ? 1u : 0u) << i;
           } else if (rr < it->rows) {

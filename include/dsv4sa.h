@@ -699,6 +699,8 @@ DSV4SA_API int dsv4sa_cache_append(const dsv4sa_append_args* args, cudaStream_t 
  *     bits at and above the sequence's nodes count nothing): entry draft_entry + j of the
  *     window pool, where dsv4sa_cache_append put them.  anc null: a chain, bits 0..j;
  *     draft_entry -1: no drafted rows.
+ * A position below 0 has no window.  Nodes may lie any distance apart: the rows between their
+ * windows are not read, and rows that no node sees may be without a page.
  * A node without any row gets zeros (lse: the sink).  q, out and lse rows outside every
  * sequence are neither read nor written.  A sequence whose bounds do not lie within
  * [0, T] or hold more than max_nodes nodes is left out, and a page id, an entry or a row of
