@@ -17,8 +17,9 @@ constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------- table
 // An angle is a phase: w_i / 2 pi as a 64-bit fraction of a turn, times the position, modulo
-// 2^64.  Whole turns drop out exactly, so a position of 2^40 costs no more precision than one of
-// 1.  The nearest quarter turn is taken off in whole numbers, too; what is left, at most an eighth of a
+// 2^64.  Whole turns drop out exactly; the fraction is the nearest one, half a step of 2^-64 turn off,
+// so position n is off by at most n 2^-62.3 (2^-31 at the last 31-bit position, 2^-24, fp32's own
+// rounding, at 2^38).  A frequency in fp64 would be off by n 2^-53.  The nearest quarter turn is taken off in whole numbers, too; what is left, at most an eighth of a
 // turn with 64 bits below the point, is rounded to fp32 and goes through the Taylor series of
 // sine and cosine (to x^9 and x^10: 2^-28 and 2^-32 at pi / 4).  A thread keeps one pair and
 // adds a constant phase from row to row.  Bound by HBM (written once) and instructions both: 1M rows
@@ -205,6 +206,28 @@ cudaError_t launch_rope_lu(const RopeParams& p, bool norm, bool halves, cudaStre
 
 }  // namespace
 
+// Pairs of doubles, hi + lo with |lo| at most half a step of hi: about 100 bits (Dekker, "A
+// floating-point technique for extending the available precision", 1971; the product by fma).
+struct Two {
+  double hi, lo;
+};
+static Two sum_of(double a, double b) {    // |a| >= |b|
+  const double s = a + b;
+  return {s, b - (s - a)};
+}
+static Two add(Two a, Two b) {
+  const double s = a.hi + b.hi, t = s - a.hi;
+  return sum_of(s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo));
+}
+static Two mul(Two a, Two b) {
+  const double p = a.hi * b.hi;
+  return sum_of(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+static Two ratio(double a, double b) {
+  const double q = a / b;
+  return {q, std::fma(-q, b, a) / b};
+}
+
 int launch_rope_table(float* cs, int64_t rows, int32_t pairs, int64_t first, double base, double factor,
                       int64_t original_len, double beta_fast, double beta_slow, cudaStream_t stream) {
   constexpr double kPi = 3.14159265358979323846;
@@ -223,12 +246,21 @@ int launch_rope_table(float* cs, int64_t rows, int32_t pairs, int64_t first, dou
     lo = std::fmax(std::floor(border(beta_fast)), 0.0);
     hi = std::fmin(std::ceil(border(beta_slow)), d - 1);
   }
-  for (int32_t i = 0; i < pairs; ++i) {
-    const double w = std::pow(base, -2.0 * i / d);
-    double keep = 0;        // original_len 0: every frequency is divided (positions interpolated)
-    if (original_len > 0) keep = 1 - std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
-    const double scaled = factor == 1.0 ? w : w / factor * (1 - keep) + w * keep;
-    p.turn[i] = static_cast<uint64_t>(std::ldexp(scaled / (2 * kPi), 64));
+  // base^(-1 / pairs): fp64's, and one step of Newton's on base x^pairs = 1
+  const double near = std::pow(base, -1.0 / pairs);
+  Two p2 = {near, 0}, power = {base, 0};
+  for (int32_t n = pairs; n > 0; n >>= 1, p2 = mul(p2, p2))
+    if (n & 1) power = mul(power, p2);
+  const Two root = mul({near, 0}, add({1, 0}, {-add(power, {-1, 0}).hi / pairs, 0}));
+  const Two shrink = ratio(1.0, factor), per_turn = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};   // 1 / factor, 1 / 2 pi
+  Two w = {1, 0};
+  for (int32_t i = 0; i < pairs; ++i, w = mul(w, root)) {
+    // the part of w that is divided; original_len 0: all (positions interpolated)
+    Two part = {1, 0};
+    if (original_len > 0) part = i <= lo ? Two{0, 0} : i >= hi ? Two{1, 0} : ratio(i - lo, hi - lo);
+    const Two turns = mul(mul(w, add(add({1, 0}, {-part.hi, -part.lo}), mul(shrink, part))), per_turn);
+    const double x = std::ldexp(turns.hi, 64), whole = std::floor(x);       // below 2^62
+    p.turn[i] = static_cast<uint64_t>(whole) + static_cast<uint64_t>(std::llround((x - whole) + std::ldexp(turns.lo, 64)));
   }
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSV4SA_ERR_CUDA;

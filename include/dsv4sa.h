@@ -602,9 +602,9 @@ DSV4SA_API int dsv4sa_rmsnorm_quant(const void* x, int64_t x_stride, const void*
  *                      hi = min(ceil(at(beta_slow)), 2 pairs - 1), at(beta) = 2 pairs *
  *                      ln(original_len / (2 pi beta)) / (2 ln base)
  * What the attention, the compressor, dsv4sa_rope and dsv4sa_cache_append take as
- * rope_cs (those of 512 dims with pairs = 32).  Frequencies are fp64; an angle is
- * reduced to a part of a turn without rounding (64 bits), then rounded to fp32
- * once, so far positions are as exact as near ones.
+ * rope_cs (those of 512 dims with pairs = 32).  A frequency is the nearest 64-bit part
+ * of a turn, whole turns are taken off exactly, and what is left of an angle is fp32: off by
+ * position * 2^-62 at most before that rounding (2^-31 at the last 31-bit position, 2^-24 at 2^38).
  *   cs      device fp32 [rows][pairs][2], 8-byte aligned
  *   pairs   1..DSV4SA_MAX_ROPE_PAIRS;  base > 1;  factor >= 1;  first >= 0
  */
