@@ -542,8 +542,9 @@ DSV4SA_API int dsv4sa_tree_attn(const dsv4sa_tree_args* a, cudaStream_t stream) 
     return DSV4SA_ERR_INVALID_ARG;
   if (a->H < 1 || a->H > DSV4SA_MAX_HEADS || a->max_nodes > DSV4SA_MAX_TREE_NODES) return DSV4SA_ERR_UNSUPPORTED;
   if (a->n_max > (1 << 29) || a->window > DSV4SA_MAX_TREE_WINDOW || a->draft_entry > (1 << 30)) return DSV4SA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(a->T) * a->H >= (int64_t{1} << 31) ||
-      static_cast<int64_t>(a->n_seqs) * ((static_cast<int64_t>(a->max_nodes) * a->H + 63) / 64) >= (int64_t{1} << 31))
+  // beyond these a warp's search through empty sequences could outlast the other warps' wait for it
+  if (a->n_seqs > (1 << 24) || static_cast<int64_t>(a->T) * a->H >= (int64_t{1} << 31) ||
+      static_cast<int64_t>(a->n_seqs) * ((static_cast<int64_t>(a->max_nodes) * a->H + 63) / 64) > (int64_t{1} << 28))
     return DSV4SA_ERR_UNSUPPORTED;
   if (a->T == 0 || a->n_seqs == 0 || a->max_nodes == 0) return DSV4SA_OK;
   if (!a->q || !a->out || !aligned(a->q, 16) || !aligned(a->out, 16) || !words(a->attn_sink) || !aligned(a->lse, 4)) return DSV4SA_ERR_INVALID_ARG;

@@ -716,7 +716,7 @@ typedef struct {
   int32_t      T;
   int32_t      H;               /* 1..128 */
   float        softmax_scale;
-  int32_t      n_seqs;
+  int32_t      n_seqs;          /* <= 2^24; n_seqs * ceil(max_nodes * H / 64) <= 2^28, T * H < 2^31 */
   const float* attn_sink;       /* device fp32 [H] */
   const int32_t* node_start;    /* device int32 [n_seqs + 1] */
   const int32_t* seq_row;       /* device int32 [n_seqs]: page-table row (of both tables); null: b */
