@@ -496,6 +496,11 @@ DSV4SA_API int dsv4sa_rope(const dsv4sa_rope_args* a, cudaStream_t stream) {
   const int64_t ot = T > 1 ? a->out_tok_stride : 0, oh = H > 1 ? a->out_head_stride : 0;
   for (const int64_t s : {xt, xh, ot, oh})
     if (s < 0 || s % 8 != 0 || s > most) return DSV4SA_ERR_INVALID_ARG;
+  // no span of tokens or heads is longer than that either, so the sums below stay within 64 bits
+  for (const int64_t s : {xt, ot})
+    if (T > 1 && s > most / (T - 1)) return DSV4SA_ERR_INVALID_ARG;
+  for (const int64_t s : {xh, oh})
+    if (H > 1 && s > most / (H - 1)) return DSV4SA_ERR_INVALID_ARG;
   // the rows of out lie apart: heads within a token, or tokens within a head
   if (!((H == 1 || oh >= dim) && (T == 1 || ot >= (H - 1) * oh + dim)) && !((T == 1 || ot >= dim) && (H == 1 || oh >= (T - 1) * ot + dim)))
     if (T > 0) return DSV4SA_ERR_INVALID_ARG;

@@ -628,7 +628,7 @@ DSV4SA_API int dsv4sa_rope_table(float* cs, int64_t rows, int32_t pairs, int64_t
 #define DSV4SA_ROPE_PAIRS 0
 #define DSV4SA_ROPE_HALVES 1
 typedef struct {
-  const void*  x;              /* bf16, 16-byte aligned; strides in values, multiples of 8 */
+  const void*  x;              /* bf16, 16-byte aligned; strides in values, multiples of 8, spans <= 2^40 */
   int64_t      x_tok_stride;
   int64_t      x_head_stride;
   void*        out;            /* bf16; x itself with x's strides (in place), or apart from it */
