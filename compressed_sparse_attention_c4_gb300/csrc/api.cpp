@@ -646,12 +646,13 @@ DSV4SA_API int dsv4sa_selftest_wait_timeout(int32_t* result, cudaStream_t stream
 
 DSV4SA_API int dsv4sa_check_errors(cudaStream_t stream, uint32_t* bits_out) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return DSV4SA_ERR_CUDA;
-  const uint32_t bits = dsv4sa::read_error_word_indexer(stream, true) | dsv4sa::read_error_word_topk(stream, true) |
-                        dsv4sa::read_error_word_attn(stream, true) | dsv4sa::read_error_word_attn_decode(stream, true) |
-                        dsv4sa::read_error_word_writer(stream, true) |
-                        dsv4sa::read_error_word_compress(stream, true) | dsv4sa::read_error_word_pages(stream, true) |
-                        dsv4sa::read_error_word_attn_fp4(stream, true) | dsv4sa::read_error_word_rope(stream, true) |
-                        dsv4sa::read_error_word_append(stream, true) | dsv4sa::read_error_word_attn_tree(stream, true);
+  uint32_t* const words[dsv4sa::kErrorWords] = {
+      dsv4sa::error_word_indexer(), dsv4sa::error_word_topk(), dsv4sa::error_word_attn(), dsv4sa::error_word_attn_decode(),
+      dsv4sa::error_word_attn_fp4(), dsv4sa::error_word_attn_tree(), dsv4sa::error_word_writer(), dsv4sa::error_word_compress(),
+      dsv4sa::error_word_pages(), dsv4sa::error_word_rope(), dsv4sa::error_word_append()};
+  uint32_t bits = 0;
+  const int rc = dsv4sa::collect_errors(words, &bits, stream);
+  if (rc != DSV4SA_OK) return rc;
   if (cudaGetLastError() != cudaSuccess) return DSV4SA_ERR_CUDA;
   if (bits_out) *bits_out = bits;
   if (bits & 2u) return DSV4SA_ERR_DEVICE_TIMEOUT;

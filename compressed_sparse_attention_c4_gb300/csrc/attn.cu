@@ -871,16 +871,6 @@ int launch_topk_sparse_attn(const dsv4sa_attn_args* a, const float* logits, int6
   return launch_sparse_attn(DSV4SA_ATTN_DECODE, a, stream);
 }
 
-uint32_t read_error_word_attn(cudaStream_t stream, bool clear) {
-  uint32_t v = 0;
-  cudaMemcpyFromSymbolAsync(&v, g_err_word, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
-  cudaStreamSynchronize(stream);
-  if (clear && v) {
-    const uint32_t z = 0;
-    cudaMemcpyToSymbolAsync(g_err_word, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
-    cudaStreamSynchronize(stream);
-  }
-  return v;
-}
+uint32_t* error_word_attn() { return error_word(); }
 
 }  // namespace dsv4sa

@@ -1040,16 +1040,6 @@ int launch_decode_cluster(const AttnParams& p, int hn, int groups, cudaStream_t 
 
 }  // namespace attn
 
-uint32_t read_error_word_attn_decode(cudaStream_t stream, bool clear) {
-  uint32_t v = 0;
-  cudaMemcpyFromSymbolAsync(&v, g_err_word, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
-  cudaStreamSynchronize(stream);
-  if (clear && v) {
-    const uint32_t z = 0;
-    cudaMemcpyToSymbolAsync(g_err_word, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
-    cudaStreamSynchronize(stream);
-  }
-  return v;
-}
+uint32_t* error_word_attn_decode() { return error_word(); }
 
 }  // namespace dsv4sa

@@ -1019,16 +1019,6 @@ int launch_fp4(int32_t mode, AttnParams& p, cudaStream_t stream) {
 
 }  // namespace attn
 
-uint32_t read_error_word_attn_fp4(cudaStream_t stream, bool clear) {
-  uint32_t v = 0;
-  cudaMemcpyFromSymbolAsync(&v, g_err_word, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
-  cudaStreamSynchronize(stream);
-  if (clear && v) {
-    const uint32_t z = 0;
-    cudaMemcpyToSymbolAsync(g_err_word, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
-    cudaStreamSynchronize(stream);
-  }
-  return v;
-}
+uint32_t* error_word_attn_fp4() { return error_word(); }
 
 }  // namespace dsv4sa

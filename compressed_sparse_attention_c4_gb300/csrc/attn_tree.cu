@@ -1202,16 +1202,6 @@ int launch_tree_window_indices(const int32_t* node_start, const int32_t* ctx, co
              : DSV4SA_ERR_CUDA;
 }
 
-uint32_t read_error_word_attn_tree(cudaStream_t stream, bool clear) {
-  uint32_t v = 0;
-  cudaMemcpyFromSymbolAsync(&v, g_err_word, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
-  cudaStreamSynchronize(stream);
-  if (clear && v) {
-    const uint32_t z = 0;
-    cudaMemcpyToSymbolAsync(g_err_word, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
-    cudaStreamSynchronize(stream);
-  }
-  return v;
-}
+uint32_t* error_word_attn_tree() { return error_word(); }
 
 }  // namespace dsv4sa

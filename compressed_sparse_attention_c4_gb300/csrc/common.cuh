@@ -26,8 +26,14 @@ constexpr uint32_t kErrTimeout = 2u;
 constexpr uint32_t kErrPages = 4u;    // no free page was left
 
 // One error word per translation unit (internal linkage); each .cu file
-// exposes a host reader for its own copy (see dsv4sa_internal.h).
+// exposes the address of its own copy (see dsv4sa_internal.h).
 static __device__ uint32_t g_err_word;
+
+// On the current device; null where it cannot be had.
+static inline uint32_t* error_word() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_err_word) == cudaSuccess ? static_cast<uint32_t*>(p) : nullptr;
+}
 
 __device__ __forceinline__ void raise_error(uint32_t bits) { atomicOr(&g_err_word, bits); }
 

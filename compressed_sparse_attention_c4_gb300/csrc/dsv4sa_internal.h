@@ -61,17 +61,21 @@ inline bool attn_over_fp4(const dsv4sa_attn_args* a) {
   return d && d->kind == DSV4SA_POOL_KV_FP4;
 }
 
-uint32_t read_error_word_indexer(cudaStream_t stream, bool clear);
-uint32_t read_error_word_topk(cudaStream_t stream, bool clear);
-uint32_t read_error_word_attn(cudaStream_t stream, bool clear);
-uint32_t read_error_word_attn_decode(cudaStream_t stream, bool clear);
-uint32_t read_error_word_writer(cudaStream_t stream, bool clear);
-uint32_t read_error_word_compress(cudaStream_t stream, bool clear);
-uint32_t read_error_word_attn_fp4(cudaStream_t stream, bool clear);
-uint32_t read_error_word_pages(cudaStream_t stream, bool clear);
-uint32_t read_error_word_rope(cudaStream_t stream, bool clear);
-uint32_t read_error_word_append(cudaStream_t stream, bool clear);
-uint32_t read_error_word_attn_tree(cudaStream_t stream, bool clear);
+// The error words of the current device, one in each kernel file that raises errors (null: not to be had).
+uint32_t* error_word_indexer();
+uint32_t* error_word_topk();
+uint32_t* error_word_attn();
+uint32_t* error_word_attn_decode();
+uint32_t* error_word_writer();
+uint32_t* error_word_compress();
+uint32_t* error_word_attn_fp4();
+uint32_t* error_word_pages();
+uint32_t* error_word_rope();
+uint32_t* error_word_append();
+uint32_t* error_word_attn_tree();
+constexpr int kErrorWords = 11;
+// Their bits, read and cleared on the stream, which is waited for.
+int collect_errors(uint32_t* const (&words)[kErrorWords], uint32_t* bits, cudaStream_t stream);
 int launch_selftest_wait_timeout(int32_t* result, cudaStream_t stream);
 int launch_compress_windows(const void* kv, const void* score, int64_t tok_stride, int64_t n_tok,
                             const int32_t* first_tok,

@@ -1018,16 +1018,6 @@ int launch_indexer_logits_fp4(const dsv4sa_pool_desc* kpool, const int32_t* page
   return err == cudaSuccess ? DSV4SA_OK : DSV4SA_ERR_CUDA;
 }
 
-uint32_t read_error_word_indexer(cudaStream_t stream, bool clear) {
-  uint32_t v = 0;
-  cudaMemcpyFromSymbolAsync(&v, g_err_word, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
-  cudaStreamSynchronize(stream);
-  if (clear && v) {
-    const uint32_t z = 0;
-    cudaMemcpyToSymbolAsync(g_err_word, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
-    cudaStreamSynchronize(stream);
-  }
-  return v;
-}
+uint32_t* error_word_indexer() { return error_word(); }
 
 }  // namespace dsv4sa

@@ -639,16 +639,6 @@ int launch_cache_compact(const dsv4sa_cache_desc* src, const dsv4sa_cache_desc* 
                          0, stream, c));
 }
 
-uint32_t read_error_word_pages(cudaStream_t stream, bool clear) {
-  uint32_t v = 0;
-  cudaMemcpyFromSymbolAsync(&v, g_err_word, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
-  cudaStreamSynchronize(stream);
-  if (clear && v) {
-    const uint32_t z = 0;
-    cudaMemcpyToSymbolAsync(g_err_word, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
-    cudaStreamSynchronize(stream);
-  }
-  return v;
-}
+uint32_t* error_word_pages() { return error_word(); }
 
 }  // namespace dsv4sa

@@ -648,17 +648,7 @@ int launch_topk(const float* logits, int64_t logits_stride, const int32_t* n_vis
   return DSV4SA_OK;
 }
 
-uint32_t read_error_word_topk(cudaStream_t stream, bool clear) {
-  uint32_t v = 0;
-  cudaMemcpyFromSymbolAsync(&v, g_err_word, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
-  cudaStreamSynchronize(stream);
-  if (clear && v) {
-    const uint32_t z = 0;
-    cudaMemcpyToSymbolAsync(g_err_word, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
-    cudaStreamSynchronize(stream);
-  }
-  return v;
-}
+uint32_t* error_word_topk() { return error_word(); }
 
 }  // namespace dsv4sa
 
