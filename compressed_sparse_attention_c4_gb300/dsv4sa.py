@@ -708,12 +708,13 @@ def dsv4sa_rope(x, rope_cs, pos, out=None, rope_off=None, layout: int = ROPE_PAI
         raise DSV4SAError("dsv4sa_rope", st)
 
 
-def _table_rows(pt, name, least):
-    """Rows of a page table, which has to have at least so many."""
-    rows = pt.numel() // pt.shape[-1] if pt.dim() and pt.shape[-1] else 0
+def _page_table(pt, name, least, here):
+    """Address, entries a row and rows of a page table, which has to have at least so many."""
+    p, shape = _dev(pt, name, _int32, here), pt.shape
+    rows, stride = shape if len(shape) == 2 else (pt.numel() // max(shape[-1], 1), shape[-1])
     if rows < least:
         raise ValueError(f"{name} must have a row for each sequence ({least} at least)")
-    return rows
+    return p, stride, rows
 
 
 def dsv4sa_cache_append(pool: PoolDesc, page_table, row_seq, row_pos, rows, rope_cs=None, row_entry=None, ring: int = 0,
@@ -742,10 +743,9 @@ def dsv4sa_cache_append(pool: PoolDesc, page_table, row_seq, row_pos, rows, rope
         if eps is None or norm_w.shape != (HEAD_DIM,):
             raise ValueError("norm_w must be [512], with eps")
         wp = _dev(norm_w, "norm_w", _f32, here)
-    pt_rows = _table_rows(page_table, "page_table", 1 if n else 0)
-    a = AppendArgs(ctypes.pointer(_pool(pool, "pool", here)), _dev(page_table, "page_table", _int32, here), page_table.shape[-1],
-                   ring, _dev(row_seq, "row_seq", _int32, here), lists[0], lists[1], lists[2], rp, rs, shape[0], n, cs,
-                   0 if rope_cs is None else rope_cs.shape[0], 0 if eps is None else 1, wp, eps or 0.0, pt_rows)
+    pt, pt_stride, pt_rows = _page_table(page_table, "page_table", 1 if n else 0, here)
+    a = AppendArgs(ctypes.pointer(_pool(pool, "pool", here)), pt, pt_stride, ring, _dev(row_seq, "row_seq", _int32, here), lists[0],
+                   lists[1], lists[2], rp, rs, shape[0], n, cs, 0 if rope_cs is None else rope_cs.shape[0], 0 if eps is None else 1, wp, eps or 0.0, pt_rows)
     st = lib().dsv4sa_cache_append(ctypes.byref(a), _stream(stream, here))
     if st:
         raise DSV4SAError("dsv4sa_cache_append", st)
@@ -966,16 +966,13 @@ def dsv4sa_tree_attn(q, sink, node_start, ctx, pos, comp, comp_pt, n_vis, n_max:
         rows = _dev(seq_row, "seq_row", _int32, here)
     cd = cpt = wd = wpt = rcs = rpos = None
     cpt_stride = wpt_stride = cpt_rows = wpt_rows = rope_rows = 0
+    least = B if seq_row is None else 1
     if comp is not None:
         cd = ctypes.pointer(_pool(comp, "comp", here))
-        cpt = _dev(comp_pt, "comp_pt", _int32, here)
-        cpt_stride = comp_pt.shape[-1]
-        cpt_rows = _table_rows(comp_pt, "comp_pt", 1 if seq_row is not None else B) if n_max > 0 else 0
+        cpt, cpt_stride, cpt_rows = _page_table(comp_pt, "comp_pt", least if n_max > 0 else 0, here)
     if win is not None:
         wd = ctypes.pointer(_pool(win, "win", here))
-        wpt = _dev(win_pt, "win_pt", _int32, here)
-        wpt_stride = win_pt.shape[-1]
-        wpt_rows = _table_rows(win_pt, "win_pt", 1 if seq_row is not None else B) if window > 0 or draft_entry >= 0 else 0
+        wpt, wpt_stride, wpt_rows = _page_table(win_pt, "win_pt", least if window > 0 or draft_entry >= 0 else 0, here)
     if rope_cs is not None:
         rcs = _table_of(rope_cs, 32, here)
         rpos = _dev(rope_pos, "rope_pos", _int32, here)

@@ -47,9 +47,11 @@ def test_append_counts_table_rows(L, gpu0):
     rows, seq = on((5, 512), bf16), on((5,), i32)
     L.dsv4sa_cache_append(L.PoolDesc(), on((2, 4), i32), seq, seq, rows)
     L.dsv4sa_cache_append(L.PoolDesc(), on((0, 4), i32), seq[:0], seq[:0], rows[:0])
-    with pytest.raises(ValueError, match="row"):
-        L.dsv4sa_cache_append(L.PoolDesc(), on((0, 4), i32), seq, seq, rows)
-    assert L.lib.reached == ["dsv4sa_cache_append"] * 2
+    L.dsv4sa_cache_append(L.PoolDesc(), on((4,), i32), seq, seq, rows)           # a table of one row
+    for table in ((0, 4), (2, 0, 4)):
+        with pytest.raises(ValueError, match="row"):
+            L.dsv4sa_cache_append(L.PoolDesc(), on(table, i32), seq, seq, rows)
+    assert L.lib.reached == ["dsv4sa_cache_append"] * 3
 
 
 def test_append_call_refuses_negative_table_rows(L):
