@@ -701,6 +701,13 @@ DSV4SA_API int dsv4sa_cache_append(const dsv4sa_append_args* args, cudaStream_t 
  *     draft_entry -1: no drafted rows.
  * A position below 0 has no window.  Nodes may lie any distance apart: the rows between their
  * windows are not read, and rows that no node sees may be without a page.
+ * Drafted rows are seen by anc alone: with a window below a tree's depth the caller leaves the bits of
+ * ancestors that it has passed out of anc (a null anc keeps the whole chain).
+ * An entry has one content for all nodes of a sequence.  Where a drafted token completes an entry
+ * (pos + 1 a multiple of the compression ratio), nodes at and below it see, in plain decoding, an
+ * entry made with drafted tokens.  If they are all on one branch, write that entry before the call
+ * and count it in their n_vis; branches that would complete different ones cannot be in one call
+ * as plain decoding has them: end the tree before such a token.
  * A node without any row gets zeros (lse: the sink).  q, out and lse rows outside every
  * sequence are neither read nor written.  A sequence whose bounds do not lie within
  * [0, T] or hold more than max_nodes nodes is left out, and a page id, an entry or a row of
