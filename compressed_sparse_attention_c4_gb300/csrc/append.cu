@@ -6,8 +6,8 @@
 // rounding instead of the three of separate calls.  Without the norm the codes and scales are
 // those of the cache writer, bit for bit.
 //
-// A warp per row, lane c holding the 16-byte units c and 32 + c (8 values each): loads and
-// stores are contiguous, a 64-value block is eight neighbouring lanes (a 32-value FP4 block
+// A warp takes a row at a time, lane c holding the 16-byte units c and 32 + c (8 values each): loads
+// and stores are contiguous, a 64-value block is eight neighbouring lanes (a 32-value FP4 block
 // four), and the rotated units 56-63 are the second ones of lanes 24-31, whole pairs in a lane.
 // Norm weights and the row's table entries come from L1 and L2.
 #include "common.cuh"
@@ -84,10 +84,12 @@ __device__ __forceinline__ uint2 e4m3x8(const float2 (&y)[4], float scale, bool 
 // A warp takes `per` consecutive rows.  Lane l looks up row l's slot -- one chain of dependent
 // loads for all of them -- and the rows themselves come through shared memory, kStages of them
 // on the way at a time: each lane copies, and later reads, its own 16-byte units, so nothing
-// has to be waited for but the copy.  65529 FP8 rows with the norm 33.4 us (18.3 at the copy
-// bandwidth, 15.8 without the table rows that sequences share; 24 warps a multiprocessor; not
-// profiled: instructions and shuffles of the norm and the quotients by estimate), 57.6 with a row a warp and loads one after the other; 32749 FP4 rows 10.4 (8.0),
-// 17.6 so; 32 rows 2.6.
+// has to be waited for but the copy.  65529 FP8 rows with the norm 33.3 us (18.3 at the copy
+// bandwidth, 15.8 without the table rows that sequences share), 57.6 with a row a warp and loads
+// one after the other; 32749 FP4 rows without it 10.3 (8.0), 17.6 so; 32 rows 2.6.  By the counters
+// (caches cold: 36.8 us) the FP8 kernel issues in 56 % of its slots and has 18 warps a
+// multiprocessor on average: 80 registers let three CTAs in, and the batches below are sized
+// for four, so the last quarter of them runs with most of the GPU idle.  FP4: 59 % and 25.
 constexpr int kStages = 4;
 constexpr int kMaxRows = 16;             // of a warp's batch
 constexpr int kStageBytes = 1024 + 256;  // the row, and its rotation
@@ -239,7 +241,8 @@ cudaError_t launch_append(AppendParams& p, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cudaErrorUnknown;
-  // batches that keep every multiprocessor's warps busy with one each, as far as there are rows
+  // batches for four CTAs a multiprocessor (what the 64 registers without the norm allow; with it
+  // three fit at a time), as far as there are rows
   constexpr int64_t kWarps = kThreads / 32;
   const int64_t n = p.n, want = (n + sms * 4 * kWarps - 1) / (sms * 4 * kWarps);
   p.per = static_cast<int32_t>(want < 1 ? 1 : (want > kMaxRows ? kMaxRows : want));

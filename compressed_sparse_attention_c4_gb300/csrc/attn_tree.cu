@@ -11,8 +11,9 @@
 // entries, §2.8; "DeepSeek-V4 in SGLang" MQALayer: one kv tensor is both K and V.)
 //
 // Work.  The queries of a sequence are one matrix of nodes x heads rows; an item is 64 of them,
-// which share the rows that are read and widened for them.  An item's rows -- the entries that
-// any of its nodes sees, then window, then drafted rows -- are cut into chunks of 128.  All
+// for which its rows are read and widened once: eight nodes of 8 heads share them, a node of 64
+// heads reads the sequence's rows for itself.  An item's rows -- the entries that any of its nodes
+// sees, then the union of their windows, then drafted rows -- are cut into chunks of 128.  All
 // chunks of all items are dealt out to the CTAs in equal contiguous runs, by a scan that every
 // CTA makes over the batch's lengths, so long and short sequences fill the GPU alike.  A run's
 // first and last item may be cut: their sums go to the workspace and a second kernel joins them.
@@ -28,17 +29,21 @@
 //   softmax warps (8): thread = row, 32 of the item's columns.  P is BF16 against a max that is
 //     only moved (and O rescaled) when a score passes it by 2^8.
 // What bounds it: shared memory and the hand-overs from warp to warp.  A chunk takes about 6800
-// cycles (trees of 16 nodes, 64 heads, 8336 rows, traced): 2700 to widen its two halves, of which
-// the first half's 1270 nothing else can hide, 1200 for the second half of S, 1320 for the
-// softmax, 1090 until PV has read the first half; the matrix instructions read 384 KB of shared
-// memory (3070 cycles at 128 bytes a clock), the tile's stores are 128 KB more, and loads that pass
-// L1 meanwhile wait.  8 sequences x 16 nodes x 64 heads at 8192 entries: 227 us, 615 TFLOP/s, 0.32
-// of the matrix peak; 32 x 4 nodes at 512 entries 31.1 us; one token of 16 heads at 512 entries
-// 18.9 (scan of the lengths, the item's description, Q, a chunk, its sums, the joining kernel).
-// Sixteen warps that load, widen and do the softmax in turn (so that widening overlaps PV) took
-// 255 to 268 us for the first of these, 236 then with warps of one kind each: their loads wait for the shared memory
-// that the matrix instructions use.  Loads that leave L1 out took 311.  Dealing out an item's last step as a chunk, and the
-// first item's Q fetched by the softmax warps: mixed batch of 64 sequences 91 -> 79 us.
+// cycles (trees of 16 nodes, 64 heads, 8336 rows; clock stamps of an instrumented copy): 2700 to
+// widen its two halves, of which the first half's 1270 nothing else can hide, 1200 for the second
+// half of S, 1320 for the softmax, 1090 until PV has read the first half; the matrix instructions
+// read 384 KB of shared memory (3070 cycles at 128 bytes a clock) and the tile's stores are 128 KB
+// more.  By the counters nothing is full: tensor pipe 28 % (20 for FP4 rows and 8 heads), L1 and
+// shared memory 50, issue slots 43, DRAM 3; a warp waits 9.1 of 14 cycles between instructions
+// for TMEM and global loads, 1.5 at barriers.  72 registers a thread; 212 bytes of spill stores a
+// thread (180 for FP4 rows), most of them the scheduler's, whose warpgroup has 40 registers.
+// 8 sequences x 16 nodes x 64 heads at 8192 entries: 225 us, 621 TFLOP/s, 0.33 of the measured
+// matrix rate; 32 x 4 nodes at 512 entries 30.8 us; one token of 16 heads at 512 entries 17.8 to
+// 18.9 (scan of the lengths, the item's description, Q, a chunk, its sums, the joining kernel);
+// 64 FP4 sequences of 8 heads 78.7.
+// Tried and not kept: sixteen warps that load, widen and do the softmax in turn (so that widening
+// overlaps PV), 255 to 268 us for the first of these, 236 then with warps of one kind each; loads
+// that leave L1 out, 311.
 // Only chunks that hold a row that some node does not see look at masks.  A row that holds an
 // infinity or a NaN shows in its scores, which then are no numbers for any column: it is taken
 // out of the tile (0 times it would be a NaN for nodes that do not see it), and the nodes that

@@ -23,7 +23,7 @@ constexpr int kThreads = 256;
 // turn with 64 bits below the point, is rounded to fp32 and goes through the Taylor series of
 // sine and cosine (to x^9 and x^10: 2^-28 and 2^-32 at pi / 4).  A thread keeps one pair and
 // adds a constant phase from row to row.  Bound by HBM (written once) and instructions both: 1M rows
-// of 32 pairs 46.4 us, 39.7 at the measured copy bandwidth; CUDA's sincospif took 59.7.
+// of 32 pairs 46.4 us, 39.5 at the measured copy bandwidth; CUDA's sincospif took 59.7.
 struct TableParams {
   float2* cs;
   int64_t first;
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
 // c, c + L, ... .  Pairs side by side lie in one unit; with the pairs in two halves a lane loads
 // its unit's partner too (the neighbours of its group have just asked for the same lines).
 // In place and without a norm only the rotated units are touched.  Bound by HBM: 4096 x 64 heads of
-// 512, normed, 86.8 us (79.5 at the copy bandwidth), 8191 x 64 of 128 in halves 48.3 (40.0), 32 x 64
+// 512, normed, 86.9 us (79.2 at the copy bandwidth), 8191 x 64 of 128 in halves 48.2 (39.8), 32 x 64
 // of 512 2.4 (latency: position, table row).
 struct RopeParams {
   const uint4* x;
