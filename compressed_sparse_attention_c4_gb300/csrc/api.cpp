@@ -95,7 +95,7 @@ bool smem_attr_once(int device, int slot, const void* kernel, int bytes) {
 
 extern "C" {
 
-DSV4SA_API int dsv4sa_version(void) { return 100; }
+DSV4SA_API int dsv4sa_version(void) { return 101; }
 
 DSV4SA_API const char* dsv4sa_status_string(int s) {
   switch (s) {
@@ -652,8 +652,7 @@ DSV4SA_API int dsv4sa_check_errors(cudaStream_t stream, uint32_t* bits_out) {
       dsv4sa::error_word_pages(), dsv4sa::error_word_rope(), dsv4sa::error_word_append()};
   uint32_t bits = 0;
   const int rc = dsv4sa::collect_errors(words, &bits, stream);
-  if (rc != DSV4SA_OK) return rc;
-  if (cudaGetLastError() != cudaSuccess) return DSV4SA_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess || rc != DSV4SA_OK) return DSV4SA_ERR_CUDA;
   if (bits_out) *bits_out = bits;
   if (bits & 2u) return DSV4SA_ERR_DEVICE_TIMEOUT;
   if (bits & 1u) return DSV4SA_ERR_INDEX_OOB;

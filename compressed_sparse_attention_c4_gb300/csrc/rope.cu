@@ -19,9 +19,10 @@ constexpr int kThreads = 256;
 // An angle is a phase: w_i / 2 pi as a 64-bit fraction of a turn, times the position, modulo
 // 2^64.  Whole turns drop out exactly; the fraction is the nearest one, half a step of 2^-64 turn off,
 // so position n is off by at most n 2^-62.3 (2^-31 at the last 31-bit position, 2^-24, fp32's own
-// rounding, at 2^38).  A frequency in fp64 would be off by n 2^-53.  The nearest quarter turn is taken off in whole numbers, too; what is left, at most an eighth of a
-// turn with 64 bits below the point, is rounded to fp32 and goes through the Taylor series of
-// sine and cosine (to x^9 and x^10: 2^-28 and 2^-32 at pi / 4).  A thread keeps one pair and
+// rounding, at 2^38).  A frequency in fp64 would be off by n 2^-53.  The nearest quarter turn is
+// taken off in whole numbers, too; what is left, at most an eighth of a turn with 64 bits below the
+// point, is rounded to fp32 and goes through the Taylor series of sine and cosine (to x^9 and
+// x^10: 2^-28 and 2^-32 at pi / 4).  A thread keeps one pair and
 // adds a constant phase from row to row.  Bound by HBM (written once) and instructions both: 1M rows
 // of 32 pairs 46.4 us, 39.5 at the measured copy bandwidth; CUDA's sincospif took 59.7.
 struct TableParams {

@@ -745,7 +745,8 @@ def dsv4sa_cache_append(pool: PoolDesc, page_table, row_seq, row_pos, rows, rope
         wp = _dev(norm_w, "norm_w", _f32, here)
     pt, pt_stride, pt_rows = _page_table(page_table, "page_table", 1 if n else 0, here)
     a = AppendArgs(ctypes.pointer(_pool(pool, "pool", here)), pt, pt_stride, ring, _dev(row_seq, "row_seq", _int32, here), lists[0],
-                   lists[1], lists[2], rp, rs, shape[0], n, cs, 0 if rope_cs is None else rope_cs.shape[0], 0 if eps is None else 1, wp, eps or 0.0, pt_rows)
+                   lists[1], lists[2], rp, rs, shape[0], n, cs, 0 if rope_cs is None else rope_cs.shape[0], 0 if eps is None else 1, wp,
+                   eps or 0.0, pt_rows)
     st = lib().dsv4sa_cache_append(ctypes.byref(a), _stream(stream, here))
     if st:
         raise DSV4SAError("dsv4sa_cache_append", st)
@@ -966,7 +967,7 @@ def dsv4sa_tree_attn(q, sink, node_start, ctx, pos, comp, comp_pt, n_vis, n_max:
         rows = _dev(seq_row, "seq_row", _int32, here)
     cd = cpt = wd = wpt = rcs = rpos = None
     cpt_stride = wpt_stride = cpt_rows = wpt_rows = rope_rows = 0
-    least = B if seq_row is None else 1
+    least = B if seq_row is None else min(B, 1)
     if comp is not None:
         cd = ctypes.pointer(_pool(comp, "comp", here))
         cpt, cpt_stride, cpt_rows = _page_table(comp_pt, "comp_pt", least if n_max > 0 else 0, here)

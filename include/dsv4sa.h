@@ -921,7 +921,8 @@ DSV4SA_API int dsv4sa_step_destroy(dsv4sa_step* step);
 /* Static text for a status code. */
 DSV4SA_API const char* dsv4sa_status_string(int status);
 
-/* Library version as 10000*major + 100*minor + patch. */
+/* Library version as 10000*major + 100*minor + patch.  From 101 on dsv4sa_tree_args ends with the
+ * rows of its page tables (8 bytes more than before). */
 DSV4SA_API int dsv4sa_version(void);
 
 #ifdef __cplusplus
